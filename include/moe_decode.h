@@ -89,6 +89,11 @@ extern "C" {
 /* written by the device into the workspace status word */
 #define MOE_EDEVICE_BAD_INDEX (-100) /* moe_ffn got an index outside [0, E);
                                         that (token, slot) was skipped */
+#define MOE_EDEVICE_OVERFLOW (-102)  /* moe_paged_plan: more new tokens than
+                                        slot_map holds, a request longer
+                                        than its row of the block table, or
+                                        the free list ran out; the tokens
+                                        concerned got slot -1 */
 #define MOE_ETIMEOUT (-101)          /* a bounded device wait ran out; the
                                         call's outputs are incomplete and the
                                         workspace must be re-initialised:
@@ -285,6 +290,116 @@ int moe_fp8_dequant(const uint8_t* codes, const float* scales, int64_t rows,
  * weights are loaded. */
 int moe_transpose_down(const void* w2, int64_t n, int H, int I, void* w2t,
                        void* stream);
+
+/* ------------------------------------------------------------- paged step
+ * The operators around the layer in one decode, speculative-verify or
+ * chunked-prompt step of B requests: places in a paged KV cache for the
+ * step's new tokens, the write of their keys and values, their attention
+ * over the cache, and the choice of tokens from the output layer's logits.
+ * "Chasing the Batch-1 Floor", "The shape of a batch-1 step"; "DSpark in
+ * SGLang", "Verify modes" (verify blocks of variable length).
+ *
+ * A step's tokens lie packed, request after request: request b's new tokens
+ * are rows q_start[b] .. q_start[b + 1] - 1 of the token arrays. Rows from
+ * q_start[B] on are padding (a step captured in a graph at a fixed T). The
+ * lengths are device data: nothing here reads them on the host.
+ *
+ * Device conditions go to the status word of ws (at least
+ * MOE_PAGED_WORKSPACE_BYTES, zeroed once with moe_workspace_init). */
+#define MOE_PAGED_WORKSPACE_BYTES 1024u
+#define MOE_PAGED_MAX_REQUESTS 4096
+
+/* A paged KV cache: n_blocks blocks (pages) of block_size tokens. Element
+ * (block i, token j, head h, d) of K lies at k + i * k_block_stride + j *
+ * k_token_stride + h * k_head_stride + d (elements), and of V alike, so both
+ * [block][token][head][d] and [block][head][token][d] layouts, and K and V
+ * interleaved in one buffer, are described by their strides. */
+typedef struct moe_kv_cache {
+    void* k;
+    void* v;
+    int32_t dtype;      /* 0 bf16, 1 fp16 (queries and outputs alike) */
+    int32_t n_blocks;   /* n_blocks * block_size <= 2^31 - 1 */
+    int32_t block_size; /* a multiple of 8, at most 1024 */
+    int32_t kv_heads;   /* 1..256 */
+    int32_t head_dim;   /* 64 or 128 */
+    int64_t k_block_stride, k_token_stride, k_head_stride; /* multiples of 8, */
+    int64_t v_block_stride, v_token_stride, v_head_stride; /* at least head_dim */
+} moe_kv_cache;
+
+/* Block tables and slot maps of a step from its requests' lengths.
+ * ctx_lens, new_lens int32 [B]: tokens already in the cache, new tokens.
+ * Request b holds ceil(ctx_lens[b] / block_size) blocks, listed in
+ * block_tables [B, max_blocks]; it needs ceil((ctx + new) / block_size). The
+ * missing ones are taken from free_list [n_free] in request order, starting
+ * at *free_head (0 when free_head is NULL), and written into block_tables.
+ * Outputs: q_start [B + 1], seq_lens [B] = ctx + new, taken [1] (blocks
+ * taken; the next step's head is *free_head + *taken) and for each of T
+ * token rows slot_map [T] (block * block_size + offset, -1 for padding) and
+ * positions [T] (position in its request, -1 for padding; may be NULL). The
+ * call writes the same results when repeated on the same inputs.
+ * B <= MOE_PAGED_MAX_REQUESTS. Outputs must not overlap inputs.
+ * A negative length, an old block id below 0 or a slot beyond 2^31 - 1
+ * reports MOE_EDEVICE_BAD_INDEX (the length counts as 0, the token gets slot
+ * -1); running out of room reports MOE_EDEVICE_OVERFLOW. */
+int moe_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int B, const int32_t* free_list, int n_free,
+                   const int32_t* free_head, int32_t* block_tables, int max_blocks, int block_size,
+                   int32_t* q_start, int32_t* seq_lens, int32_t* slot_map, int32_t* positions, int T,
+                   int32_t* taken, void* ws, size_t ws_bytes, void* stream);
+
+/* Writes T tokens' keys and values into the cache: token t's head h, at
+ * k_new + t * k_token_stride + h * k_head_stride (elements; multiples of 8,
+ * so that slices of a fused projection's output do), goes to slot
+ * slot_map[t]. Slot -1 is skipped; a slot outside the cache is skipped and
+ * reported (MOE_EDEVICE_BAD_INDEX). Slots of one call must differ. */
+int moe_paged_append(const void* k_new, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
+                     int64_t v_token_stride, int64_t v_head_stride, int T, const int32_t* slot_map,
+                     const moe_kv_cache* cache, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of the step's new tokens over the paged cache, which already
+ * holds their keys and values. q [T, q_heads, head_dim] by its strides
+ * (elements, multiples of 8), q_heads a multiple of kv_heads (at most 32
+ * times); query head h reads kv head h / (q_heads / kv_heads). Row t of
+ * request b sits at position p = seq_lens[b] - (q_start[b + 1] -
+ * q_start[b]) + t - q_start[b] and sees the keys j <= p, with window > 0
+ * only those with j > p - window:
+ *   out[t, h] = sum_j softmax_j(scale q . k_j) v_j     [T, q_heads, head_dim], contiguous
+ *   lse[t, h] = ln sum_j exp(scale q . k_j)            fp32 [T, q_heads], may be NULL
+ * A row that sees no key (p < 0) and padding rows get out = 0, lse = -inf.
+ * Products are summed in fp32, the softmax weights rounded once to the
+ * cache's type for the second product. Pages that hold no visible key are
+ * not read (their table entries may be anything), and what lies in a page
+ * beyond the visible keys may be anything, NaN included. A visible key whose
+ * page is not in [0, n_blocks), or beyond max_blocks, is reported
+ * (MOE_EDEVICE_BAD_INDEX) and that request's outputs are unspecified.
+ * scale <= 0 takes 1 / sqrt(head_dim). block_tables int32 [B, max_blocks].
+ * ws: moe_paged_attention_workspace_bytes(q_heads, cache). The result is
+ * deterministic. */
+size_t moe_paged_attention_workspace_bytes(int q_heads, const moe_kv_cache* cache);
+int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int T, int q_heads,
+                        const moe_kv_cache* cache, const int32_t* block_tables, int max_blocks,
+                        const int32_t* q_start, const int32_t* seq_lens, int B, float scale, int window, void* out,
+                        float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* One token from each of M rows of logits [M, V] (row_stride elements from
+ * row to row; dtype 0: fp32, as moe_lm_head writes, 1: bf16), each with its
+ * own settings (device arrays [M], NULL: off for every row):
+ *   w_i = exp((l_i - max l) / temperature); order: l descending, index ascending
+ *   kept: the first top_k (top_k <= 0: all), of those the shortest run whose
+ *         mass reaches top_p of theirs (top_p >= 1: all; at least one), of
+ *         those the ones with w_i >= min_p (<= 0: all; above 1 counts as 1)
+ *   token = the lowest index at which the kept tokens' cumulated mass, in
+ *           index order, exceeds u * (their total mass)
+ * temperature <= 0 (or NaN) takes the largest logit's lowest index;
+ * temperature NULL is 1. u fp32 [M] in [0, 1) (clamped to it). A NaN logit
+ * counts as -inf; +inf shares all the mass. Masses are summed in 64-bit
+ * fixed point, so the result does not depend on any order. token int32 [M]
+ * (-1 for a row without any logit above -inf), prob fp32 [M] or NULL: the
+ * token's share of the kept mass (0 with token -1).
+ * V <= MOE_SAMPLE_MAX_VOCAB, any M >= 1; logits aligned to their type. */
+#define MOE_SAMPLE_MAX_VOCAB 720896
+int moe_sample(const void* logits, int dtype, int M, int V, int64_t row_stride, const float* u,
+               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+               int32_t* token, float* prob, void* stream);
 
 /* Synchronises `stream`, then copies the device status word of `ws` to
  * *dev_status (MOE_OK or a device code above). Not for the hot path. */

@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_decode.so")
 
 OK = 0
 EINVAL, ESHAPE, EM, EWORKSPACE, EALIGN, ECUDA, ENODEVICE, ESCRATCH = -1, -2, -3, -4, -5, -6, -7, -8
-EDEVICE_BAD_INDEX, ETIMEOUT = -100, -101
+EDEVICE_BAD_INDEX, ETIMEOUT, EDEVICE_OVERFLOW = -100, -101, -102
 F_NO_PDL = 1
 F_RESET_SCRATCH = 2
 F_DEBUG_FORCE_TIMEOUT = 256
@@ -30,6 +30,10 @@ OPT_TRACE_BUFFER = 3
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 LM_HEAD_WORKSPACE_BYTES = 1024
 STATIC_SCRATCH_BYTES = 524288
+PAGED_WORKSPACE_BYTES = 1024
+PAGED_MAX_REQUESTS = 4096
+SAMPLE_MAX_VOCAB = 720896
+DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
 class MoeError(RuntimeError):
@@ -48,6 +52,13 @@ class Shape(ctypes.Structure):
 class _Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "w3", "w2", "s1", "s3", "s2", "ws1", "ws3", "ws2", "w2t",
                                                  "ws2t")]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("dtype", "n_blocks", "block_size", "kv_heads", "head_dim")] + [
+        (n, ctypes.c_int64) for n in ("k_block_stride", "k_token_stride", "k_head_stride", "v_block_stride",
+                                      "v_token_stride", "v_head_stride")]
 
 
 def _load():
@@ -75,10 +86,18 @@ def _load():
     lib.moe_fp8_quantize.argtypes = [P, I64, I32, I32, P, P, P]
     lib.moe_fp8_dequant.argtypes = [P, P, I64, I32, I32, P, P]
     lib.moe_transpose_down.argtypes = [P, I64, I32, I32, P, P]
+    F32, cp = ctypes.c_float, ctypes.POINTER(_KvCache)
+    lib.moe_paged_plan.argtypes = [P, P, I32, P, I32, P, P, I32, I32, P, P, P, P, I32, P, P, SZ, P]
+    lib.moe_paged_append.argtypes = [P, I64, I64, P, I64, I64, I32, P, cp, P, SZ, P]
+    lib.moe_paged_attention_workspace_bytes.argtypes = [I32, cp]
+    lib.moe_paged_attention_workspace_bytes.restype = SZ
+    lib.moe_paged_attention.argtypes = [P, I64, I64, I32, I32, cp, P, I32, P, P, I32, F32, I32, P, P, P, SZ, P]
+    lib.moe_sample.argtypes = [P, I32, I32, I32, I64, P, P, P, P, P, P, P, P]
     lib.moe_last_launch_count.argtypes = []
     for f in ("moe_workspace_init", "moe_route", "moe_ffn", "moe_decode_layer", "moe_decode_layer_static_scratch",
               "moe_read_status", "moe_static_scratch_status", "moe_mxfp4_dequant", "moe_set_option", "moe_last_launch_count",
-              "moe_lm_head", "moe_fp8_quantize", "moe_fp8_dequant", "moe_transpose_down"):
+              "moe_lm_head", "moe_fp8_quantize", "moe_fp8_dequant", "moe_transpose_down",
+              "moe_paged_plan", "moe_paged_append", "moe_paged_attention", "moe_sample"):
         getattr(lib, f).restype = I32
     return lib
 
@@ -239,3 +258,150 @@ def fp8_dequant(codes, scales, block: int, out, stream=None):
     rows, K = codes.shape
     _check(lib.moe_fp8_dequant(_ptr(codes), _ptr(scales), rows, K, block, _ptr(out), _stream(stream)),
            "moe_fp8_dequant")
+
+
+# ---------------------------------------------------------------- paged step
+def _want(ok: bool, what: str, code: int = EINVAL):
+    if not ok:
+        raise MoeError(code, what)
+
+
+def _raw(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _vector(t: Optional[torch.Tensor], n: Optional[int], dtype: torch.dtype, what: str):
+    """A contiguous device vector of n elements (None: any number), or None."""
+    if t is not None:
+        _want(t.dtype == dtype and t.is_contiguous() and t.is_cuda and (n is None or t.numel() == n), what)
+
+
+class KvCache:
+    """A paged KV cache: K and V [n_blocks, block_size, kv_heads, head_dim]
+    bf16 or fp16 views (any strides that are multiples of 8 elements, the last
+    dimension contiguous: `.transpose(1, 2)` of a [block, head, token, d]
+    buffer is one). Keeps the tensors alive; build it once, next to them."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _want(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in DTYPES
+              and k.stride(3) == 1 and v.stride(3) == 1, "KvCache: K and V [blocks, tokens, heads, d], one dtype", ESHAPE)
+        self.k, self.v = k, v
+        n_blocks, self.block_size, self.kv_heads, self.head_dim = k.shape
+        # a dimension of one element has no stride of its own
+        sk, sv = ([t.stride(i) if t.shape[i] > 1 else max(t.stride(i), (self.head_dim + 7) // 8 * 8) for i in range(3)]
+                  for t in (k, v))
+        self.dtype = k.dtype
+        self._c = _KvCache(k.data_ptr(), v.data_ptr(), DTYPES[k.dtype], n_blocks, self.block_size, self.kv_heads,
+                           self.head_dim, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2])
+        self._ref = ctypes.pointer(self._c)
+
+
+def paged_workspace(q_heads: int = 0, cache: Optional[KvCache] = None, device="cuda", stream=None) -> torch.Tensor:
+    """A zeroed workspace for the paged-step calls: for paged_attention with
+    q_heads over `cache`, or, without them, for paged_plan and paged_append."""
+    n = PAGED_WORKSPACE_BYTES if cache is None else int(
+        lib.moe_paged_attention_workspace_bytes(q_heads, cache._ref))
+    _want(n > 0, "moe_paged_attention_workspace_bytes", ESHAPE)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    workspace_init(ws, stream)
+    return ws
+
+
+def paged_plan(ctx_lens, new_lens, free_list, block_tables, block_size: int, q_start, seq_lens, slot_map, taken, ws,
+               positions=None, free_head=None, stream=None):
+    """Block tables and slot map of a step (moe_paged_plan). All int32 device
+    tensors: ctx_lens, new_lens [B], free_list [F], block_tables [B, W]
+    (updated in place), outputs q_start [B + 1], seq_lens [B], slot_map [T],
+    positions [T], taken [1]; free_head [1] is where the free list begins."""
+    B, T = ctx_lens.numel(), slot_map.numel()
+    i32 = torch.int32
+    _vector(ctx_lens, B, i32, "paged_plan: ctx_lens int32 [B]")
+    _vector(new_lens, B, i32, "paged_plan: new_lens int32 [B]")
+    _vector(free_list, None, i32, "paged_plan: free_list int32 [F]")
+    _vector(free_head, 1, i32, "paged_plan: free_head int32 [1]")
+    _want(block_tables.dim() == 2 and block_tables.shape[0] == B, "paged_plan: block_tables int32 [B, W]")
+    _vector(block_tables, None, i32, "paged_plan: block_tables int32 [B, W]")
+    _vector(q_start, B + 1, i32, "paged_plan: q_start int32 [B + 1]")
+    _vector(seq_lens, B, i32, "paged_plan: seq_lens int32 [B]")
+    _vector(slot_map, T, i32, "paged_plan: slot_map int32 [T]")
+    _vector(positions, T, i32, "paged_plan: positions int32 [T]")
+    _vector(taken, 1, i32, "paged_plan: taken int32 [1]")
+    rc = lib.moe_paged_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, free_list.data_ptr(), free_list.numel(),
+                            _raw(free_head), block_tables.data_ptr(), block_tables.shape[1], block_size,
+                            q_start.data_ptr(), seq_lens.data_ptr(), slot_map.data_ptr(), _raw(positions), T,
+                            taken.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if rc:
+        raise MoeError(rc, "moe_paged_plan")
+
+
+def paged_append(k_new, v_new, slot_map, cache: KvCache, ws, stream=None):
+    """Writes k_new, v_new [T, kv_heads, head_dim] (last dimension contiguous,
+    e.g. slices of a fused projection's output) to the cache's slots
+    slot_map [T] (moe_paged_append)."""
+    T = k_new.shape[0]
+    _want(k_new.shape == (T, cache.kv_heads, cache.head_dim) and v_new.shape == k_new.shape,
+          "paged_append: k_new, v_new [T, kv_heads, head_dim]", ESHAPE)
+    _want(k_new.dtype == cache.dtype and v_new.dtype == cache.dtype and k_new.stride(2) == 1 and v_new.stride(2) == 1
+          and k_new.is_cuda and v_new.is_cuda, "paged_append: k_new, v_new of the cache's dtype on the device")
+    _vector(slot_map, T, torch.int32, "paged_append: slot_map int32 [T]")
+    kt, kh, _ = k_new.stride()
+    vt, vh, _ = v_new.stride()
+    rc = lib.moe_paged_append(k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T, slot_map.data_ptr(), cache._ref,
+                              ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if rc:
+        raise MoeError(rc, "moe_paged_append")
+
+
+def paged_attention(q, cache: KvCache, block_tables, q_start, seq_lens, out, ws, lse=None, scale: float = 0.0,
+                    window: int = 0, stream=None):
+    """Attention of the step's tokens q [T, q_heads, head_dim] over the paged
+    cache (moe_paged_attention): out [T, q_heads, head_dim] contiguous, lse
+    fp32 [T, q_heads] or None; block_tables int32 [B, W], q_start int32
+    [B + 1], seq_lens int32 [B] as paged_plan gives them; window > 0: only the
+    last `window` keys; scale <= 0: 1 / sqrt(head_dim)."""
+    T, heads, d = q.shape
+    B = seq_lens.numel()
+    _want(d == cache.head_dim and out.shape == q.shape, "paged_attention: q, out [T, q_heads, head_dim]", ESHAPE)
+    _want(q.dtype == cache.dtype and out.dtype == cache.dtype and q.is_cuda and out.is_cuda
+          and q.stride(2) == 1 and out.is_contiguous(), "paged_attention: q, out of the cache's dtype on the device")
+    _want(block_tables.dim() == 2 and block_tables.shape[0] == B, "paged_attention: block_tables int32 [B, W]")
+    _vector(block_tables, None, torch.int32, "paged_attention: block_tables int32 [B, W]")
+    _vector(q_start, B + 1, torch.int32, "paged_attention: q_start int32 [B + 1]")
+    _vector(seq_lens, B, torch.int32, "paged_attention: seq_lens int32 [B]")
+    _vector(lse, T * heads, torch.float32, "paged_attention: lse fp32 [T, q_heads]")
+    qt, qh, _ = q.stride()
+    rc = lib.moe_paged_attention(q.data_ptr(), qt, qh, T, heads, cache._ref, block_tables.data_ptr(),
+                                 block_tables.shape[1], q_start.data_ptr(), seq_lens.data_ptr(), B, scale, window,
+                                 out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if rc:
+        raise MoeError(rc, "moe_paged_attention")
+
+
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def sample(logits, u, tokens, probs=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """One token from each row of logits [M, V] (fp32 or bf16) with the random
+    numbers u fp32 [M] in [0, 1) (moe_sample): tokens int32 [M], probs fp32
+    [M] or None; per-row settings temperature, top_p, min_p fp32 [M], top_k
+    int32 [M], None for off."""
+    M, V = logits.shape
+    _want(logits.dtype in _LOGITS and logits.is_cuda and (V == 1 or logits.stride(1) == 1),
+          "sample: logits fp32 or bf16 [M, V], rows contiguous, on the device")
+    f32 = torch.float32
+    _vector(u, M, f32, "sample: u fp32 [M]")
+    _vector(tokens, M, torch.int32, "sample: tokens int32 [M]")
+    _vector(probs, M, f32, "sample: probs fp32 [M]")
+    _vector(temperature, M, f32, "sample: temperature fp32 [M]")
+    _vector(top_k, M, torch.int32, "sample: top_k int32 [M]")
+    _vector(top_p, M, f32, "sample: top_p fp32 [M]")
+    _vector(min_p, M, f32, "sample: min_p fp32 [M]")
+    rc = lib.moe_sample(logits.data_ptr(), _LOGITS[logits.dtype], M, V, logits.stride(0) if M > 1 else V, u.data_ptr(),
+                        _raw(temperature), _raw(top_k), _raw(top_p), _raw(min_p), tokens.data_ptr(), _raw(probs),
+                        _raw_stream(stream))
+    if rc:
+        raise MoeError(rc, "moe_sample")

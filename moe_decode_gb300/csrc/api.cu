@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "moe_decode.h"
+#include "host.h"
 #include "launch.h"
 #include "layer_params.h"
 
@@ -15,26 +16,13 @@
 // created with the module).
 static __device__ __align__(256) uint8_t g_static_scratch[MOE_STATIC_SCRATCH_BYTES];
 
-namespace {
+namespace moe {
 
-using moe::LayerParams;
-
-struct Options {
-    int grid_ctas = 0;
-    long long timeout_ns = 1000000000LL;
-    unsigned long long* trace = nullptr;
-};
 Options g_opt;
 thread_local int g_last_launches = 0;
 
-struct DeviceInfo {
-    int sms = 0;
-    int smem_optin = 0;
-    bool coop = false;
-};
-constexpr int kMaxDevices = 64;
-DeviceInfo g_dev[kMaxDevices];
-std::mutex g_dev_mu;
+static DeviceInfo g_dev[kMaxDevices];
+static std::mutex g_dev_mu;
 
 int device_info(DeviceInfo* out) {
     int dev = 0;
@@ -58,6 +46,20 @@ int device_info(DeviceInfo* out) {
     *out = d;
     return MOE_OK;
 }
+
+}  // namespace moe
+
+namespace {
+
+using moe::DeviceInfo;
+using moe::LayerParams;
+using moe::align_up;
+using moe::aligned16;
+using moe::device_info;
+using moe::g_dev_mu;
+using moe::g_last_launches;
+using moe::g_opt;
+using moe::kMaxDevices;
 
 void* g_scratch_ptr[kMaxDevices];
 
@@ -87,10 +89,6 @@ int static_scratch(void** out, cudaStream_t st) {
     *out = ptr;
     return MOE_OK;
 }
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Shape limits of the kernels (see moe_decode.h).
 int check_shape(const moe_shape* s, int M) {
@@ -496,7 +494,8 @@ const char* moe_status_str(int code) {
         case MOE_ECUDA: return "CUDA runtime error";
         case MOE_ENODEVICE: return "no usable CUDA device";
         case MOE_ESCRATCH: return "shape and M need more than the static scratch (MOE_STATIC_SCRATCH_BYTES = 512 KiB)";
-        case MOE_EDEVICE_BAD_INDEX: return "device: expert index out of range (entry skipped)";
+        case MOE_EDEVICE_BAD_INDEX: return "device: expert index, block, slot or length out of range (entry skipped)";
+        case MOE_EDEVICE_OVERFLOW: return "device: new tokens or blocks beyond the slot map, block table or free list";
         case MOE_ETIMEOUT: return "device: bounded wait ran out (outputs incomplete; re-initialise the workspace)";
         default: return "unknown status";
     }

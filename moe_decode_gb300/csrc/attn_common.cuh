@@ -1,0 +1,239 @@
+// What the kernels of attention over the paged cache share: the requests'
+// lengths, the division of the work over the CTAs, bounded waits, tensor-map
+// copies of pages.
+//
+// An item is up to ROWS query rows of one request and one kv head: row R of a
+// request is token R / group, query head R % group of the kv head's group, so
+// that the heads that share keys share the read. A unit is one tile of
+// kAttnTile keys of one item. All units of the call in the order request, kv
+// head, row tile, key tile are divided evenly: CTA c takes the units [cU/G,
+// (c+1)U/G), whatever the lengths. An item whose units all lie in one CTA is
+// finished there; of one that spans CTAs each leaves its part (unnormalised
+// sums, largest score, sum of weights) in the workspace, and a second kernel
+// joins the parts in the order of the keys.
+#pragma once
+#include <cuda.h>
+
+#include "layer_params.h"
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+struct Request {
+    int q0, n;     // first token row, tokens
+    int pos0;      // position of the first token (negative: rows that see nothing)
+    bool bad;
+};
+
+__device__ __forceinline__ Request attn_request(const AttnParams& p, int r) {
+    Request q;
+    const int a = p.q_start[r], b = p.q_start[r + 1];
+    int seq = p.seq[r];
+    q.bad = a < 0 || b < a || b > p.T || seq < 0;
+    q.q0 = a;
+    q.n = q.bad ? 0 : b - a;
+    q.pos0 = q.bad ? 0 : seq - q.n;
+    return q;
+}
+
+// Keys [lo, hi) that the rows [row0, row0 + rows) of a request see between
+// them, inside the block table; `over` where a row sees past it.
+__device__ __forceinline__ void attn_keys(const AttnParams& p, const Request& q, int row0, int rows, int& lo, int& hi,
+                                          bool& over) {
+    const int first = q.pos0 + row0 / p.group, last = q.pos0 + (row0 + rows - 1) / p.group;
+    const int64_t cap = (int64_t)p.max_blocks * p.block_size;
+    over = last + 1 > cap;
+    hi = (int)min((int64_t)last + 1, cap);
+    lo = p.window > 0 ? max(first - p.window + 1, 0) : 0;
+    if (hi <= lo) lo = hi = 0;
+}
+
+// Units of one row tile. A row tile without keys is one unit: its rows are
+// written all the same.
+__device__ __forceinline__ int attn_tiles(int lo, int hi) {
+    return hi > lo ? (hi - 1) / kAttnTile - lo / kAttnTile + 1 : 1;
+}
+
+// Units of request r for one kv head.
+template <int ROWS>
+__device__ __forceinline__ int64_t attn_request_units(const AttnParams& p, const Request& q) {
+    const int rows = q.n * p.group;
+    int64_t u = 0;
+    for (int r0 = 0; r0 < rows; r0 += ROWS) {
+        int lo, hi;
+        bool over;
+        attn_keys(p, q, r0, min(ROWS, rows - r0), lo, hi, over);
+        u += attn_tiles(lo, hi);
+    }
+    return u;
+}
+
+// A place in the order of units, and the CTA's range.
+struct Place {
+    int64_t total;      // units of the call
+    int64_t begin, end; // this CTA's
+    int request;        // request of unit `begin`
+    int64_t rest;       // units of that request before `begin`
+};
+
+// Finds the CTA's range and the request that it begins in, all threads
+// together. `scan` is shared memory of THREADS / 32 values, `found` one of
+// two.
+template <int ROWS, int THREADS, class Class>
+__device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, Class mine, int64_t* scan, int64_t* found) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + THREADS - 1) / THREADS;
+    const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
+    int64_t own = 0;
+    bool bad = false;
+    for (int r = r0; r < r1; ++r) {
+        const Request q = attn_request(p, r);
+        bad |= q.bad;
+        if (mine(q)) own += attn_request_units<ROWS>(p, q) * p.kv_heads;
+    }
+    if (bad) atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
+    int64_t sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) scan[warp] = sum;
+    if (tid == 0) {
+        found[0] = p.B;
+        found[1] = 0;
+    }
+    __syncthreads();
+    Place at;
+    at.total = 0;
+    int64_t before = sum - own;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += scan[w];
+        at.total += scan[w];
+    }
+    at.begin = at.total * cta / p.G;
+    at.end = at.total * (cta + 1) / p.G;
+    if (own > 0 && before <= at.begin && at.begin < before + own) {
+        for (int r = r0; r < r1; ++r) {
+            const Request q = attn_request(p, r);
+            const int64_t u = mine(q) ? attn_request_units<ROWS>(p, q) * p.kv_heads : 0;
+            if (at.begin < before + u) {
+                found[0] = r;
+                found[1] = at.begin - before;
+                break;
+            }
+            before += u;
+        }
+    }
+    __syncthreads();
+    at.request = (int)found[0];
+    at.rest = found[1];
+    return at;
+}
+
+// The items of a CTA's range, one after another; every role of the CTA walks
+// them alike.
+template <int ROWS, class Class>
+struct Walk {
+    const AttnParams& p;
+    Class mine;
+    int64_t unit, end;  // next unit of the range
+    int r, head, row0;
+    int skip;           // tiles of the item at hand before the range
+    Request q;
+    // the item at hand
+    int rows, lo, hi, tile0, tiles;
+    int t0, t1;         // its tiles [t0, t1) in this range
+    bool over;
+
+    __device__ __forceinline__ Walk(const AttnParams& params, const Place& at, Class c)
+        : p(params), mine(c), unit(at.begin), end(at.end), r(at.request), head(0), row0(0), skip(0) {
+        if (unit >= end) return;
+        q = attn_request(p, r);
+        const int64_t per_head = attn_request_units<ROWS>(p, q);
+        head = (int)(at.rest / per_head);
+        int64_t rest = at.rest - head * per_head;
+        for (;; row0 += ROWS) {
+            item();
+            if (rest < tiles) break;
+            rest -= tiles;
+        }
+        skip = (int)rest;
+    }
+    __device__ __forceinline__ void item() {
+        rows = min(ROWS, q.n * p.group - row0);
+        attn_keys(p, q, row0, rows, lo, hi, over);
+        tile0 = lo / kAttnTile;
+        tiles = attn_tiles(lo, hi);
+    }
+    // The next item into the fields; false at the end of the range.
+    __device__ __forceinline__ bool next() {
+        if (unit >= end) return false;
+        item();
+        t0 = skip;
+        t1 = (int)min((int64_t)tiles, t0 + (end - unit));
+        return true;
+    }
+    __device__ __forceinline__ void done() {
+        unit += t1 - t0;
+        skip = 0;
+        if (unit >= end) return;
+        row0 += ROWS;
+        if (row0 < q.n * p.group) return;
+        row0 = 0;
+        if (++head < p.kv_heads) return;
+        head = 0;
+        do {
+            q = attn_request(p, ++r);
+        } while (!mine(q) || q.n == 0);
+    }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+    // An item that began in an earlier CTA leaves part 0, one that goes on in
+    // the next CTA part 1.
+    __device__ __forceinline__ int part() const { return t0 > 0 ? 0 : 1; }
+};
+
+// Waits for the phase with parity `parity`, at most timeout_ns; false, with
+// the status and `flag` set, when it ran out or another wait of the CTA did.
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const AttnParams& p, volatile int* flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*flag) return false;
+        if (global_timer_ns() - t0 > p.timeout_ns) {
+            atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -101 /* MOE_ETIMEOUT */);
+            *flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// One box of a cache's tensor map (dimensions d, token of the block, head,
+// block) into shared memory: `box` keys by 64 dimensions, 128 bytes a key in
+// the 128-byte swizzle. x (0 or 64) is 16-byte aligned in either case.
+__device__ __forceinline__ void attn_copy(uint32_t dst, const CUtensorMap* map, int x, int token, int head, int block,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(token), "r"(head), "r"(block), "r"(bar)
+        : "memory");
+}
+
+// Two fp32 into one register of the type, `lo` in the low half (one rounding).
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t d;
+    if (DT == 0) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+}  // namespace moe

@@ -1,0 +1,512 @@
+// Attention of few query rows over the paged cache: decoding streams, verify
+// chains and short chunks, and the kernel that joins the parts of items that
+// span CTAs.
+#include "attn_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRows = kAttnRows;
+constexpr int kConsumers = 4;  // warps; one producer warp on top
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kWarpKeys = kAttnTile / kConsumers;
+
+template <int D>
+struct DecodeShape {
+    static constexpr int kPanel = kAttnTile * 128;           // 64 dimensions of a tile's keys
+    static constexpr int kHalf = kPanel * (D / 64);          // K (or V) of a tile
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kQ = kRows * D * 2;
+    static constexpr int kMerge = kRows * (D + 4) * 4;
+    static constexpr int kOffQ = kStages * kStage;
+    static constexpr int kOffMerge = kOffQ + kQ;
+    static constexpr int kOffStat = kOffMerge + kMerge;      // largest score and sum of each warp's rows
+    static constexpr int kOffBar = kOffStat + kConsumers * kRows * 8;
+    static constexpr int kBytes = kOffBar + 256 + 1024;      // and room to align
+};
+
+template <int DT>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (DT == 0)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+struct Small {
+    __device__ __forceinline__ bool operator()(const Request&) const { return true; }
+};
+
+// Each of the four consumer warps takes 32 keys of every tile against all of
+// the item's rows (16 or 32), with its own running largest score, sum and
+// output, so no warp reads another's keys from shared memory; the four are
+// joined once at the end of the item.
+template <int D, int DT>
+__global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_constant__ AttnParams p,
+                                                                   const __grid_constant__ CUtensorMap kmap,
+                                                                   const __grid_constant__ CUtensorMap vmap) {
+    using S = DecodeShape<D>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ int64_t scan[kThreads / 32], found[2];
+    __shared__ int abort_flag;
+    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+    uint8_t* sm = dyn + (base - smem_u32(dyn));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t full = base + S::kOffBar, empty = full + 8 * S::kStages;
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, kConsumers);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    const Place at = attn_place<kRows, kThreads>(p, blockIdx.x, Small(), scan, found);
+    if (at.begin >= at.end) return;
+    volatile int* flag = &abort_flag;
+    Walk<kRows, Small> walk(p, at, Small());
+
+    if (warp == kConsumers) {
+        // producer: lane i brings the tile's i-th box, if a row sees any of it
+        const int boxes = kAttnTile / p.box;
+        int stage = 0, issued = 0;
+        uint32_t parity = 1;
+        bool ok = true;
+        for (; ok && walk.next(); walk.done()) {
+            if (walk.over && lane == 0)
+                atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
+            const int32_t* table = p.tables + (int64_t)walk.r * p.max_blocks;
+            for (int t = walk.t0; t < walk.t1; ++t) {
+                const int key = (walk.tile0 + t) * kAttnTile + lane * p.box;
+                bool take = lane < boxes && key < walk.hi && key + p.box > walk.lo;
+                int block = 0, off = 0;
+                if (take) {
+                    const int page = key / p.block_size;
+                    off = key - page * p.block_size;
+                    block = table[page];
+                    if ((unsigned)block >= (unsigned)p.n_blocks) {
+                        atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
+                        take = false;
+                    }
+                }
+                ok = attn_wait(empty + 8 * stage, parity, p, flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int n = __popc(__ballot_sync(0xffffffffu, take));
+                if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 4));
+                __syncwarp();
+                if (take) {
+                    const uint32_t dst = base + stage * S::kStage + lane * p.box * 128;
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) {
+                        attn_copy(dst + x * S::kPanel, &kmap, 64 * x, off, walk.head, block, full + 8 * stage);
+                        attn_copy(dst + S::kHalf + x * S::kPanel, &vmap, 64 * x, off, walk.head, block,
+                                  full + 8 * stage);
+                    }
+                }
+                ++issued;
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    parity ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            // copies may be in flight: see the last ones land (again bounded)
+            for (int i = max(0, issued - S::kStages); i < issued; ++i) {
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(full + 8 * (i % S::kStages), (uint32_t)((i / S::kStages) & 1)) &&
+                       global_timer_ns() - t0 < p.timeout_ns) {
+                }
+            }
+        }
+        return;
+    }
+
+    const int quad = lane >> 2, pair = lane & 3;
+    int stage = 0;
+    uint32_t parity = 0;
+    uint8_t* qs = sm + S::kOffQ;
+    const uint32_t q_addr = base + S::kOffQ;
+    float2* stat = reinterpret_cast<float2*>(sm + S::kOffStat);  // [warp][row]
+    float* merge = reinterpret_cast<float*>(sm + S::kOffMerge);  // [row][D + 4]
+    for (; walk.next(); walk.done()) {
+        // the item's rows into shared memory, 16-byte pieces swizzled like the
+        // keys; rows past the end are zeros
+        const int mts = walk.rows > 16 ? 2 : 1;
+        for (int i = tid; i < mts * 16 * (D / 8); i += kConsumers * 32) {
+            const int row = i / (D / 8), c = i % (D / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < walk.rows) {
+                const int R = walk.row0 + row, t = R / p.group, h = walk.head * p.group + (R - t * p.group);
+                v = *reinterpret_cast<const uint4*>(p.q + (walk.q.q0 + t) * p.q_token + h * p.q_head + c * 8);
+            }
+            *reinterpret_cast<uint4*>(qs + row * (D * 2) + ((c ^ (row & 7)) << 4)) = v;
+        }
+        named_bar_sync(1, kConsumers * 32);
+        // the last key that each of this thread's rows sees, and the first
+        int last[2][2], from[2][2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int row = a * 16 + b * 8 + quad;
+                const int pos = walk.q.pos0 + (walk.row0 + row) / p.group;
+                last[a][b] = row < walk.rows ? min(pos, walk.hi - 1) : -1;
+                from[a][b] = p.window > 0 ? pos - p.window + 1 : 0;
+            }
+        const int first_pos = walk.q.pos0 + walk.row0 / p.group;
+        const int last_from =
+            p.window > 0 ? walk.q.pos0 + (walk.row0 + walk.rows - 1) / p.group - p.window + 1 : 0;
+        float o[2][D / 8][4];
+        float m[2][2], l[2][2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[a][i][j] = 0.f;
+            m[a][0] = m[a][1] = -INFINITY;
+            l[a][0] = l[a][1] = 0.f;
+        }
+        for (int t = walk.t0; t < walk.t1; ++t) {
+            if (!attn_wait(full + 8 * stage, parity, p, flag)) break;
+            const int key0 = (walk.tile0 + t) * kAttnTile + warp * kWarpKeys;
+            const uint32_t ks = base + stage * S::kStage + warp * kWarpKeys * 128, vs = ks + S::kHalf;
+            if (key0 < walk.hi && key0 + kWarpKeys > walk.lo) {
+                const bool ragged = key0 < walk.lo || key0 + kWarpKeys > walk.hi;
+                if (ragged) {
+                    // values that no row sees may be anything: a weight of 0 times
+                    // NaN is not 0, so they are cleared
+                    const int key = key0 + lane;
+                    if (key < walk.lo || key >= walk.hi) {
+                        uint8_t* v = sm + stage * S::kStage + S::kHalf + (warp * kWarpKeys + lane) * 128;
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                *reinterpret_cast<uint4*>(v + x * S::kPanel + c * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+                float s[2][4][4];
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[a][i][j] = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t qa[2][4], kb[2][4];
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+                        if (a < mts) {
+                            const int row = a * 16 + (lane & 15), c = 2 * k + (lane >> 4);
+                            ldsm_x4(q_addr + row * (D * 2) + ((c ^ (row & 7)) << 4), qa[a]);
+                        }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // 16 keys each
+                        const int row = h * 16 + ((lane >> 4) << 3) + (lane & 7), c = 2 * (k & 3) + ((lane >> 3) & 1);
+                        ldsm_x4(ks + (k >> 2) * S::kPanel + row * 128 + ((c ^ (row & 7)) << 4), kb[h]);
+                    }
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+                        if (a < mts)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                mma_16816<DT>(s[a][2 * h], qa[a], kb[h][0], kb[h][1]);
+                                mma_16816<DT>(s[a][2 * h + 1], qa[a], kb[h][2], kb[h][3]);
+                            }
+                }
+                const bool mask = key0 + kWarpKeys > min(first_pos + 1, walk.hi) || key0 < last_from;
+                uint32_t pa[2][2][4];
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    if (a >= mts) continue;
+                    if (mask) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int key = key0 + i * 8 + 2 * pair + (j & 1);
+                                if (key > last[a][j >> 1] || key < from[a][j >> 1]) s[a][i][j] = -INFINITY;
+                            }
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(s[a][i][2 * b], s[a][i][2 * b + 1]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        mx *= p.scale_log2;
+                        const bool grows = mx > m[a][b];
+                        if (__any_sync(0xffffffffu, grows)) {
+                            const float to = fmaxf(mx, m[a][b]);
+                            const float f = grows ? exp2_approx(m[a][b] - to) : 1.f;
+                            m[a][b] = to;
+                            l[a][b] *= f;
+#pragma unroll
+                            for (int i = 0; i < D / 8; ++i) {
+                                o[a][i][2 * b] *= f;
+                                o[a][i][2 * b + 1] *= f;
+                            }
+                        }
+                        const float ref = m[a][b] == -INFINITY ? 0.f : m[a][b];
+                        float sum = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = exp2_approx(fmaf(s[a][i][2 * b], p.scale_log2, -ref));
+                            const float y = exp2_approx(fmaf(s[a][i][2 * b + 1], p.scale_log2, -ref));
+                            sum += x + y;
+                            // rounded once to the values' type for the second
+                            // product: 2^-9 (bf16) of each weight, independent
+                            // from key to key; the sum keeps the fp32 weights
+                            pa[a][i >> 1][(i & 1) * 2 + b] = pack2<DT>(x, y);
+                        }
+                        l[a][b] += sum;
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        uint32_t vb[4];
+                        const int row = h * 16 + (lane & 15), c = 2 * (i & 3) + (lane >> 4);
+                        ldsm_x4_trans(vs + (i >> 2) * S::kPanel + row * 128 + ((c ^ (row & 7)) << 4), vb);
+#pragma unroll
+                        for (int a = 0; a < 2; ++a)
+                            if (a < mts) {
+                                mma_16816<DT>(o[a][2 * i], pa[a][h], vb[0], vb[1]);
+                                mma_16816<DT>(o[a][2 * i + 1], pa[a][h], vb[2], vb[3]);
+                            }
+                    }
+                if (ragged) fence_proxy_async_shared();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * stage);
+            if (++stage == S::kStages) {
+                stage = 0;
+                parity ^= 1u;
+            }
+        }
+        // join the four warps: each scales to the largest score of all, then
+        // they add up one after another
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                l[a][b] += __shfl_xor_sync(0xffffffffu, l[a][b], 1);
+                l[a][b] += __shfl_xor_sync(0xffffffffu, l[a][b], 2);
+                if (pair == 0) stat[warp * kRows + a * 16 + b * 8 + quad] = make_float2(m[a][b], l[a][b]);
+            }
+        named_bar_sync(1, kConsumers * 32);
+        float big[2][2], sum[2][2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int row = a * 16 + b * 8 + quad;
+                float mx = -INFINITY, tot = 0.f;
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w) mx = fmaxf(mx, stat[w * kRows + row].x);
+                const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w)
+                    tot += stat[w * kRows + row].y * exp2_approx(stat[w * kRows + row].x - ref);
+                big[a][b] = mx;
+                sum[a][b] = tot;
+                const float f = exp2_approx(m[a][b] - ref);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[a][i][2 * b] *= f;
+                    o[a][i][2 * b + 1] *= f;
+                }
+            }
+        for (int w = 0; w < kConsumers; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+                    if (a < mts)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int i = 0; i < D / 8; ++i) {
+                                float2* at2 = reinterpret_cast<float2*>(merge + (a * 16 + b * 8 + quad) * (D + 4) +
+                                                                        i * 8 + 2 * pair);
+                                float2 v = make_float2(o[a][i][2 * b], o[a][i][2 * b + 1]);
+                                if (w > 0) {
+                                    const float2 u = *at2;
+                                    v.x += u.x;
+                                    v.y += u.y;
+                                }
+                                *at2 = v;
+                            }
+            }
+            named_bar_sync(1, kConsumers * 32);
+        }
+        // statistics by row, then the rows: 16 bytes of output a thread
+        if (warp == 0 && pair == 0)
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) stat[a * 16 + b * 8 + quad] = make_float2(big[a][b], sum[a][b]);
+        named_bar_sync(1, kConsumers * 32);
+        const bool whole = walk.whole();
+        float* part = p.part + ((int64_t)blockIdx.x * 2 + walk.part()) * attn_part_floats(kRows, D);
+        for (int i = tid; i < walk.rows * (D / 8); i += kConsumers * 32) {
+            const int row = i / (D / 8), c = i % (D / 8);
+            const float4 x = *reinterpret_cast<const float4*>(merge + row * (D + 4) + c * 8);
+            const float4 y = *reinterpret_cast<const float4*>(merge + row * (D + 4) + c * 8 + 4);
+            if (whole) {
+                const float2 ml = stat[row];
+                const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+                const int R = walk.row0 + row, t = R / p.group, h = walk.head * p.group + (R - t * p.group);
+                const int64_t at_row = (int64_t)(walk.q.q0 + t) * p.heads + h;
+                uint4 v;
+                v.x = pack2<DT>(x.x * inv, x.y * inv);
+                v.y = pack2<DT>(x.z * inv, x.w * inv);
+                v.z = pack2<DT>(y.x * inv, y.y * inv);
+                v.w = pack2<DT>(y.z * inv, y.w * inv);
+                *reinterpret_cast<uint4*>(p.out + at_row * D + c * 8) = v;
+                if (c == 0 && p.lse) p.lse[at_row] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * 0.693147180559945f : -INFINITY;
+            } else {
+                *reinterpret_cast<float4*>(part + row * D + c * 8) = x;
+                *reinterpret_cast<float4*>(part + row * D + c * 8 + 4) = y;
+                if (c == 0) reinterpret_cast<float2*>(part + kRows * D)[row] = stat[row];
+            }
+        }
+        // the next item writes the rows and the statistics after its own barrier
+        named_bar_sync(1, kConsumers * 32);
+    }
+}
+
+// Joins the parts of the item that begins in CTA c and goes on past its end
+// (there is at most one), part after part in the order of the keys, and
+// clears padding rows.
+template <int D, int DT, int ROWS, class Class>
+__global__ __launch_bounds__(128) void attn_join_kernel(const __grid_constant__ AttnParams p) {
+    __shared__ int64_t scan[4], found[2];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x;
+    const int last = min(max(p.q_start[p.B], 0), p.T);
+    for (int64_t i = (int64_t)last * p.heads + blockIdx.x * 4 + (tid >> 5); i < (int64_t)p.T * p.heads;
+         i += (int64_t)gridDim.x * 4) {
+        reinterpret_cast<uint32_t*>(p.out + i * D)[tid & 31] = 0u;
+        if (D == 128) reinterpret_cast<uint32_t*>(p.out + i * D)[32 + (tid & 31)] = 0u;
+        if (p.lse && (tid & 31) == 0) p.lse[i] = -INFINITY;
+    }
+    const int c = blockIdx.x;
+    const Place at = attn_place<ROWS, 128>(p, c, Class(), scan, found);
+    if (at.begin >= at.end || at.end >= at.total) return;
+    Walk<ROWS, Class> walk(p, at, Class());
+    // the last item of the range
+    bool spans = false;
+    while (walk.next()) {
+        spans = walk.t0 == 0 && walk.t1 < walk.tiles;
+        if (walk.unit + (walk.t1 - walk.t0) >= walk.end) break;
+        walk.done();
+    }
+    if (!spans) return;
+    // its parts: CTA c's part 1, then part 0 of the CTAs up to its last unit
+    const int64_t end = at.end + (walk.tiles - walk.t1);
+    int parts = 1;
+    for (int k = c + 1; k < p.G; ++k) {
+        const int64_t b = at.total * k / p.G, e = at.total * (k + 1) / p.G;
+        if (b >= end) break;
+        if (e > b) parts = k - c + 1;
+    }
+    constexpr int kFloats = attn_part_floats(ROWS, D);
+    auto part_of = [&](int k) { return p.part + ((int64_t)(c + k) * 2 + (k == 0 ? 1 : 0)) * kFloats; };
+    auto empty = [&](int k) { return at.total * (c + k) / p.G >= at.total * (c + k + 1) / p.G; };
+    constexpr int kPer = D / 8;
+    for (int i = tid; i < walk.rows * kPer; i += 128) {
+        const int row = i / kPer, d = (i % kPer) * 8;
+        float mx = -INFINITY, sum = 0.f;
+        for (int k = 0; k < parts; ++k)
+            if (!empty(k)) mx = fmaxf(mx, reinterpret_cast<const float2*>(part_of(k) + ROWS * D)[row].x);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float v[8] = {};
+        for (int k = 0; k < parts; ++k) {
+            if (empty(k)) continue;
+            const float* f = part_of(k);
+            const float2 ml = reinterpret_cast<const float2*>(f + ROWS * D)[row];
+            const float w = exp2_approx(ml.x - ref);
+            sum += w * ml.y;
+            const float4 x = *reinterpret_cast<const float4*>(f + row * D + d);
+            const float4 y = *reinterpret_cast<const float4*>(f + row * D + d + 4);
+            v[0] += w * x.x; v[1] += w * x.y; v[2] += w * x.z; v[3] += w * x.w;
+            v[4] += w * y.x; v[5] += w * y.y; v[6] += w * y.z; v[7] += w * y.w;
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int R = walk.row0 + row, t = R / p.group, h = walk.head * p.group + (R - t * p.group);
+        const int64_t at_row = (int64_t)(walk.q.q0 + t) * p.heads + h;
+        uint4 o;
+        o.x = pack2<DT>(v[0] * inv, v[1] * inv);
+        o.y = pack2<DT>(v[2] * inv, v[3] * inv);
+        o.z = pack2<DT>(v[4] * inv, v[5] * inv);
+        o.w = pack2<DT>(v[6] * inv, v[7] * inv);
+        *reinterpret_cast<uint4*>(p.out + at_row * D + d) = o;
+        if (d == 0 && p.lse) p.lse[at_row] = sum > 0.f ? (mx + log2f(sum)) * 0.693147180559945f : -INFINITY;
+    }
+}
+
+template <class... Args>
+cudaError_t launch(void (*kern)(Args...), int grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D, int DT>
+cudaError_t launch_typed(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream,
+                         int* launches) {
+    cudaError_t e = launch(attn_decode_kernel<D, DT>, p.G, kThreads, DecodeShape<D>::kBytes, stream, p, k, v);
+    if (e != cudaSuccess) return e;
+    *launches = 1;
+    e = launch(attn_join_kernel<D, DT, kRows, Small>, p.G, 128, 0, stream, p);
+    if (e == cudaSuccess) *launches = 2;
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_attn(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
+                        cudaStream_t stream, int* launches) {
+    const CUtensorMap& k = *static_cast<const CUtensorMap*>(k_map);
+    const CUtensorMap& v = *static_cast<const CUtensorMap*>(v_map);
+    *launches = 0;
+    if (head_dim == 128)
+        return dtype == 0 ? launch_typed<128, 0>(p, k, v, stream, launches) : launch_typed<128, 1>(p, k, v, stream, launches);
+    return dtype == 0 ? launch_typed<64, 0>(p, k, v, stream, launches) : launch_typed<64, 1>(p, k, v, stream, launches);
+}
+
+}  // namespace moe

@@ -1,0 +1,90 @@
+// Launch parameters of the paged-step kernels (plan, cache append, attention
+// over the paged cache, sampling). Plain C++, shared by the host launchers
+// and the kernels.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace moe {
+
+constexpr int kMaxRequests = 4096;
+
+struct PlanParams {
+    const int32_t* ctx;
+    const int32_t* fresh;  // new tokens of each request
+    const int32_t* free_list;
+    const int32_t* free_head;  // may be null
+    int32_t* tables;
+    int32_t* q_start;
+    int32_t* seq;
+    int32_t* slots;
+    int32_t* positions;  // may be null
+    int32_t* taken;
+    unsigned* ctrl;
+    int B, n_free, max_blocks, block_size, T;
+};
+
+struct AppendParams {
+    const uint16_t* src[2];  // new keys, new values
+    uint16_t* dst[2];        // the cache's K and V
+    int64_t src_token[2], src_head[2];
+    int64_t dst_block[2], dst_token[2], dst_head[2];
+    const int32_t* slots;
+    unsigned* ctrl;
+    int T, heads, dim_shift;  // head_dim = 8 << dim_shift
+    int block_size;
+    int64_t n_slots;
+};
+
+constexpr int kSampleThreads = 512;
+constexpr int kSampleBins = 2048;
+constexpr int kSampleMaxSlice = 45056;  // logits of a row that one CTA holds
+
+struct SampleParams {
+    const void* logits;
+    const float* u;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* token;
+    float* prob;
+    int64_t row_stride;
+    int V, C, slice;
+};
+
+// Attention over the paged cache. Keys are taken in tiles of kAttnTile.
+constexpr int kAttnTile = 128;
+constexpr int kAttnRows = 32;       // query rows of an item of the decode kernel
+constexpr int kAttnMaxGrid = 256;   // CTAs of a launch (workspace sizing)
+
+struct AttnParams {
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;  // may be null
+    const int32_t* tables;
+    const int32_t* q_start;
+    const int32_t* seq;
+    unsigned* ctrl;
+    float* part;  // partial results of items that span CTAs, [G][2]
+    int64_t q_token, q_head;
+    int T, B, heads, kv_heads, group;
+    int max_blocks, block_size, n_blocks;
+    int box;     // keys that one copy brings
+    int window;
+    int G;       // CTAs
+    float scale_log2;  // scale * log2(e)
+    unsigned long long timeout_ns;
+};
+
+cudaError_t launch_attn(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
+                        cudaStream_t stream, int* launches);
+// Floats of one partial result of `rows` rows.
+constexpr int attn_part_floats(int rows, int head_dim) { return rows * (head_dim + 2); }
+
+cudaError_t launch_paged_plan(const PlanParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_paged_append(const AppendParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_sample(const SampleParams& p, int M, int dtype, cudaStream_t stream);
+
+}  // namespace moe

@@ -1,0 +1,163 @@
+"""moe_sample against the rules in float64 (tests/paged_util.py). Masses are
+sums of terms with a relative error of some 2^-23, so the cumulated mass is
+off by far less than 2^-20 of the total: a row whose u (or top_p) comes that
+near to a border may take the neighbour."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from paged_util import sample_row
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api():
+    from moe_decode_gb300 import build
+    build.build()
+    from moe_decode_gb300 import api as a
+    return a
+
+
+def run(api, logits, u, **settings):
+    M = logits.shape[0]
+    tokens = torch.full((M,), -7, dtype=torch.int32, device="cuda")
+    probs = torch.full((M,), math.nan, device="cuda")
+    f = {n: (None if v is None else torch.as_tensor(v, dtype=torch.int32 if n == "top_k" else torch.float32).expand(M).contiguous().cuda())
+         for n, v in settings.items()}
+    api.sample(logits, torch.as_tensor(u, dtype=torch.float32).expand(M).contiguous().cuda(), tokens, probs=probs, **f)
+    assert api.last_launch_count() == 1
+    return tokens.cpu().numpy(), probs.cpu().numpy(), {n: (None if v is None else v.cpu().numpy()) for n, v in f.items()}
+
+
+def check(api, logits, u, least=0.9, **settings):
+    tokens, probs, f = run(api, logits, u, **settings)
+    u = np.broadcast_to(np.asarray(u, np.float32), (logits.shape[0],))
+    at = lambda n, r, off: off if f.get(n) is None else f[n][r].item()  # noqa: E731
+    clear = 0
+    for r, row in enumerate(logits.double().cpu().numpy()):
+        want, prob, margin = sample_row(row, float(u[r]), at("temperature", r, 1.0), at("top_k", r, 0), at("top_p", r, 1.0),
+                                        at("min_p", r, 0.0))
+        if margin > 2.0 ** -20:
+            clear += 1
+            assert tokens[r] == want, (r, tokens[r], want, margin)
+            # a term's error and the rounding of the answer to fp32
+            assert abs(probs[r] - prob) <= 2.0 ** -20 * prob, (r, probs[r], prob)
+    assert clear >= least * len(u)
+
+
+def logits_of(M, V, seed, dtype=torch.float32, spread=2.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.empty((M, V), device="cuda").normal_(0, spread, generator=g)
+    hot = torch.randint(0, V, (M, 20), device="cuda", generator=g)
+    x.scatter_add_(1, hot, torch.empty((M, 20), device="cuda").normal_(5, 2, generator=g))
+    return x.to(dtype), torch.rand(M, device="cuda", generator=g).cpu()
+
+
+SETTINGS = [dict(), dict(temperature=0.7), dict(top_k=50), dict(top_p=0.9), dict(min_p=0.05), dict(temperature=0.0),
+            dict(top_k=1), dict(temperature=1.3, top_k=1000, top_p=0.95), dict(top_k=7, top_p=0.5, min_p=0.2),
+            dict(temperature=0.05, top_p=0.99), dict(temperature=8.0, top_p=0.7), dict(temperature=30.0, top_k=20000, top_p=0.999)]
+
+
+@pytest.mark.parametrize("V", [1, 2, 31, 1000, 4097, 50257])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("settings", SETTINGS, ids=lambda d: "-".join("%s%g" % p for p in d.items()) or "plain")
+def test_settings(api, V, dtype, settings):
+    x, u = logits_of(5, V, V + len(settings), dtype)
+    # (no count of clear rows here: top_p 0.999 of 20,000 nearly equal masses
+    # ends within 2^-20 of a border in every row)
+    check(api, x, u, least=0.0, **settings)
+
+
+@pytest.mark.parametrize("M,V", [(1, 157184), (16, 157184), (40, 33333), (200, 3001), (1, 720896), (3, 131073)])
+def test_rows_and_vocabularies(api, M, V):
+    rs = np.random.RandomState(M)
+    x, u = logits_of(M, V, M)
+    check(api, x, u, least=0.8, temperature=rs.choice([0.0, 0.6, 1.0, 1.5], M), top_k=rs.choice([0, 1, 20, 1000, V, V + 5], M),
+          top_p=rs.choice([1.0, 0.5, 0.95], M), min_p=rs.choice([0.0, 0.01], M))
+
+
+def test_rows_at_any_stride_and_alignment(api):
+    base, u = logits_of(6, 5003, 3)
+    for dtype in (torch.float32, torch.bfloat16):
+        wide = torch.full((6, 5011), 99.0, dtype=dtype, device="cuda")
+        wide[:, 3:5006] = base.to(dtype)
+        check(api, wide[:, 3:5006], u, top_p=0.9)
+
+
+@pytest.mark.parametrize("n", [1, 700, 1025, 5000, 40000])
+@pytest.mark.parametrize("settings", [dict(top_k=3), dict(top_k=1500), dict(top_p=0.37), dict(top_k=4000, top_p=0.61), dict()], ids=str)
+def test_ties_take_the_lower_index(api, n, settings):
+    """n equal logits above a few others: the order among them is the index."""
+    x = torch.full((4, 60000), -3.0, device="cuda")
+    x[:, 100:100 + n] = 2.5
+    x[1, 50] = 4.0
+    x[2, 59999] = 2.75
+    x[3] = 1.0
+    check(api, x, [0.2, 0.7, 0.999, 0.41], least=0.5, **settings)
+
+
+def test_infinities_and_nan(api):
+    x = torch.randn((6, 2000), device="cuda")
+    x[0] = -math.inf
+    x[1] = math.nan
+    x[2, 5::7] = math.nan
+    x[2, 6::7] = -math.inf
+    x[3, [40, 900, 1500]] = math.inf
+    x[4] = -math.inf
+    x[4, 1234] = -1e30
+    x[5, :1000] = -math.inf
+    x[5, 1000:] = -0.0
+    x[5, 1500] = 0.0
+    for settings in (dict(), dict(temperature=0.0), dict(top_k=2), dict(top_k=1999, top_p=0.5), dict(top_p=0.3, min_p=0.5)):
+        for u in (0.0, 0.4, 0.99):
+            check(api, x, u, least=0.5, **settings)
+    tokens, probs, _ = run(api, x, 0.5)
+    assert tokens[0] == tokens[1] == -1 and probs[0] == probs[1] == 0
+    assert tokens[3] == 900 and abs(probs[3] - 1 / 3) < 1e-6 and tokens[4] == 1234 and probs[4] == 1
+
+
+def test_random_numbers_at_and_beyond_their_ends(api):
+    x, _ = logits_of(6, 3000, 8)
+    want = [0, 0, 2999, 2999, 0, 2999]
+    tokens, _, _ = run(api, torch.zeros_like(x), [0.0, -1.0, 1.0, 7.0, math.nan, float(np.nextafter(np.float32(1), np.float32(0)))])
+    assert tokens.tolist() == want
+    x[:, 2000:] = -math.inf
+    tokens, _, _ = run(api, x, 1.0, top_p=0.9)
+    assert (tokens < 2000).all()
+
+
+def test_settings_beyond_their_ends(api):
+    x, u = logits_of(3, 3000, 9)
+    plain = run(api, x, u)[0]
+    for settings in (dict(top_k=-5), dict(top_k=1 << 30), dict(top_p=1.0), dict(top_p=5.0), dict(min_p=-1.0), dict(temperature=1.0)):
+        assert (run(api, x, u, **settings)[0] == plain).all()
+    best = x.argmax(1).cpu().numpy()
+    for settings in (dict(temperature=-1.0), dict(temperature=math.nan), dict(top_p=0.0), dict(top_p=-3.0), dict(min_p=1.0),
+                     dict(min_p=9.0), dict(temperature=1e-35), dict(top_k=1)):
+        assert (run(api, x, u, **settings)[0] == best).all(), settings
+    tokens, probs, _ = run(api, x, 0.5, temperature=math.inf)
+    assert (tokens == 1500).all() and np.allclose(probs, 1 / 3000, rtol=1e-6)
+
+
+def test_frequencies_follow_the_masses(api):
+    """20,000 rows of one distribution with evenly spread u: each token's
+    count is its mass times the rows, to a row or two."""
+    x = torch.tensor([0.0, 1.0, -1.0, 2.0, 0.5, -math.inf, 1.5, -2.0], device="cuda")
+    n = 20000
+    u = (torch.arange(n) + 0.5) / n
+    tokens, _, _ = run(api, x.expand(n, 8).contiguous(), u, temperature=0.8, top_k=6)
+    w = np.exp(x.cpu().numpy().astype(np.float64) / 0.8)
+    w[[5, 7]] = 0
+    assert np.abs(np.bincount(tokens, minlength=8) - n * w / w.sum()).max() <= 2
+
+
+def test_same_token_on_any_split(api):
+    """Rows of one call and each row by itself go over other numbers of CTAs."""
+    x, u = logits_of(40, 20011, 12)
+    together = run(api, x, u, top_p=0.93, temperature=1.1)
+    for r in range(0, 40, 7):
+        alone = run(api, x[r:r + 1], u[r:r + 1], top_p=0.93, temperature=1.1)
+        assert alone[0][0] == together[0][r] and alone[1][0] == together[1][r]
