@@ -184,7 +184,8 @@ size_t moe_paged_attention_workspace_bytes(int q_heads, const moe_kv_cache* cach
     if (check_cache(cache) != MOE_OK) return 0;
     if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 32) return 0;
     return MOE_PAGED_WORKSPACE_BYTES +
-           (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows, cache->head_dim) * sizeof(float);
+           (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows + moe::kAttnChunkRows, cache->head_dim) *
+               sizeof(float);
 }
 
 int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int T, int q_heads,
@@ -222,6 +223,7 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     p.seq = seq_lens;
     p.ctrl = static_cast<unsigned*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MOE_PAGED_WORKSPACE_BYTES);
+    p.chunk_part = p.part + (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows, cache->head_dim);
     p.q_token = q_token_stride;
     p.q_head = q_head_stride;
     p.T = T;

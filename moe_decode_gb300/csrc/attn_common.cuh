@@ -20,6 +20,8 @@
 
 namespace moe {
 
+constexpr float kLn2 = 0.693147180559945f;
+
 struct Request {
     int q0, n;     // first token row, tokens
     int pos0;      // position of the first token (negative: rows that see nothing)
@@ -55,19 +57,60 @@ __device__ __forceinline__ int attn_tiles(int lo, int hi) {
     return hi > lo ? (hi - 1) / kAttnTile - lo / kAttnTile + 1 : 1;
 }
 
-// Units of request r for one kv head.
+// The row tiles of a request in order: units of each, with the token of a
+// tile's first and last row kept by addition (a chunk of 8,192 tokens has some
+// hundred row tiles, and one thread counts them).
+template <int ROWS>
+struct RowTiles {
+    const AttnParams& p;
+    int pos0, rows, row0 = 0;
+    int first, first_rem;  // token of the tile's first row, row within the token
+    int step, step_rem;
+    int64_t cap;
+    __device__ __forceinline__ RowTiles(const AttnParams& params, const Request& q)
+        : p(params), pos0(q.pos0), rows(q.n * params.group), first(0), first_rem(0), step(ROWS / params.group),
+          step_rem(ROWS % params.group), cap((int64_t)params.max_blocks * params.block_size) {}
+    __device__ __forceinline__ bool more() const { return row0 < rows; }
+    __device__ __forceinline__ int tiles() const {
+        int last = first + step + (first_rem + step_rem >= p.group ? 1 : 0);  // token of the next tile's first row
+        if ((first_rem + step_rem) % p.group == 0) --last;                    // which may begin there
+        if (row0 + ROWS >= rows) last = (rows - 1) / p.group;
+        const int hi = (int)min((int64_t)pos0 + last + 1, cap);
+        const int lo = p.window > 0 ? max(pos0 + first - p.window + 1, 0) : 0;
+        return attn_tiles(lo, hi);
+    }
+    __device__ __forceinline__ void next() {
+        row0 += ROWS;
+        first += step;
+        first_rem += step_rem;
+        if (first_rem >= p.group) {
+            first_rem -= p.group;
+            ++first;
+        }
+    }
+};
+
+// Units of a request for one kv head.
 template <int ROWS>
 __device__ __forceinline__ int64_t attn_request_units(const AttnParams& p, const Request& q) {
-    const int rows = q.n * p.group;
     int64_t u = 0;
-    for (int r0 = 0; r0 < rows; r0 += ROWS) {
-        int lo, hi;
-        bool over;
-        attn_keys(p, q, r0, min(ROWS, rows - r0), lo, hi, over);
-        u += attn_tiles(lo, hi);
-    }
+    for (RowTiles<ROWS> t(p, q); t.more(); t.next()) u += t.tiles();
     return u;
 }
+
+// Which kernel takes a request.
+struct Few {
+    static constexpr int kRows = kAttnRows;
+    static __device__ __forceinline__ bool mine(const AttnParams& p, const Request& q) {
+        return q.n > 0 && q.n * p.group <= kAttnFewRows;
+    }
+};
+struct Many {
+    static constexpr int kRows = kAttnChunkRows;
+    static __device__ __forceinline__ bool mine(const AttnParams& p, const Request& q) {
+        return q.n * p.group > kAttnFewRows;
+    }
+};
 
 // A place in the order of units, and the CTA's range.
 struct Place {
@@ -80,8 +123,9 @@ struct Place {
 // Finds the CTA's range and the request that it begins in, all threads
 // together. `scan` is shared memory of THREADS / 32 values, `found` one of
 // two.
-template <int ROWS, int THREADS, class Class>
-__device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, Class mine, int64_t* scan, int64_t* found) {
+template <class Class, int THREADS>
+__device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_t* scan, int64_t* found) {
+    constexpr int ROWS = Class::kRows;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + THREADS - 1) / THREADS;
     const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
@@ -90,7 +134,7 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, Class 
     for (int r = r0; r < r1; ++r) {
         const Request q = attn_request(p, r);
         bad |= q.bad;
-        if (mine(q)) own += attn_request_units<ROWS>(p, q) * p.kv_heads;
+        if (Class::mine(p, q)) own += attn_request_units<ROWS>(p, q) * p.kv_heads;
     }
     if (bad) atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
     int64_t sum = own;
@@ -117,7 +161,7 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, Class 
     if (own > 0 && before <= at.begin && at.begin < before + own) {
         for (int r = r0; r < r1; ++r) {
             const Request q = attn_request(p, r);
-            const int64_t u = mine(q) ? attn_request_units<ROWS>(p, q) * p.kv_heads : 0;
+            const int64_t u = Class::mine(p, q) ? attn_request_units<ROWS>(p, q) * p.kv_heads : 0;
             if (at.begin < before + u) {
                 found[0] = r;
                 found[1] = at.begin - before;
@@ -134,10 +178,10 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, Class 
 
 // The items of a CTA's range, one after another; every role of the CTA walks
 // them alike.
-template <int ROWS, class Class>
+template <class Class>
 struct Walk {
+    static constexpr int ROWS = Class::kRows;
     const AttnParams& p;
-    Class mine;
     int64_t unit, end;  // next unit of the range
     int r, head, row0;
     int skip;           // tiles of the item at hand before the range
@@ -147,18 +191,16 @@ struct Walk {
     int t0, t1;         // its tiles [t0, t1) in this range
     bool over;
 
-    __device__ __forceinline__ Walk(const AttnParams& params, const Place& at, Class c)
-        : p(params), mine(c), unit(at.begin), end(at.end), r(at.request), head(0), row0(0), skip(0) {
+    __device__ __forceinline__ Walk(const AttnParams& params, const Place& at)
+        : p(params), unit(at.begin), end(at.end), r(at.request), head(0), row0(0), skip(0) {
         if (unit >= end) return;
         q = attn_request(p, r);
         const int64_t per_head = attn_request_units<ROWS>(p, q);
         head = (int)(at.rest / per_head);
         int64_t rest = at.rest - head * per_head;
-        for (;; row0 += ROWS) {
-            item();
-            if (rest < tiles) break;
-            rest -= tiles;
-        }
+        RowTiles<ROWS> t(p, q);
+        for (; rest >= t.tiles(); t.next()) rest -= t.tiles();
+        row0 = t.row0;
         skip = (int)rest;
     }
     __device__ __forceinline__ void item() {
@@ -186,7 +228,7 @@ struct Walk {
         head = 0;
         do {
             q = attn_request(p, ++r);
-        } while (!mine(q) || q.n == 0);
+        } while (!Class::mine(p, q));
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
     // An item that began in an earlier CTA leaves part 0, one that goes on in

@@ -45,10 +45,6 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr));
 }
 
-struct Small {
-    __device__ __forceinline__ bool operator()(const Request&) const { return true; }
-};
-
 // Each of the four consumer warps takes 32 keys of every tile against all of
 // the item's rows (16 or 32), with its own running largest score, sum and
 // output, so no warp reads another's keys from shared memory; the four are
@@ -75,10 +71,10 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     }
     pdl_wait();
     pdl_launch_dependents();
-    const Place at = attn_place<kRows, kThreads>(p, blockIdx.x, Small(), scan, found);
+    const Place at = attn_place<Few, kThreads>(p, blockIdx.x, scan, found);
     if (at.begin >= at.end) return;
     volatile int* flag = &abort_flag;
-    Walk<kRows, Small> walk(p, at, Small());
+    Walk<Few> walk(p, at);
 
     if (warp == kConsumers) {
         // producer: lane i brings the tile's i-th box, if a row sees any of it
@@ -384,7 +380,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 v.z = pack2<DT>(y.x * inv, y.y * inv);
                 v.w = pack2<DT>(y.z * inv, y.w * inv);
                 *reinterpret_cast<uint4*>(p.out + at_row * D + c * 8) = v;
-                if (c == 0 && p.lse) p.lse[at_row] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * 0.693147180559945f : -INFINITY;
+                if (c == 0 && p.lse) p.lse[at_row] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
             } else {
                 *reinterpret_cast<float4*>(part + row * D + c * 8) = x;
                 *reinterpret_cast<float4*>(part + row * D + c * 8 + 4) = y;
@@ -396,26 +392,17 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     }
 }
 
-// Joins the parts of the item that begins in CTA c and goes on past its end
-// (there is at most one), part after part in the order of the keys, and
-// clears padding rows.
-template <int D, int DT, int ROWS, class Class>
-__global__ __launch_bounds__(128) void attn_join_kernel(const __grid_constant__ AttnParams p) {
-    __shared__ int64_t scan[4], found[2];
-    pdl_wait();
-    pdl_launch_dependents();
+// Joins the parts of the item of CTA c that goes on past the CTA's end (there
+// is at most one that begins there), part after part in the order of the
+// keys: kAttnRows rows from row `from` on.
+template <int D, int DT, class Class>
+__device__ __forceinline__ void join(const AttnParams& p, const float* parts, int c, int from, int64_t* scan,
+                                     int64_t* found) {
+    constexpr int ROWS = Class::kRows;
     const int tid = threadIdx.x;
-    const int last = min(max(p.q_start[p.B], 0), p.T);
-    for (int64_t i = (int64_t)last * p.heads + blockIdx.x * 4 + (tid >> 5); i < (int64_t)p.T * p.heads;
-         i += (int64_t)gridDim.x * 4) {
-        reinterpret_cast<uint32_t*>(p.out + i * D)[tid & 31] = 0u;
-        if (D == 128) reinterpret_cast<uint32_t*>(p.out + i * D)[32 + (tid & 31)] = 0u;
-        if (p.lse && (tid & 31) == 0) p.lse[i] = -INFINITY;
-    }
-    const int c = blockIdx.x;
-    const Place at = attn_place<ROWS, 128>(p, c, Class(), scan, found);
+    const Place at = attn_place<Class, 128>(p, c, scan, found);
     if (at.begin >= at.end || at.end >= at.total) return;
-    Walk<ROWS, Class> walk(p, at, Class());
+    Walk<Class> walk(p, at);
     // the last item of the range
     bool spans = false;
     while (walk.next()) {
@@ -423,27 +410,28 @@ __global__ __launch_bounds__(128) void attn_join_kernel(const __grid_constant__ 
         if (walk.unit + (walk.t1 - walk.t0) >= walk.end) break;
         walk.done();
     }
-    if (!spans) return;
+    if (!spans || from >= walk.rows) return;
     // its parts: CTA c's part 1, then part 0 of the CTAs up to its last unit
     const int64_t end = at.end + (walk.tiles - walk.t1);
-    int parts = 1;
+    int n = 1;
     for (int k = c + 1; k < p.G; ++k) {
         const int64_t b = at.total * k / p.G, e = at.total * (k + 1) / p.G;
         if (b >= end) break;
-        if (e > b) parts = k - c + 1;
+        if (e > b) n = k - c + 1;
     }
     constexpr int kFloats = attn_part_floats(ROWS, D);
-    auto part_of = [&](int k) { return p.part + ((int64_t)(c + k) * 2 + (k == 0 ? 1 : 0)) * kFloats; };
+    auto part_of = [&](int k) { return parts + ((int64_t)(c + k) * 2 + (k == 0 ? 1 : 0)) * kFloats; };
     auto empty = [&](int k) { return at.total * (c + k) / p.G >= at.total * (c + k + 1) / p.G; };
     constexpr int kPer = D / 8;
-    for (int i = tid; i < walk.rows * kPer; i += 128) {
+    const int to = min(from + kAttnRows, walk.rows);
+    for (int i = tid + from * kPer; i < to * kPer; i += 128) {
         const int row = i / kPer, d = (i % kPer) * 8;
         float mx = -INFINITY, sum = 0.f;
-        for (int k = 0; k < parts; ++k)
+        for (int k = 0; k < n; ++k)
             if (!empty(k)) mx = fmaxf(mx, reinterpret_cast<const float2*>(part_of(k) + ROWS * D)[row].x);
         const float ref = mx == -INFINITY ? 0.f : mx;
         float v[8] = {};
-        for (int k = 0; k < parts; ++k) {
+        for (int k = 0; k < n; ++k) {
             if (empty(k)) continue;
             const float* f = part_of(k);
             const float2 ml = reinterpret_cast<const float2*>(f + ROWS * D)[row];
@@ -463,18 +451,41 @@ __global__ __launch_bounds__(128) void attn_join_kernel(const __grid_constant__ 
         o.z = pack2<DT>(v[4] * inv, v[5] * inv);
         o.w = pack2<DT>(v[6] * inv, v[7] * inv);
         *reinterpret_cast<uint4*>(p.out + at_row * D + d) = o;
-        if (d == 0 && p.lse) p.lse[at_row] = sum > 0.f ? (mx + log2f(sum)) * 0.693147180559945f : -INFINITY;
+        if (d == 0 && p.lse) p.lse[at_row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
     }
 }
 
+// Padding rows, and the parts of both kernels: block (c, 0) joins the decode
+// kernel's of CTA c, block (c, 1 + i) rows [32 i, 32 i + 32) of the chunk
+// kernel's (only there when that kernel ran).
+template <int D, int DT>
+__global__ __launch_bounds__(128) void attn_join_kernel(const __grid_constant__ AttnParams p) {
+    __shared__ int64_t scan[4], found[2];
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.y > 0) {
+        join<D, DT, Many>(p, p.chunk_part, blockIdx.x, (blockIdx.y - 1) * kAttnRows, scan, found);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int last = min(max(p.q_start[p.B], 0), p.T);
+    for (int64_t i = (int64_t)last * p.heads + blockIdx.x * 4 + (threadIdx.x >> 5); i < (int64_t)p.T * p.heads;
+         i += (int64_t)gridDim.x * 4) {
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) reinterpret_cast<uint32_t*>(p.out + i * D)[32 * x + lane] = 0u;
+        if (p.lse && lane == 0) p.lse[i] = -INFINITY;
+    }
+    join<D, DT, Few>(p, p.part, blockIdx.x, 0, scan, found);
+}
+
 template <class... Args>
-cudaError_t launch(void (*kern)(Args...), int grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
+cudaError_t launch(void (*kern)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
     if (smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
@@ -489,11 +500,18 @@ cudaError_t launch(void (*kern)(Args...), int grid, int threads, int smem, cudaS
 template <int D, int DT>
 cudaError_t launch_typed(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream,
                          int* launches) {
-    cudaError_t e = launch(attn_decode_kernel<D, DT>, p.G, kThreads, DecodeShape<D>::kBytes, stream, p, k, v);
+    cudaError_t e =
+        launch(attn_decode_kernel<D, DT>, dim3((unsigned)p.G), kThreads, DecodeShape<D>::kBytes, stream, p, k, v);
     if (e != cudaSuccess) return e;
-    *launches = 1;
-    e = launch(attn_join_kernel<D, DT, kRows, Small>, p.G, 128, 0, stream, p);
-    if (e == cudaSuccess) *launches = 2;
+    ++*launches;
+    const bool many = (int64_t)p.T * p.group > kAttnFewRows;
+    if (many) {
+        e = launch_attn_chunk(p, &k, &v, D, DT, stream);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    e = launch(attn_join_kernel<D, DT>, dim3((unsigned)p.G, many ? 1 + kAttnChunkRows / kAttnRows : 1), 128, 0, stream, p);
+    if (e == cudaSuccess) ++*launches;
     return e;
 }
 

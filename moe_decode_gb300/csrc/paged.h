@@ -57,6 +57,9 @@ struct SampleParams {
 // Attention over the paged cache. Keys are taken in tiles of kAttnTile.
 constexpr int kAttnTile = 128;
 constexpr int kAttnRows = 32;       // query rows of an item of the decode kernel
+constexpr int kAttnChunkRows = 256; // and of the chunk kernel
+// Requests with more query rows a kv head than this go to the chunk kernel.
+constexpr int kAttnFewRows = 64;
 constexpr int kAttnMaxGrid = 256;   // CTAs of a launch (workspace sizing)
 
 struct AttnParams {
@@ -67,7 +70,8 @@ struct AttnParams {
     const int32_t* q_start;
     const int32_t* seq;
     unsigned* ctrl;
-    float* part;  // partial results of items that span CTAs, [G][2]
+    float* part;        // partial results of items that span CTAs, [G][2]
+    float* chunk_part;  // and those of the chunk kernel's
     int64_t q_token, q_head;
     int T, B, heads, kv_heads, group;
     int max_blocks, block_size, n_blocks;
@@ -78,8 +82,13 @@ struct AttnParams {
     unsigned long long timeout_ns;
 };
 
+// Key and value maps are CUtensorMaps. The decode kernel and the join
+// of all parts; the chunk kernel (between the two, where any request may have
+// many rows).
 cudaError_t launch_attn(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
                         cudaStream_t stream, int* launches);
+cudaError_t launch_attn_chunk(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
+                              cudaStream_t stream);
 // Floats of one partial result of `rows` rows.
 constexpr int attn_part_floats(int rows, int head_dim) { return rows * (head_dim + 2); }
 
