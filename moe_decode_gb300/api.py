@@ -270,8 +270,18 @@ def _raw(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it: 0.3 us a
+# call where torch.cuda.current_stream() takes 2.9 (measured on the host of a
+# GB300), of a call whose launch takes 4.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _current_raw_stream(torch.cuda.current_device())
 
 
 def _vector(t: Optional[torch.Tensor], n: Optional[int], dtype: torch.dtype, what: str):

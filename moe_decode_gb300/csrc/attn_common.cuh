@@ -6,8 +6,8 @@
 // request is token R / group, query head R % group of the kv head's group, so
 // that the heads that share keys share the read. A unit is one tile of
 // kAttnTile keys of one item. All units of the call in the order request, kv
-// head, row tile, key tile are divided evenly: CTA c takes the units [cU/G,
-// (c+1)U/G), whatever the lengths. An item whose units all lie in one CTA is
+// head, row tile, key tile are divided evenly: of G CTAs (or as many as there
+// are units) CTA c takes the units [cU/G, (c+1)U/G), whatever the lengths. An item whose units all lie in one CTA is
 // finished there; of one that spans CTAs each leaves its part (unnormalised
 // sums, largest score, sum of weights) in the workspace, and a second kernel
 // joins the parts in the order of the keys.
@@ -115,6 +115,7 @@ struct Many {
 // A place in the order of units, and the CTA's range.
 struct Place {
     int64_t total;      // units of the call
+    int ctas;           // CTAs with units
     int64_t begin, end; // this CTA's
     int request;        // request of unit `begin`
     int64_t rest;       // units of that request before `begin`
@@ -156,8 +157,9 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_
         if (w < warp) before += scan[w];
         at.total += scan[w];
     }
-    at.begin = at.total * cta / p.G;
-    at.end = at.total * (cta + 1) / p.G;
+    at.ctas = (int)min((int64_t)p.G, at.total);
+    at.begin = cta < at.ctas ? at.total * cta / at.ctas : at.total;
+    at.end = cta < at.ctas ? at.total * (cta + 1) / at.ctas : at.total;
     if (own > 0 && before <= at.begin && at.begin < before + own) {
         for (int r = r0; r < r1; ++r) {
             const Request q = attn_request(p, r);

@@ -7,9 +7,10 @@ namespace moe {
 namespace {
 
 constexpr int kRows = kAttnRows;
-constexpr int kConsumers = 4;  // warps; one producer warp on top
+constexpr int kKeyWarps = 4;               // warps that share a tile's keys
+constexpr int kConsumers = 2 * kKeyWarps;  // for each of two sets of 16 rows; one producer warp on top
 constexpr int kThreads = (kConsumers + 1) * 32;
-constexpr int kWarpKeys = kAttnTile / kConsumers;
+constexpr int kWarpKeys = kAttnTile / kKeyWarps;
 
 template <int D>
 struct DecodeShape {
@@ -22,7 +23,7 @@ struct DecodeShape {
     static constexpr int kOffQ = kStages * kStage;
     static constexpr int kOffMerge = kOffQ + kQ;
     static constexpr int kOffStat = kOffMerge + kMerge;      // largest score and sum of each warp's rows
-    static constexpr int kOffBar = kOffStat + kConsumers * kRows * 8;
+    static constexpr int kOffBar = kOffStat + kKeyWarps * kRows * 8;
     static constexpr int kBytes = kOffBar + 256 + 1024;      // and room to align
 };
 
@@ -45,10 +46,9 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr));
 }
 
-// Each of the four consumer warps takes 32 keys of every tile against all of
-// the item's rows (16 or 32), with its own running largest score, sum and
-// output, so no warp reads another's keys from shared memory; the four are
-// joined once at the end of the item.
+// Each consumer warp takes 32 keys of every tile against 16 of the item's 32
+// rows, with its own running largest score, sum and output; the four warps of
+// a set of rows are joined once at the end of the item.
 template <int D, int DT>
 __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_constant__ AttnParams p,
                                                                    const __grid_constant__ CUtensorMap kmap,
@@ -134,17 +134,17 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     }
 
     const int quad = lane >> 2, pair = lane & 3;
+    const int set = warp / kKeyWarps, kw = warp % kKeyWarps;  // rows [16 set, 16 set + 16), a quarter of the keys
     int stage = 0;
     uint32_t parity = 0;
     uint8_t* qs = sm + S::kOffQ;
-    const uint32_t q_addr = base + S::kOffQ;
-    float2* stat = reinterpret_cast<float2*>(sm + S::kOffStat);  // [warp][row]
+    const uint32_t q_addr = base + S::kOffQ + set * 16 * (D * 2);
+    float2* stat = reinterpret_cast<float2*>(sm + S::kOffStat);  // [key warp][row]
     float* merge = reinterpret_cast<float*>(sm + S::kOffMerge);  // [row][D + 4]
     for (; walk.next(); walk.done()) {
         // the item's rows into shared memory, 16-byte pieces swizzled like the
         // keys; rows past the end are zeros
-        const int mts = walk.rows > 16 ? 2 : 1;
-        for (int i = tid; i < mts * 16 * (D / 8); i += kConsumers * 32) {
+        for (int i = tid; i < kRows * (D / 8); i += kConsumers * 32) {
             const int row = i / (D / 8), c = i % (D / 8);
             uint4 v = make_uint4(0, 0, 0, 0);
             if (row < walk.rows) {
@@ -154,43 +154,37 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             *reinterpret_cast<uint4*>(qs + row * (D * 2) + ((c ^ (row & 7)) << 4)) = v;
         }
         named_bar_sync(1, kConsumers * 32);
-        // the last key that each of this thread's rows sees, and the first
-        int last[2][2], from[2][2];
+        const bool active = set * 16 < walk.rows;
+        // the last key that each of this thread's two rows sees, and the first
+        int last[2], from[2];
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int row = a * 16 + b * 8 + quad;
-                const int pos = walk.q.pos0 + (walk.row0 + row) / p.group;
-                last[a][b] = row < walk.rows ? min(pos, walk.hi - 1) : -1;
-                from[a][b] = p.window > 0 ? pos - p.window + 1 : 0;
-            }
-        const int first_pos = walk.q.pos0 + walk.row0 / p.group;
-        const int last_from =
-            p.window > 0 ? walk.q.pos0 + (walk.row0 + walk.rows - 1) / p.group - p.window + 1 : 0;
-        float o[2][D / 8][4];
-        float m[2][2], l[2][2];
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[a][i][j] = 0.f;
-            m[a][0] = m[a][1] = -INFINITY;
-            l[a][0] = l[a][1] = 0.f;
+        for (int b = 0; b < 2; ++b) {
+            const int row = set * 16 + b * 8 + quad;
+            const int pos = walk.q.pos0 + (walk.row0 + row) / p.group;
+            last[b] = row < walk.rows ? min(pos, walk.hi - 1) : -1;
+            from[b] = p.window > 0 ? pos - p.window + 1 : 0;
         }
+        const int all_to = min(walk.q.pos0 + walk.row0 / p.group + 1, walk.hi);
+        const int all_from = p.window > 0 ? walk.q.pos0 + (walk.row0 + walk.rows - 1) / p.group - p.window + 1 : 0;
+        float o[D / 8][4];
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
         for (int t = walk.t0; t < walk.t1; ++t) {
             if (!attn_wait(full + 8 * stage, parity, p, flag)) break;
-            const int key0 = (walk.tile0 + t) * kAttnTile + warp * kWarpKeys;
-            const uint32_t ks = base + stage * S::kStage + warp * kWarpKeys * 128, vs = ks + S::kHalf;
-            if (key0 < walk.hi && key0 + kWarpKeys > walk.lo) {
+            const int key0 = (walk.tile0 + t) * kAttnTile + kw * kWarpKeys;
+            const uint32_t ks = base + stage * S::kStage + kw * kWarpKeys * 128, vs = ks + S::kHalf;
+            if (active && key0 < walk.hi && key0 + kWarpKeys > walk.lo) {
                 const bool ragged = key0 < walk.lo || key0 + kWarpKeys > walk.hi;
                 if (ragged) {
                     // values that no row sees may be anything: a weight of 0 times
-                    // NaN is not 0, so they are cleared
+                    // NaN is not 0, so they are cleared (by both sets of rows,
+                    // each before its own reads)
                     const int key = key0 + lane;
                     if (key < walk.lo || key >= walk.hi) {
-                        uint8_t* v = sm + stage * S::kStage + S::kHalf + (warp * kWarpKeys + lane) * 128;
+                        uint8_t* v = sm + stage * S::kStage + S::kHalf + (kw * kWarpKeys + lane) * 128;
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
 #pragma unroll
@@ -199,84 +193,71 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                     }
                     __syncwarp();
                 }
-                float s[2][4][4];
+                float s[4][4];
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s[a][i][j] = 0.f;
+                    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    uint32_t qa[2][4], kb[2][4];
-#pragma unroll
-                    for (int a = 0; a < 2; ++a)
-                        if (a < mts) {
-                            const int row = a * 16 + (lane & 15), c = 2 * k + (lane >> 4);
-                            ldsm_x4(q_addr + row * (D * 2) + ((c ^ (row & 7)) << 4), qa[a]);
-                        }
+                    uint32_t qa[4], kb[2][4];
+                    {
+                        const int row = lane & 15, c = 2 * k + (lane >> 4);
+                        ldsm_x4(q_addr + row * (D * 2) + ((c ^ (row & 7)) << 4), qa);
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 16 keys each
                         const int row = h * 16 + ((lane >> 4) << 3) + (lane & 7), c = 2 * (k & 3) + ((lane >> 3) & 1);
                         ldsm_x4(ks + (k >> 2) * S::kPanel + row * 128 + ((c ^ (row & 7)) << 4), kb[h]);
                     }
 #pragma unroll
-                    for (int a = 0; a < 2; ++a)
-                        if (a < mts)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                mma_16816<DT>(s[a][2 * h], qa[a], kb[h][0], kb[h][1]);
-                                mma_16816<DT>(s[a][2 * h + 1], qa[a], kb[h][2], kb[h][3]);
-                            }
+                    for (int h = 0; h < 2; ++h) {
+                        mma_16816<DT>(s[2 * h], qa, kb[h][0], kb[h][1]);
+                        mma_16816<DT>(s[2 * h + 1], qa, kb[h][2], kb[h][3]);
+                    }
                 }
-                const bool mask = key0 + kWarpKeys > min(first_pos + 1, walk.hi) || key0 < last_from;
-                uint32_t pa[2][2][4];
+                if (key0 + kWarpKeys > all_to || key0 < all_from) {
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    if (a >= mts) continue;
-                    if (mask) {
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int key = key0 + i * 8 + 2 * pair + (j & 1);
-                                if (key > last[a][j >> 1] || key < from[a][j >> 1]) s[a][i][j] = -INFINITY;
-                            }
-                    }
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(s[a][i][2 * b], s[a][i][2 * b + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        mx *= p.scale_log2;
-                        const bool grows = mx > m[a][b];
-                        if (__any_sync(0xffffffffu, grows)) {
-                            const float to = fmaxf(mx, m[a][b]);
-                            const float f = grows ? exp2_approx(m[a][b] - to) : 1.f;
-                            m[a][b] = to;
-                            l[a][b] *= f;
-#pragma unroll
-                            for (int i = 0; i < D / 8; ++i) {
-                                o[a][i][2 * b] *= f;
-                                o[a][i][2 * b + 1] *= f;
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = key0 + i * 8 + 2 * pair + (j & 1);
+                            if (key > last[j >> 1] || key < from[j >> 1]) s[i][j] = -INFINITY;
                         }
-                        const float ref = m[a][b] == -INFINITY ? 0.f : m[a][b];
-                        float sum = 0.f;
+                }
+                uint32_t pa[2][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float x = exp2_approx(fmaf(s[a][i][2 * b], p.scale_log2, -ref));
-                            const float y = exp2_approx(fmaf(s[a][i][2 * b + 1], p.scale_log2, -ref));
-                            sum += x + y;
-                            // rounded once to the values' type for the second
-                            // product: 2^-9 (bf16) of each weight, independent
-                            // from key to key; the sum keeps the fp32 weights
-                            pa[a][i >> 1][(i & 1) * 2 + b] = pack2<DT>(x, y);
+                for (int b = 0; b < 2; ++b) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(s[i][2 * b], s[i][2 * b + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    mx *= p.scale_log2;
+                    const bool grows = mx > m[b];
+                    if (__any_sync(0xffffffffu, grows)) {
+                        const float f = grows ? exp2_approx(m[b] - mx) : 1.f;
+                        if (grows) m[b] = mx;
+                        l[b] *= f;
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            o[i][2 * b] *= f;
+                            o[i][2 * b + 1] *= f;
                         }
-                        l[a][b] += sum;
                     }
+                    const float ref = m[b] == -INFINITY ? 0.f : m[b];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = exp2_approx(fmaf(s[i][2 * b], p.scale_log2, -ref));
+                        const float y = exp2_approx(fmaf(s[i][2 * b + 1], p.scale_log2, -ref));
+                        sum += x + y;
+                        // rounded once to the values' type for the second
+                        // product: half a step of each weight, independent
+                        // from key to key; the sum keeps the fp32 weights
+                        pa[i >> 1][(i & 1) * 2 + b] = pack2<DT>(x, y);
+                    }
+                    l[b] += sum;
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -285,12 +266,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                         uint32_t vb[4];
                         const int row = h * 16 + (lane & 15), c = 2 * (i & 3) + (lane >> 4);
                         ldsm_x4_trans(vs + (i >> 2) * S::kPanel + row * 128 + ((c ^ (row & 7)) << 4), vb);
-#pragma unroll
-                        for (int a = 0; a < 2; ++a)
-                            if (a < mts) {
-                                mma_16816<DT>(o[a][2 * i], pa[a][h], vb[0], vb[1]);
-                                mma_16816<DT>(o[a][2 * i + 1], pa[a][h], vb[2], vb[3]);
-                            }
+                        mma_16816<DT>(o[2 * i], pa[h], vb[0], vb[1]);
+                        mma_16816<DT>(o[2 * i + 1], pa[h], vb[2], vb[3]);
                     }
                 if (ragged) fence_proxy_async_shared();
             }
@@ -301,68 +278,59 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 parity ^= 1u;
             }
         }
-        // join the four warps: each scales to the largest score of all, then
-        // they add up one after another
+        // join the warps that share the rows: each scales to the largest score
+        // of all, then they add up one after another
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                l[a][b] += __shfl_xor_sync(0xffffffffu, l[a][b], 1);
-                l[a][b] += __shfl_xor_sync(0xffffffffu, l[a][b], 2);
-                if (pair == 0) stat[warp * kRows + a * 16 + b * 8 + quad] = make_float2(m[a][b], l[a][b]);
-            }
+        for (int b = 0; b < 2; ++b) {
+            l[b] += __shfl_xor_sync(0xffffffffu, l[b], 1);
+            l[b] += __shfl_xor_sync(0xffffffffu, l[b], 2);
+            if (pair == 0) stat[kw * kRows + set * 16 + b * 8 + quad] = make_float2(m[b], l[b]);
+        }
         named_bar_sync(1, kConsumers * 32);
-        float big[2][2], sum[2][2];
+        float big[2], sum[2];
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int b = 0; b < 2; ++b) {
+            const int row = set * 16 + b * 8 + quad;
+            float mx = -INFINITY, tot = 0.f;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int row = a * 16 + b * 8 + quad;
-                float mx = -INFINITY, tot = 0.f;
+            for (int w = 0; w < kKeyWarps; ++w) mx = fmaxf(mx, stat[w * kRows + row].x);
+            const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) mx = fmaxf(mx, stat[w * kRows + row].x);
-                const float ref = mx == -INFINITY ? 0.f : mx;
+            for (int w = 0; w < kKeyWarps; ++w)
+                tot += stat[w * kRows + row].y * exp2_approx(stat[w * kRows + row].x - ref);
+            big[b] = mx;
+            sum[b] = tot;
+            const float f = exp2_approx(m[b] - ref);
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w)
-                    tot += stat[w * kRows + row].y * exp2_approx(stat[w * kRows + row].x - ref);
-                big[a][b] = mx;
-                sum[a][b] = tot;
-                const float f = exp2_approx(m[a][b] - ref);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    o[a][i][2 * b] *= f;
-                    o[a][i][2 * b + 1] *= f;
-                }
+            for (int i = 0; i < D / 8; ++i) {
+                o[i][2 * b] *= f;
+                o[i][2 * b + 1] *= f;
             }
-        for (int w = 0; w < kConsumers; ++w) {
-            if (warp == w) {
+        }
+        for (int w = 0; w < kKeyWarps; ++w) {
+            if (kw == w && active) {
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
-                    if (a < mts)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b)
-#pragma unroll
-                            for (int i = 0; i < D / 8; ++i) {
-                                float2* at2 = reinterpret_cast<float2*>(merge + (a * 16 + b * 8 + quad) * (D + 4) +
-                                                                        i * 8 + 2 * pair);
-                                float2 v = make_float2(o[a][i][2 * b], o[a][i][2 * b + 1]);
-                                if (w > 0) {
-                                    const float2 u = *at2;
-                                    v.x += u.x;
-                                    v.y += u.y;
-                                }
-                                *at2 = v;
-                            }
+                    for (int i = 0; i < D / 8; ++i) {
+                        float2* to = reinterpret_cast<float2*>(merge + (set * 16 + b * 8 + quad) * (D + 4) + i * 8 +
+                                                               2 * pair);
+                        float2 v = make_float2(o[i][2 * b], o[i][2 * b + 1]);
+                        if (w > 0) {
+                            const float2 u = *to;
+                            v.x += u.x;
+                            v.y += u.y;
+                        }
+                        *to = v;
+                    }
             }
+            // (everyone has read the statistics by the first of these)
+            if (w == kKeyWarps - 1 && kw == 0 && pair == 0)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) stat[set * 16 + b * 8 + quad] = make_float2(big[b], sum[b]);
             named_bar_sync(1, kConsumers * 32);
         }
-        // statistics by row, then the rows: 16 bytes of output a thread
-        if (warp == 0 && pair == 0)
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) stat[a * 16 + b * 8 + quad] = make_float2(big[a][b], sum[a][b]);
-        named_bar_sync(1, kConsumers * 32);
+        // 16 bytes of output a thread
         const bool whole = walk.whole();
         float* part = p.part + ((int64_t)blockIdx.x * 2 + walk.part()) * attn_part_floats(kRows, D);
         for (int i = tid; i < walk.rows * (D / 8); i += kConsumers * 32) {
@@ -411,28 +379,25 @@ __device__ __forceinline__ void join(const AttnParams& p, const float* parts, in
         walk.done();
     }
     if (!spans || from >= walk.rows) return;
-    // its parts: CTA c's part 1, then part 0 of the CTAs up to its last unit
-    const int64_t end = at.end + (walk.tiles - walk.t1);
-    int n = 1;
-    for (int k = c + 1; k < p.G; ++k) {
-        const int64_t b = at.total * k / p.G, e = at.total * (k + 1) / p.G;
-        if (b >= end) break;
-        if (e > b) n = k - c + 1;
-    }
+    // its parts: CTA c's part 1, then part 0 of the CTAs up to that of its
+    // last unit u, the largest k with kU/G <= u
+    const int64_t u = at.end + (walk.tiles - walk.t1) - 1;
+    const int n = (int)(((u + 1) * at.ctas - 1) / at.total) - c + 1;
     constexpr int kFloats = attn_part_floats(ROWS, D);
-    auto part_of = [&](int k) { return parts + ((int64_t)(c + k) * 2 + (k == 0 ? 1 : 0)) * kFloats; };
-    auto empty = [&](int k) { return at.total * (c + k) / p.G >= at.total * (c + k + 1) / p.G; };
+    const float* first = parts + ((int64_t)c * 2 + 1) * kFloats;
+    const float* rest = parts + (int64_t)c * 2 * kFloats;  // part 0 of CTA c + k at k * 2 * kFloats
+    auto part_of = [&](int k) { return k == 0 ? first : rest + (int64_t)k * 2 * kFloats; };
     constexpr int kPer = D / 8;
     const int to = min(from + kAttnRows, walk.rows);
     for (int i = tid + from * kPer; i < to * kPer; i += 128) {
         const int row = i / kPer, d = (i % kPer) * 8;
         float mx = -INFINITY, sum = 0.f;
-        for (int k = 0; k < n; ++k)
-            if (!empty(k)) mx = fmaxf(mx, reinterpret_cast<const float2*>(part_of(k) + ROWS * D)[row].x);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) mx = fmaxf(mx, reinterpret_cast<const float2*>(part_of(k) + ROWS * D)[row].x);
         const float ref = mx == -INFINITY ? 0.f : mx;
         float v[8] = {};
+#pragma unroll 4
         for (int k = 0; k < n; ++k) {
-            if (empty(k)) continue;
             const float* f = part_of(k);
             const float2 ml = reinterpret_cast<const float2*>(f + ROWS * D)[row];
             const float w = exp2_approx(ml.x - ref);

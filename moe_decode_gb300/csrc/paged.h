@@ -39,7 +39,8 @@ struct AppendParams {
 
 constexpr int kSampleThreads = 512;
 constexpr int kSampleBins = 2048;
-constexpr int kSampleMaxSlice = 45056;  // logits of a row that one CTA holds
+constexpr int kSampleMaxSlice = 45056;   // logits of a row that one CTA holds
+constexpr int kSampleHalfSlice = 20480;  // and one of two CTAs of an SM
 
 struct SampleParams {
     const void* logits;

@@ -27,8 +27,9 @@ using u64 = unsigned long long;
 constexpr int kThreads = kSampleThreads;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kSampleBins;
-constexpr int kList = 1024;
+constexpr int kList = 128;
 constexpr int kMassBits = 42;
+static_assert(kList * 4 == kThreads, "four threads rank a member");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -79,10 +80,6 @@ struct Shared {
             uint16_t order[kList];
         } list;
     };
-    // sums over the cluster of the bins that this CTA owns (clusters of two
-    // or more; a single CTA's histogram is the sum)
-    u64 red_mass[kBins / 2];
-    uint32_t red_count[kBins / 2];
     u64 best[16];       // each CTA's largest logit and its index
     // each CTA's share of a cluster sum, in two sets used in turn: a CTA that
     // is a barrier ahead writes the other set than the one still being read
@@ -144,6 +141,14 @@ __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
+// Shared memory of a CTA: Shared, then the sums over the cluster of the bins
+// that the CTA owns (clusters of two or more; a single CTA's histogram is the
+// sum), then the slice.
+__host__ __device__ constexpr int owned_bins(int C) { return C > 1 ? kBins / C : 0; }
+__host__ __device__ constexpr int offset_sums() { return (int)((sizeof(Shared) + 15) & ~size_t(15)); }
+__host__ __device__ constexpr int offset_slice(int C) { return offset_sums() + owned_bins(C) * 12; }
+static_assert(offset_slice(16) % 16 == 0, "alignment of the slice");
+
 // The row's slice that this CTA holds, and the bound of the kept set so far:
 // codes up to `border`, of those equal to it the indices up to `tie`.
 struct Row {
@@ -167,6 +172,8 @@ template <bool BY_MASS>
 __device__ u64 narrow(Row& row, u64 target, bool with_mass, Shared& sh, uint32_t rank, int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int own = kBins / C;  // bins that this CTA sums
+    u64* red_mass = reinterpret_cast<u64*>(reinterpret_cast<uint8_t*>(&sh) + offset_sums());
+    uint32_t* red_count = reinterpret_cast<uint32_t*>(red_mass + own);
     u64 before = 0;             // mass of the codes before the group
     u64 prefix = 0;
     int shift = 64;
@@ -208,8 +215,8 @@ __device__ u64 narrow(Row& row, u64 target, bool with_mass, Shared& sh, uint32_t
                     c += ld_remote32(remote(&sh.hist.count[rank * own + i], r));
                     if (with_mass) m += ld_remote64(remote(&sh.hist.mass[rank * own + i], r));
                 }
-                sh.red_mass[i] = m;
-                sh.red_count[i] = c;
+                red_mass[i] = m;
+                red_count[i] = c;
                 pm += m;
                 pc += c;
             }
@@ -240,8 +247,8 @@ __device__ u64 narrow(Row& row, u64 target, bool with_mass, Shared& sh, uint32_t
                 skipped_count += sh.part_count[row.turn][q];
             }
             from = (uint32_t)(q * own);
-            mass_at = remote(sh.red_mass, q);
-            count_at = remote(sh.red_count, q);
+            mass_at = remote(red_mass, q);
+            count_at = remote(red_count, q);
         } else {
             __syncthreads();
         }
@@ -347,45 +354,43 @@ __device__ u64 narrow(Row& row, u64 target, bool with_mass, Shared& sh, uint32_t
             }
             cluster_sync();
             if (rank == 0) {
-                for (uint32_t i = tid; i < members; i += kThreads) {
-                    const u64 code = sh.list.code[i];
-                    const uint32_t index = sh.list.index[i];
+                // four threads count the members before one
+                {
+                    const uint32_t i = tid >> 2;
                     uint32_t place = 0;
-                    for (uint32_t j = 0; j < members; ++j) {
-                        const u64 other = sh.list.code[j];
-                        place += other < code || (other == code && sh.list.index[j] < index);
+                    if (i < members) {
+                        const u64 code = sh.list.code[i];
+                        const uint32_t index = sh.list.index[i];
+                        for (uint32_t j = tid & 3; j < members; j += 4) {
+                            const u64 other = sh.list.code[j];
+                            place += other < code || (other == code && sh.list.index[j] < index);
+                        }
                     }
-                    sh.list.order[place] = (uint16_t)i;
+                    place += __shfl_xor_sync(0xffffffffu, place, 1);
+                    place += __shfl_xor_sync(0xffffffffu, place, 2);
+                    if (i < members && (tid & 3) == 0) sh.list.order[place] = (uint16_t)i;
                 }
                 __syncthreads();
-                // mass up to each place, two places a thread
-                u64 a[2];
+                // mass up to each place
+                u64 own_mass = 0;
+                if (tid < kList) {
+                    own_mass = (uint32_t)tid < members ? sh.list.mass[sh.list.order[tid]] : 0;
+                    u64 sum = own_mass;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t i = 2 * tid + j;
-                    a[j] = i < members ? sh.list.mass[sh.list.order[i]] : 0;
-                }
-                u64 sum = a[0] + a[1];
-                const u64 mine = sum;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const u64 v = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o) sum += v;
-                }
-                if (lane == 31) sh.warp_mass[warp] = sum;
-                __syncthreads();
-                u64 b = sum - mine;
-                for (int w = 0; w < warp; ++w) b += sh.warp_mass[w];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t i = 2 * tid + j;
-                    const bool here = BY_MASS ? b < target && target <= b + a[j] : i + 1 == target;
-                    if (i < members && here) {
-                        sh.border = sh.list.code[sh.list.order[i]];
-                        sh.tie_limit = sh.list.index[sh.list.order[i]];
-                        sh.bin_mass = b + a[j];
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const u64 v = __shfl_up_sync(0xffffffffu, sum, o);
+                        if (lane >= o) sum += v;
                     }
-                    b += a[j];
+                    if (lane == 31) sh.warp_mass[warp] = sum;
+                    named_bar_sync(1, kList);
+                    u64 b = sum - own_mass;
+                    for (int w = 0; w < warp; ++w) b += sh.warp_mass[w];
+                    const bool here = BY_MASS ? b < target && target <= b + own_mass : (u64)tid + 1 == target;
+                    if ((uint32_t)tid < members && here) {
+                        sh.border = sh.list.code[sh.list.order[tid]];
+                        sh.tie_limit = sh.list.index[sh.list.order[tid]];
+                        sh.bin_mass = b + own_mass;
+                    }
                 }
             }
             cluster_sync();
@@ -445,7 +450,7 @@ template <int DT>
 __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared& sh = *reinterpret_cast<Shared*>(dyn);
-    float* xs = reinterpret_cast<float*>(dyn + ((sizeof(Shared) + 15) & ~size_t(15)));
+    float* xs = reinterpret_cast<float*>(dyn + offset_slice(p.C));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int C = p.C, m = blockIdx.x / C;
@@ -610,7 +615,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
 
 cudaError_t launch_sample(const SampleParams& p, int M, int dtype, cudaStream_t stream) {
     void (*kern)(SampleParams) = dtype == 0 ? sample_kernel<0> : sample_kernel<1>;
-    const int smem = (int)(((sizeof(Shared) + 15) & ~size_t(15)) + (size_t)p.slice * 4);
+    const int smem = offset_slice(p.C) + p.slice * 4;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess && p.C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
