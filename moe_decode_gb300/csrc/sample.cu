@@ -11,12 +11,18 @@
 //
 // One cluster a row: each CTA keeps its slice of the row in shared memory, so
 // the logits are read from HBM once. The kept set is a prefix of the order (l
-// descending, index ascending), encoded in 64 bits as (t in 2^-26 steps, the
-// bits of l reversed); top-k and top-p each look for the last member by a
-// histogram of 2048 bins of that code (count and mass), summed across the
-// cluster through distributed shared memory. The bin that holds the border is
-// split again, or, once it has at most kList members, gathered by the first
-// CTA and ranked directly.
+// descending, index ascending), encoded in 55 bits as (t in 2^-17 steps, the
+// bits of l reversed); top-k and top-p each look for its last member.
+//
+// First the search is bounded: the largest logits of the threads, one each,
+// are members too, so the bin in which k of them (or of their masses p of the
+// total) are reached cannot lie before the last member's. That histogram takes
+// one atomic a thread instead of one a logit, and nothing beyond its bin needs
+// more than a subtraction, a product and a comparison from then on. Where at
+// most kList members are left the first CTA ranks them; otherwise histograms
+// of 2048 bins of the code (count and mass, summed across the cluster through
+// distributed shared memory) narrow the last member's bin until it has so few,
+// or is one value, whose members count in index order.
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -78,6 +84,7 @@ struct Shared {
             u64 mass[kList];
             uint32_t index[kList];
             uint16_t order[kList];
+            u64 sums[kList];
         } list;
     };
     u64 best[16];       // each CTA's largest logit and its index
@@ -85,11 +92,14 @@ struct Shared {
     // is a barrier ahead writes the other set than the one still being read
     u64 part_mass[2][16];
     uint32_t part_count[2][16];
+    u64 part_all[2][16];
     u64 warp_mass[kWarps];
     u64 warp_count[kWarps];
+    u64 warp_all[kWarps];
     // what the search for a border found
     u64 before_mass, bin_mass, border;
-    uint32_t before_count, bin_count, bin, tie_limit;
+    u64 before_count;
+    uint32_t bin_count, bin, tie_limit;
     uint32_t listed;
 };
 
@@ -107,31 +117,58 @@ struct Scale {
     float hi, lo;   // log2(e) / T
 };
 
-// t in 2^-26 steps (0xffffffff from 64 on: no mass); monotone in x, since
-// each of the two roundings is.
-__device__ __forceinline__ uint32_t steps_below(float x, const Scale& s) {
-    const float d = x == s.top ? 0.f : s.top - x;
-    const float t = d * s.hi;
-    return d < 3.0e38f && t < 64.f ? (uint32_t)(t * 67108864.f) : 0xffffffffu;
+// A logit's place: t in 2^-17 steps, monotone in x, since each of its three
+// roundings is. From kNoPart on (t = 41, -inf, NaN) it has no part in the mass.
+constexpr uint32_t kStepBits = 23, kNoPart = 41u << 17;
+__device__ __forceinline__ uint32_t steps_of(float x, const Scale& s) {
+    const float d = x == s.top ? 0.f : s.top - x;  // also where both are +inf
+    return __float_as_uint(fmaf(d, s.hi, 64.f)) - 0x42800000u;
 }
-
-// w in units of 2^-42.
+// Its mass w in units of 2^-42, given that it has a part.
 __device__ __forceinline__ u64 mass_of(float x, const Scale& s) {
-    if (x == s.top) return 1ull << kMassBits;
-    const float d = s.top - x;
-    if (!(d < 3.0e38f)) return 0;
+    const bool same = x == s.top;
+    const float d = same ? 0.f : s.top - x;
     // the rounding error of the difference, then of the product
-    const float bb = d - s.top, err = (s.top - (d - bb)) - (x + bb);
+    const float bb = d - s.top, err = same ? 0.f : (s.top - (d - bb)) - (x + bb);
     const float th = d * s.hi;
-    if (!(th < 43.5f)) return 0;
     const float tl = fmaf(d, s.hi, -th) + fmaf(d, s.lo, err * s.hi);
-    const float n = rintf(th);
-    const float f = (th - n) + tl;
+    const float whole = th + 12582912.f;  // 1.5 * 2^23: rounds to a whole number n <= 41, in the low bits
+    const uint32_t n = __float_as_uint(whole) & 0x3fu;
+    const float f = (th - (whole - 12582912.f)) + tl;
     float e;
     asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-f));
-    const u64 mant = (u64)__float2uint_rn(e * 16777216.f);
-    const int sh = kMassBits - 24 - (int)n;
-    return sh >= 0 ? mant << sh : (mant + (1ull << (-sh - 1))) >> -sh;
+    // e = mant * 2^(exponent - 150), the exponent 126 or 127
+    const uint32_t b = __float_as_uint(e);
+    const u64 mant = (u64)((b & 0x7fffffu) | 0x800000u) << (kMassBits - 23);
+    return mant >> (n + 127u - (b >> 23));
+}
+
+// log2(e) / T as a sum of two fp32, without fp64 (two operations a clock and
+// SM here: a division by every thread cost 10 us a call).
+__device__ __forceinline__ void scale_of(float T, Scale& s) {
+    constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;  // their sum: log2(e) to 2^-48
+    s.hi = fminf(__fdiv_rn(kLog2e, T), 1e30f);
+    s.lo = s.hi < 1e30f ? __fdiv_rn(fmaf(-s.hi, T, kLog2e) + kLog2eRest, T) : 0.f;
+    if (!(fabsf(s.lo) < 1e30f)) s.lo = 0.f;  // T = inf
+}
+
+// floor(f * v), or the next whole number above f * v, for 0 <= f < 1: the 24
+// bits of f times v in 128 bits, shifted.
+__device__ __forceinline__ u64 share(float f, u64 v, bool up) {
+    const uint32_t b = __float_as_uint(f);
+    const int e = (int)(b >> 23);
+    const u64 mant = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
+    const int sh = 150 - (e ? e : 1);  // f = mant * 2^-sh, 24 <= sh < 150
+    const u64 lo = mant * v, hi = __umul64hi(mant, v);
+    u64 q, rest;
+    if (sh < 64) {
+        q = (hi << (64 - sh)) | (lo >> sh);
+        rest = lo << (64 - sh);
+    } else {
+        q = sh < 128 ? (sh == 64 ? hi : hi >> (sh - 64)) : 0;
+        rest = lo | (sh >= 128 ? hi : sh == 64 ? 0 : hi << (128 - sh));
+    }
+    return q + (up && rest ? 1 : 0);
 }
 
 template <class T>
@@ -149,292 +186,376 @@ __host__ __device__ constexpr int offset_sums() { return (int)((sizeof(Shared) +
 __host__ __device__ constexpr int offset_slice(int C) { return offset_sums() + owned_bins(C) * 12; }
 static_assert(offset_slice(16) % 16 == 0, "alignment of the slice");
 
-// The row's slice that this CTA holds, and the bound of the kept set so far:
-// codes up to `border`, of those equal to it the indices up to `tie`.
+// The row's slice that this CTA holds, and what bounds the kept set so far:
+// steps below `limit`, codes up to `border`, of those equal to it the indices
+// up to `tie`.
 struct Row {
     const float* x;
     int n, base;  // members and first index
     Scale scale;
+    uint32_t limit;
     u64 border;
     uint32_t tie;
     int turn;  // which set of cluster sums is next
 };
+constexpr int kCodeBits = kStepBits + 32;
 __device__ __forceinline__ u64 code_of(uint32_t steps, float x) { return ((u64)steps << 32) | (uint32_t)~value_bits(x); }
 __device__ __forceinline__ bool kept(const Row& r, u64 code, uint32_t index) {
     return code < r.border || (code == r.border && index <= r.tie);
 }
+// f(i, x, code) for each member of the row's slice in the kept set whose code
+// begins with `prefix` (bits from `shift` up).
+template <class F>
+__device__ __forceinline__ void each_member(const Row& row, u64 prefix, int shift, F f) {
+    for (int i0 = threadIdx.x; i0 < row.n; i0 += 4 * kThreads) {
+        float x[4];
+        uint32_t steps[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = i0 + j * kThreads < row.n ? row.x[i0 + j * kThreads] : -INFINITY;
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            steps[j] = steps_of(x[j], row.scale);
+            any |= steps[j] < row.limit;
+        }
+        if (!any) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const u64 code = code_of(steps[j], x[j]);
+            const int i = i0 + j * kThreads;
+            if (steps[j] < row.limit && (code >> shift) == prefix && kept(row, code, row.base + i)) f(i, x[j], code);
+        }
+    }
+}
 
-// Narrows row.border to the last member of the kept set's shortest prefix
-// whose count (BY_MASS false) or mass (true) reaches `target`; the set stays
-// as it is where all of it does not. Returns the kept set's mass then
-// (WITH_MASS: also kept by count searches).
-template <bool BY_MASS>
-__device__ u64 narrow(Row& row, u64 target, bool with_mass, Shared& sh, uint32_t rank, int C) {
+struct Found {
+    uint32_t members;  // of the bin in which the target is reached (0: it is not)
+    uint32_t bin;
+    u64 bin_mass, before_mass;
+    u64 before_count;
+    u64 all;  // sum of the threads' `own`
+};
+
+// The bin of the cluster's histogram in which the count, or the mass, reaches
+// the target; a mass target of 0 stands for `part` of the sum of `own`.
+__device__ __forceinline__ Found locate(Row& row, bool by_mass, bool with_mass, u64& target, float part, u64 own,
+                                        Shared& sh, uint32_t rank, int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int own = kBins / C;  // bins that this CTA sums
+    const int bins = kBins / C;  // that this CTA sums
     u64* red_mass = reinterpret_cast<u64*>(reinterpret_cast<uint8_t*>(&sh) + offset_sums());
-    uint32_t* red_count = reinterpret_cast<uint32_t*>(red_mass + own);
-    u64 before = 0;             // mass of the codes before the group
-    u64 prefix = 0;
-    int shift = 64;
-    for (int level = 0; level < 6; ++level) {
-        const int width = level == 2 || level == 5 ? 10 : 11, low = shift - width;
-        for (int i = tid; i < kBins; i += kThreads) {
-            sh.hist.mass[i] = 0;
-            sh.hist.count[i] = 0;
-        }
-        if (tid == 0) sh.listed = 0;
-        __syncthreads();
-        for (int i = tid; i < row.n; i += kThreads) {
-            const float x = row.x[i];
-            const uint32_t steps = steps_below(x, row.scale);
-            if (steps == 0xffffffffu) continue;
-            const u64 code = code_of(steps, x);
-            if (level && (code >> shift) != prefix) continue;
-            if (!kept(row, code, row.base + i)) continue;
-            const u64 w = mass_of(x, row.scale);
-            if (w == 0) continue;
-            const uint32_t bin = (uint32_t)(code >> low) & ((1u << width) - 1u);
-            atomicAdd(&sh.hist.count[bin], 1u);
-            if (with_mass) atomicAdd(&sh.hist.mass[bin], w);
-        }
-        const u64* mass = sh.hist.mass;
-        const uint32_t* count = sh.hist.count;
-        uint32_t from = 0;
-        u64 skipped_mass = 0;
-        u64 skipped_count = 0;
-        uint32_t mass_at = 0, count_at = 0;
+    uint32_t* red_count = reinterpret_cast<uint32_t*>(red_mass + bins);
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    u64 pm = 0, pc = 0;
+    for (int i = tid; i < bins; i += kThreads) {
+        u64 m = 0;
+        uint32_t c = 0;
         if (C > 1) {
-            cluster_sync();
-            u64 pm = 0;
-            u64 pc = 0;
-            for (int i = tid; i < own; i += kThreads) {
-                u64 m = 0;
-                uint32_t c = 0;
-                for (int r = 0; r < C; ++r) {
-                    c += ld_remote32(remote(&sh.hist.count[rank * own + i], r));
-                    if (with_mass) m += ld_remote64(remote(&sh.hist.mass[rank * own + i], r));
-                }
-                red_mass[i] = m;
-                red_count[i] = c;
-                pm += m;
-                pc += c;
+            for (int r = 0; r < C; ++r) {
+                c += ld_remote32(remote(&sh.hist.count[rank * bins + i], r));
+                if (with_mass) m += ld_remote64(remote(&sh.hist.mass[rank * bins + i], r));
             }
-            pm = warp_sum(pm);
-            pc = warp_sum(pc);
-            if (lane == 0) {
-                sh.warp_mass[warp] = pm;
-                sh.warp_count[warp] = pc;
-            }
-            __syncthreads();
-            row.turn ^= 1;
-            if (tid < C) {
-                u64 m = 0, c = 0;
-                for (int w = 0; w < kWarps; ++w) {
-                    m += sh.warp_mass[w];
-                    c += sh.warp_count[w];
-                }
-                st_remote64(remote(&sh.part_mass[row.turn][rank], tid), m);
-                st_remote32(remote(&sh.part_count[row.turn][rank], tid), (uint32_t)c);
-            }
-            cluster_sync();
-            // the CTA whose bins hold the border
-            int q = 0;
-            for (; q < C - 1; ++q) {
-                const u64 reach = BY_MASS ? skipped_mass + sh.part_mass[row.turn][q] : skipped_count + sh.part_count[row.turn][q];
-                if (reach >= target) break;
-                skipped_mass += sh.part_mass[row.turn][q];
-                skipped_count += sh.part_count[row.turn][q];
-            }
-            from = (uint32_t)(q * own);
-            mass_at = remote(red_mass, q);
-            count_at = remote(red_count, q);
+            red_mass[i] = m;
+            red_count[i] = c;
         } else {
-            __syncthreads();
+            c = sh.hist.count[i];
+            m = sh.hist.mass[i];
         }
-        // the bin: each thread sums `per` of the owner's bins, a scan finds
-        // the thread, the thread the bin
-        const int per = (own + kThreads - 1) / kThreads;
-        u64 m[4], sm = 0;
-        uint32_t c[4];
-        u64 sc = 0;
+        pm += m;
+        pc += c;
+    }
+    pm = warp_sum(pm);
+    pc = warp_sum(pc);
+    own = warp_sum(own);
+    if (lane == 0) {
+        sh.warp_mass[warp] = pm;
+        sh.warp_count[warp] = pc;
+        sh.warp_all[warp] = own;
+    }
+    if (tid == 0) sh.bin_count = 0;
+    __syncthreads();
+    row.turn ^= 1;
+    if (tid < C) {
+        u64 m = 0, c = 0, a = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            m += sh.warp_mass[w];
+            c += sh.warp_count[w];
+            a += sh.warp_all[w];
+        }
+        st_remote64(remote(&sh.part_mass[row.turn][rank], tid), m);
+        st_remote32(remote(&sh.part_count[row.turn][rank], tid), (uint32_t)c);
+        st_remote64(remote(&sh.part_all[row.turn][rank], tid), a);
+    }
+    cluster_sync();
+    Found found;
+    found.all = 0;
+    for (int r = 0; r < C; ++r) found.all += sh.part_all[row.turn][r];
+    if (by_mass && target == 0) {
+        target = part > 0.f ? share(part, found.all, true) : 0;
+        target = target > 1 ? target : 1;
+    }
+    // the CTA whose bins hold it
+    int q = 0;
+    u64 bm = 0, bc = 0;
+    for (; q < C - 1; ++q) {
+        const u64 m = sh.part_mass[row.turn][q], c = sh.part_count[row.turn][q];
+        if ((by_mass ? bm + m : bc + c) >= target) break;
+        bm += m;
+        bc += c;
+    }
+    // the bin: each thread sums `per` of that CTA's bins, a scan finds the
+    // thread, the thread the bin
+    const uint32_t mass_at = C > 1 ? remote(red_mass, q) : smem_u32(sh.hist.mass);
+    const uint32_t count_at = C > 1 ? remote(red_count, q) : smem_u32(sh.hist.count);
+    const int per = (bins + kThreads - 1) / kThreads;
+    u64 sm = 0, sc = 0;
+    for (int j = 0; j < per; ++j) {
+        const int i = tid * per + j;
+        if (i < bins) {
+            sc += ld_remote32(count_at + 4u * i);
+            if (with_mass) sm += ld_remote64(mass_at + 8u * i);
+        }
+    }
+    u64 im = sm, ic = sc;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 a = __shfl_up_sync(0xffffffffu, im, o), b = __shfl_up_sync(0xffffffffu, ic, o);
+        if (lane >= o) {
+            im += a;
+            ic += b;
+        }
+    }
+    if (lane == 31) {
+        sh.warp_mass[warp] = im;
+        sh.warp_count[warp] = ic;
+    }
+    __syncthreads();
+    bm += im - sm;
+    bc += ic - sc;
+    for (int w = 0; w < warp; ++w) {
+        bm += sh.warp_mass[w];
+        bc += sh.warp_count[w];
+    }
+    if (sc && (by_mass ? bm < target && target <= bm + sm : bc < target && target <= bc + sc)) {
+        for (int j = 0; j < per; ++j) {
             const int i = tid * per + j;
-            m[j] = 0;
-            c[j] = 0;
-            if (j < per && i < own) {
-                if (C > 1) {
-                    c[j] = ld_remote32(count_at + 4u * i);
-                    if (with_mass) m[j] = ld_remote64(mass_at + 8u * i);
-                } else {
-                    c[j] = count[i];
-                    if (with_mass) m[j] = mass[i];
-                }
-            }
-            sm += m[j];
-            sc += c[j];
-        }
-        u64 im = sm, ic = sc;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 a = __shfl_up_sync(0xffffffffu, im, o), b = __shfl_up_sync(0xffffffffu, ic, o);
-            if (lane >= o) {
-                im += a;
-                ic += b;
-            }
-        }
-        if (tid == 0) sh.bin_count = 0;
-        __syncthreads();  // also: warp_mass was read
-        if (lane == 31) {
-            sh.warp_mass[warp] = im;
-            sh.warp_count[warp] = ic;
-        }
-        __syncthreads();
-        u64 bm = skipped_mass + im - sm, bc = skipped_count + ic - sc;
-        for (int w = 0; w < warp; ++w) {
-            bm += sh.warp_mass[w];
-            bc += sh.warp_count[w];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const u64 b = BY_MASS ? bm : bc, e = b + (BY_MASS ? m[j] : c[j]);
-            if (c[j] && b < target && target <= e) {
-                sh.bin = from + tid * per + j;
+            const uint32_t c = ld_remote32(count_at + 4u * i);
+            const u64 m = with_mass ? ld_remote64(mass_at + 8u * i) : 0;
+            if (c && (by_mass ? bm + m : bc + c) >= target) {
+                sh.bin = q * bins + i;
+                sh.bin_mass = m;
+                sh.bin_count = c;
                 sh.before_mass = bm;
-                sh.before_count = (uint32_t)bc;
-                sh.bin_mass = m[j];
-                sh.bin_count = c[j];
+                sh.before_count = bc;
+                break;
             }
-            bm += m[j];
-            bc += c[j];
+            bm += m;
+            bc += c;
+        }
+    }
+    __syncthreads();
+    found.members = sh.bin_count;
+    found.bin = sh.bin;
+    found.bin_mass = sh.bin_mass;
+    found.before_mass = sh.before_mass;
+    found.before_count = sh.before_count;
+    return found;
+}
+
+// Gathers the members that begin with `prefix` in the first CTA, which ranks
+// them and finds the last one that is kept: the count-th (0: the last of all)
+// and, with by_mass, the first up to which the mass reaches `goal`, or where
+// that is 0 `part` of the mass up to the count-th. False when there are more
+// than kList. `mass` receives their mass up to the border.
+__device__ __forceinline__ bool settle(Row& row, u64 prefix, int shift, u64 count, bool by_mass, u64 goal, float part,
+                                       u64& mass, Shared& sh, uint32_t rank, int C) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    each_member(row, prefix, shift, [&](int i, float x, u64 code) {
+        const uint32_t at = atom_add_remote32(remote(&sh.listed, 0), 1u);
+        if (at < kList) {
+            st_remote64(remote(&sh.list.code[at], 0), code);
+            st_remote64(remote(&sh.list.mass[at], 0), mass_of(x, row.scale));
+            st_remote32(remote(&sh.list.index[at], 0), row.base + i);
+        }
+    });
+    cluster_sync();
+    const uint32_t members = ld_remote32(remote(&sh.listed, 0));
+    const bool fits = members <= kList;
+    if (rank == 0 && fits) {
+        // four threads count the members before one
+        {
+            const uint32_t i = tid >> 2;
+            uint32_t place = 0;
+            if (i < members) {
+                const u64 code = sh.list.code[i];
+                const uint32_t index = sh.list.index[i];
+                for (uint32_t j = tid & 3; j < members; j += 4) {
+                    const u64 other = sh.list.code[j];
+                    place += other < code || (other == code && sh.list.index[j] < index);
+                }
+            }
+            place += __shfl_xor_sync(0xffffffffu, place, 1);
+            place += __shfl_xor_sync(0xffffffffu, place, 2);
+            if (i < members && (tid & 3) == 0) sh.list.order[place] = (uint16_t)i;
         }
         __syncthreads();
-        const uint32_t members = sh.bin_count;
-        if (members == 0) {  // all of the set does not reach the target (level 0 only)
-            u64 total = 0;
-            if (C > 1)
-                for (int r = 0; r < C; ++r) total += sh.part_mass[row.turn][r];
-            else
-                for (int w = 0; w < kWarps; ++w) total += sh.warp_mass[w];
-            __syncthreads();
-            return total;
-        }
-        const uint32_t bin = sh.bin;
-        const u64 bin_mass = sh.bin_mass, below = before + sh.before_mass;
-        target -= BY_MASS ? sh.before_mass : sh.before_count;
-        prefix = (prefix << width) | bin;
-        shift = low;
-        before = below;
-        // all of the bin is kept
-        if (BY_MASS ? members == 1 : target == members) {
-            const u64 bound = shift == 0 ? prefix : (prefix << shift) | ((1ull << shift) - 1ull);
-            if (bound < row.border) {
-                row.border = bound;
-                row.tie = 0xffffffffu;
-            }
-            __syncthreads();
-            return before + bin_mass;
-        }
-        if (members <= kList) {
-            // gather the bin's members in the first CTA and rank them
-            __syncthreads();
-            for (int i = tid; i < row.n; i += kThreads) {
-                const float x = row.x[i];
-                const uint32_t steps = steps_below(x, row.scale);
-                if (steps == 0xffffffffu) continue;
-                const u64 code = code_of(steps, x);
-                if ((code >> shift) != prefix || !kept(row, code, row.base + i)) continue;
-                const u64 w = mass_of(x, row.scale);
-                if (w == 0) continue;
-                const uint32_t at = atom_add_remote32(remote(&sh.listed, 0), 1u);
-                st_remote64(remote(&sh.list.code[at], 0), code);
-                st_remote64(remote(&sh.list.mass[at], 0), w);
-                st_remote32(remote(&sh.list.index[at], 0), row.base + i);
-            }
-            cluster_sync();
-            if (rank == 0) {
-                // four threads count the members before one
-                {
-                    const uint32_t i = tid >> 2;
-                    uint32_t place = 0;
-                    if (i < members) {
-                        const u64 code = sh.list.code[i];
-                        const uint32_t index = sh.list.index[i];
-                        for (uint32_t j = tid & 3; j < members; j += 4) {
-                            const u64 other = sh.list.code[j];
-                            place += other < code || (other == code && sh.list.index[j] < index);
-                        }
-                    }
-                    place += __shfl_xor_sync(0xffffffffu, place, 1);
-                    place += __shfl_xor_sync(0xffffffffu, place, 2);
-                    if (i < members && (tid & 3) == 0) sh.list.order[place] = (uint16_t)i;
-                }
-                __syncthreads();
-                // mass up to each place
-                u64 own_mass = 0;
-                if (tid < kList) {
-                    own_mass = (uint32_t)tid < members ? sh.list.mass[sh.list.order[tid]] : 0;
-                    u64 sum = own_mass;
+        // mass up to each place
+        if (tid < kList) {
+            const u64 own = (uint32_t)tid < members ? sh.list.mass[sh.list.order[tid]] : 0;
+            u64 upto = own;
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const u64 v = __shfl_up_sync(0xffffffffu, sum, o);
-                        if (lane >= o) sum += v;
-                    }
-                    if (lane == 31) sh.warp_mass[warp] = sum;
-                    named_bar_sync(1, kList);
-                    u64 b = sum - own_mass;
-                    for (int w = 0; w < warp; ++w) b += sh.warp_mass[w];
-                    const bool here = BY_MASS ? b < target && target <= b + own_mass : (u64)tid + 1 == target;
-                    if ((uint32_t)tid < members && here) {
-                        sh.border = sh.list.code[sh.list.order[tid]];
-                        sh.tie_limit = sh.list.index[sh.list.order[tid]];
-                        sh.bin_mass = b + own_mass;
-                    }
-                }
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
             }
-            cluster_sync();
-            row.border = ld_remote64(remote(&sh.border, 0));
-            row.tie = ld_remote32(remote(&sh.tie_limit, 0));
-            const u64 in_bin = ld_remote64(remote(&sh.bin_mass, 0));
-            cluster_sync();
-            return before + in_bin;
-        }
-    }
-    // more than kList members of one value: all of one mass, in index order
-    const u64 each = sh.bin_mass / sh.bin_count;
-    const u64 need = BY_MASS ? (target + each - 1) / each : target;
-    uint32_t mine = sh.hist.count[sh.bin], lower = 0;
-    for (uint32_t r = 0; r < rank; ++r) lower += ld_remote32(remote(&sh.hist.count[sh.bin], r));
-    if (lower < need && need <= (u64)lower + mine) {
-        // warp by warp in index order
-        const int chunk = ((row.n + kWarps - 1) / kWarps + 31) / 32 * 32;
-        const int i0 = warp * chunk, i1 = min(i0 + chunk, row.n);
-        auto tied = [&](int i) {
-            if (i >= i1) return false;
-            const uint32_t steps = steps_below(row.x[i], row.scale);
-            const u64 code = code_of(steps, row.x[i]);
-            return code == prefix && kept(row, code, row.base + i);
-        };
-        uint32_t n = 0;
-        for (int i = i0; i < i1; i += 32) n += __popc(__ballot_sync(0xffffffffu, tied(i + lane)));
-        if (lane == 0) sh.warp_count[warp] = n;
-        __syncthreads();
-        u64 at = lower;
-        for (int w = 0; w < warp; ++w) at += sh.warp_count[w];
-        for (int i = i0; i < i1; i += 32) {
-            const uint32_t set = __ballot_sync(0xffffffffu, tied(i + lane));
-            const u64 place = at + __popc(set & ((2u << lane) - 1u));
-            if (((set >> lane) & 1u) && place == need)
-                for (int r = 0; r < C; ++r) st_remote32(remote(&sh.tie_limit, r), row.base + i + lane);
-            at += __popc(set);
+            if (lane == 31) sh.warp_mass[warp] = upto;
+            named_bar_sync(1, kList);
+            for (int w = 0; w < warp; ++w) upto += sh.warp_mass[w];
+            sh.list.sums[tid] = upto;
+            named_bar_sync(1, kList);
+            const uint32_t last = (count ? (uint32_t)min(count, (u64)members) : members) - 1;
+            if (by_mass && goal == 0) {
+                goal = part > 0.f ? share(part, sh.list.sums[last], true) : 0;
+                goal = goal > 1 ? goal : 1;
+            }
+            const bool here = by_mass && goal <= sh.list.sums[last] ? upto - own < goal && goal <= upto : tid == (int)last;
+            if ((uint32_t)tid < members && here) {
+                sh.border = sh.list.code[sh.list.order[tid]];
+                sh.tie_limit = sh.list.index[sh.list.order[tid]];
+                sh.bin_mass = upto;
+            }
         }
     }
     cluster_sync();
-    row.border = prefix;
-    row.tie = sh.tie_limit;
-    cluster_sync();
-    return before + need * each;
+    if (fits) {
+        row.border = ld_remote64(remote(&sh.border, 0));
+        row.tie = ld_remote32(remote(&sh.tie_limit, 0));
+        mass = ld_remote64(remote(&sh.bin_mass, 0));
+        row.limit = min(row.limit, (uint32_t)(row.border >> 32) + 1);
+        cluster_sync();
+    }
+    return fits;
+}
+
+// Narrows the row to its first k members (k > 0), and of those to the shortest
+// run that reaches `part` of their mass (by_p). `top` is the thread's largest
+// logit.
+__device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, float top, Shared& sh, uint32_t rank,
+                                       int C) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    bool bounded = false;
+    u64 total = 0;  // mass of the first k, once known
+    for (int stage = k > 0 ? 0 : 1; stage < (by_p ? 2 : 1); ++stage) {
+        const bool by_mass = stage == 1;
+        u64 target = by_mass ? 0 : (u64)k;
+        if (by_mass && total) {
+            target = part > 0.f ? share(part, total, true) : 0;
+            target = target > 1 ? target : 1;
+        }
+        u64 before = 0, prefix = 0, in_bin = 0;
+        uint32_t members = 0, bin = 0;
+        int shift = kCodeBits;
+        bool done = false;
+        for (int level = bounded ? 0 : -1; level < 5 && !done; ++level) {
+            for (int i = tid; i < kBins; i += kThreads) {
+                sh.hist.mass[i] = 0;
+                sh.hist.count[i] = 0;
+            }
+            if (tid == 0) sh.listed = 0;
+            __syncthreads();
+            const int low = level < 0 ? kCodeBits - 11 : shift - 11;
+            const bool with_mass = by_mass || (by_p && level >= 0);
+            auto enter = [&](int, float x, u64 code) {
+                const uint32_t at = (uint32_t)(code >> low) & (kBins - 1u);
+                atomicAdd(&sh.hist.count[at], 1u);
+                if (with_mass) atomicAdd(&sh.hist.mass[at], mass_of(x, row.scale));
+            };
+            u64 own = 0;
+            if (level < 0) {
+                const uint32_t steps = steps_of(top, row.scale);
+                if (steps < row.limit) enter(0, top, code_of(steps, top));
+                if (by_mass) each_member(row, 0, kCodeBits, [&](int, float x, u64) { own += mass_of(x, row.scale); });
+            } else {
+                each_member(row, prefix, shift, enter);
+            }
+            const Found f = locate(row, by_mass, with_mass, target, part, own, sh, rank, C);
+            if (level < 0) {
+                bounded = true;
+                if (f.members == 0) continue;
+                row.limit = min(row.limit, (f.bin + 1) << (kStepBits - 11));
+                // the members are the first of all: both searches at once
+                done = settle(row, 0, kCodeBits, k > 0 ? (u64)k : 0, by_p, by_mass ? target : 0, part, total, sh, rank, C);
+                if (done) return;
+                continue;
+            }
+            if (f.members == 0) {  // the set does not reach the target (first level only): all of it is kept
+                done = true;
+                if (!by_mass) {
+                    total = 0;
+                    for (int r = 0; r < C; ++r) total += sh.part_mass[row.turn][r];
+                }
+                continue;
+            }
+            target -= by_mass ? f.before_mass : f.before_count;
+            prefix = (prefix << 11) | f.bin;
+            shift = low;
+            before += f.before_mass;
+            members = f.members;
+            bin = f.bin;
+            in_bin = f.bin_mass;
+            if (by_mass ? members == 1 : target == members) {  // all of the bin is kept
+                const u64 bound = shift == 0 ? prefix : (prefix << shift) | ((1ull << shift) - 1ull);
+                if (bound < row.border) {
+                    row.border = bound;
+                    row.tie = 0xffffffffu;
+                    row.limit = min(row.limit, (uint32_t)(bound >> 32) + 1);
+                }
+                total = before + in_bin;
+                done = true;
+            } else if (members <= kList) {
+                u64 mass;
+                settle(row, prefix, shift, by_mass ? 0 : target, by_mass, target, part, mass, sh, rank, C);
+                total = before + mass;
+                done = true;
+            }
+        }
+        if (done) continue;
+        // more than kList members of one value: all of one mass, in index order
+        const u64 each = mass_of(bits_value(~(uint32_t)prefix), row.scale);
+        const u64 need = by_mass ? (target + each - 1) / each : target;
+        const uint32_t mine = sh.hist.count[bin];
+        uint32_t lower = 0;
+        for (uint32_t r = 0; r < rank; ++r) lower += ld_remote32(remote(&sh.hist.count[bin], r));
+        if (lower < need && need <= (u64)lower + mine) {
+            // warp by warp in index order
+            const int chunk = ((row.n + kWarps - 1) / kWarps + 31) / 32 * 32;
+            const int i0 = warp * chunk, i1 = min(i0 + chunk, row.n);
+            auto tied = [&](int i) {
+                if (i >= i1) return false;
+                const u64 code = code_of(steps_of(row.x[i], row.scale), row.x[i]);
+                return code == prefix && kept(row, code, row.base + i);
+            };
+            uint32_t n = 0;
+            for (int i = i0; i < i1; i += 32) n += __popc(__ballot_sync(0xffffffffu, tied(i + lane)));
+            if (lane == 0) sh.warp_count[warp] = n;
+            __syncthreads();
+            u64 at = lower;
+            for (int w = 0; w < warp; ++w) at += sh.warp_count[w];
+            for (int i = i0; i < i1; i += 32) {
+                const uint32_t set = __ballot_sync(0xffffffffu, tied(i + lane));
+                const u64 place = at + __popc(set & ((2u << lane) - 1u));
+                if (((set >> lane) & 1u) && place == need)
+                    for (int r = 0; r < C; ++r) st_remote32(remote(&sh.tie_limit, r), row.base + i + lane);
+                at += __popc(set);
+            }
+        }
+        cluster_sync();
+        row.border = prefix;
+        row.tie = sh.tie_limit;
+        row.limit = min(row.limit, (uint32_t)(prefix >> 32) + 1);
+        total = before + need * each;
+        cluster_sync();
+    }
 }
 
 template <int DT>
@@ -447,7 +568,7 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
+__global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared& sh = *reinterpret_cast<Shared*>(dyn);
     float* xs = reinterpret_cast<float*>(dyn + offset_slice(p.C));
@@ -463,6 +584,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
     row.x = xs;
     row.border = ~0ull;
     row.tie = 0xffffffffu;
+    row.limit = kNoPart;
     row.turn = 0;
     // the slice into shared memory; its largest logit, lowest index first
     const int64_t start = (int64_t)m * p.row_stride + row.base;
@@ -498,6 +620,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
         }
     }
     for (int i = nv * kVec + tid; i < row.n; i += kThreads) see(clean(load_logit<DT>(src, i)), i);
+    const float own_top = best ? bits_value((uint32_t)(best >> 32)) : -INFINITY;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const u64 other = __shfl_xor_sync(0xffffffffu, best, o);
@@ -523,64 +646,45 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
         }
         return;  // no CTA reads another's memory after the last barrier
     }
-    const double c = fmin(1.4426950408889634 / (double)T, 1e30);
-    row.scale.hi = (float)c;
-    row.scale.lo = (float)(c - (double)row.scale.hi);
+    scale_of(T, row.scale);
 
     const float top_p = p.top_p ? p.top_p[m] : 1.f;
     const bool by_p = top_p < 1.f;
-    u64 total = 0;
-    bool known = false;
-    if (k > 0 && k < p.V) {
-        total = narrow<false>(row, (u64)k, by_p, sh, rank, C);
-        known = true;
-    }
-    if (by_p) {
-        if (!known) {
-            // the mass of everything
-            u64 w = 0;
-            for (int i = tid; i < row.n; i += kThreads) w += mass_of(xs[i], row.scale);
-            w = warp_sum(w);
-            if (lane == 0) sh.warp_mass[warp] = w;
-            __syncthreads();
-            row.turn ^= 1;
-            if (tid < C) {
-                u64 s = 0;
-                for (int i = 0; i < kWarps; ++i) s += sh.warp_mass[i];
-                st_remote64(remote(&sh.part_mass[row.turn][rank], tid), s);
-            }
-            cluster_sync();
-            for (int r = 0; r < C; ++r) total += sh.part_mass[row.turn][r];
-        }
-        const double want = ceil((double)top_p * (double)total);
-        narrow<true>(row, want >= 1.0 ? (u64)want : 1ull, true, sh, rank, C);
-    }
+    if ((k > 0 && k < p.V) || by_p) narrow(row, k < p.V ? max(k, 0) : 0, by_p, top_p, own_top, sh, rank, C);
 
-    // the kept mass in index order: CTA by CTA, warp by warp
+    // The kept mass in index order: each thread takes consecutive logits, an
+    // odd number of them so that a warp's 32 lie in 32 banks.
     const float min_p = p.min_p ? fminf(p.min_p[m], 1.f) : 0.f;
-    const u64 least = min_p > 0.f ? (u64)ceil((double)min_p * (double)(1ull << kMassBits)) : 0ull;
-    const uint32_t last_step = (uint32_t)(row.border >> 32);
+    const u64 least = min_p > 0.f ? __float2ull_ru(min_p * (float)(1ull << kMassBits)) : 0ull;
     auto mass_at = [&](int i) -> u64 {
         const float x = xs[i];
-        const uint32_t steps = steps_below(x, row.scale);
-        if (steps > last_step || steps == 0xffffffffu) return 0;
-        if (steps == last_step && !kept(row, code_of(steps, x), row.base + i)) return 0;
+        const uint32_t steps = steps_of(x, row.scale);
+        if (steps >= row.limit || !kept(row, code_of(steps, x), row.base + i)) return 0;
         const u64 w = mass_of(x, row.scale);
         return w >= least ? w : 0;
     };
-    const int chunk = ((row.n + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int i0 = warp * chunk, i1 = min(i0 + chunk, row.n);
-    u64 w = 0;
-    for (int i = i0 + lane; i < i1; i += 32) w += mass_at(i);
-    w = warp_sum(w);
+    const int len = ((row.n + kThreads - 1) / kThreads) | 1;
+    const int i0 = min(tid * len, row.n), i1 = min(i0 + len, row.n);
+    u64 own = 0;
+    {
+        int i = i0;
+        for (; i + 4 <= i1; i += 4) own += (mass_at(i) + mass_at(i + 1)) + (mass_at(i + 2) + mass_at(i + 3));
+        for (; i < i1; ++i) own += mass_at(i);
+    }
+    u64 upto = own;  // of the warp's threads up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
     __syncthreads();
-    if (lane == 0) sh.warp_mass[warp] = w;
+    if (lane == 31) sh.warp_mass[warp] = upto;
     __syncthreads();
     row.turn ^= 1;
     if (tid < C) {
-        u64 s = 0;
-        for (int i = 0; i < kWarps; ++i) s += sh.warp_mass[i];
-        st_remote64(remote(&sh.part_mass[row.turn][rank], tid), s);
+        u64 sum = 0;
+        for (int i = 0; i < kWarps; ++i) sum += sh.warp_mass[i];
+        st_remote64(remote(&sh.part_mass[row.turn][rank], tid), sum);
     }
     cluster_sync();
     u64 before = 0, all = 0;
@@ -590,21 +694,26 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
     }
     for (int i = 0; i < warp; ++i) before += sh.warp_mass[i];
     const float u = p.u[m];
-    u64 goal = u > 0.f ? (u64)((double)u * (double)all) : 0ull;
-    if (!(u < 1.f) || goal >= all) goal = u > 0.f ? all - 1 : 0ull;
-    if (before > goal || goal >= before + w) return;
-    // this warp's chunk holds the token: the first with cdf > goal
-    for (int i = i0; i < i1; i += 32) {
-        const u64 own = i + lane < i1 ? mass_at(i + lane) : 0ull;
-        u64 sum = own;
+    const u64 goal = !(u > 0.f) ? 0ull : u < 1.f ? share(u, all, false) : all - 1;
+    // the thread whose logits hold the first cumulated mass above the goal,
+    // then its warp over those logits
+    before += upto - own;
+    const uint32_t holder = __ballot_sync(0xffffffffu, before <= goal && goal < before + own);
+    if (holder == 0) return;
+    const int who = __ffs(holder) - 1;
+    before = __shfl_sync(0xffffffffu, before, who);
+    const int from = __shfl_sync(0xffffffffu, i0, who), to = __shfl_sync(0xffffffffu, i1, who);
+    for (int i = from; i < to; i += 32) {
+        const u64 one = i + lane < to ? mass_at(i + lane) : 0ull;
+        u64 sum = one;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const u64 v = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += v;
         }
-        if (before + sum - own <= goal && goal < before + sum) {
+        if (before + sum - one <= goal && goal < before + sum) {
             p.token[m] = row.base + i + lane;
-            if (p.prob) p.prob[m] = (float)((double)own / (double)all);
+            if (p.prob) p.prob[m] = __fdiv_rn(__ull2float_rn(one), __ull2float_rn(all));
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
         if (before > goal) break;
