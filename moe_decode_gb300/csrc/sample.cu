@@ -14,15 +14,22 @@
 // descending, index ascending), encoded in 55 bits as (t in 2^-17 steps, the
 // bits of l reversed); top-k and top-p each look for its last member.
 //
-// First the search is bounded: the largest logits of the threads, one each,
-// are members too, so the bin in which k of them (or of their masses p of the
-// total) are reached cannot lie before the last member's. That histogram takes
-// one atomic a thread instead of one a logit, and nothing beyond its bin needs
-// more than a subtraction, a product and a comparison from then on. Where at
-// most kList members are left the first CTA ranks them; otherwise histograms
-// of 2048 bins of the code (count and mass, summed across the cluster through
-// distributed shared memory) narrow the last member's bin until it has so few,
-// or is one value, whose members count in index order.
+// Top-k. The largest logits of the threads, one each, are members too, so the
+// bin in which k of them are reached cannot lie before the last member's: a
+// histogram (2048 bins of the code, summed across the cluster through
+// distributed shared memory) that takes one atomic a thread, not one a logit.
+// Nothing beyond its bin needs more than a subtraction, a product and a
+// comparison from then on. Where at most kList members are left the first CTA
+// ranks them, with top-p at once.
+//
+// Top-p otherwise. One sweep sums the masses and counts the members of each
+// bin; a bin's masses differ by 2% at most, so the counts bound the border to
+// a few bins. A second sweep sums the masses before those exactly, and the
+// histogram (count and mass) of those alone, in 2048 parts.
+//
+// Either way the last member's bin is split again until it has at most kList
+// members, which are ranked, or is one value, whose members count in index
+// order.
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -90,16 +97,11 @@ struct Shared {
     u64 best[16];       // each CTA's largest logit and its index
     // each CTA's share of a cluster sum, in two sets used in turn: a CTA that
     // is a barrier ahead writes the other set than the one still being read
-    u64 part_mass[2][16];
-    uint32_t part_count[2][16];
-    u64 part_all[2][16];
-    u64 warp_mass[kWarps];
-    u64 warp_count[kWarps];
-    u64 warp_all[kWarps];
+    u64 part[2][16];
+    u64 warp_sum[2][kWarps];
     // what the search for a border found
-    u64 before_mass, bin_mass, border;
-    u64 before_count;
-    uint32_t bin_count, bin, tie_limit;
+    u64 before, bin_mass, border;
+    uint32_t bin_count, bin, bin_to, tie_limit;
     uint32_t listed;
 };
 
@@ -118,18 +120,16 @@ struct Scale {
 };
 
 // A logit's place: t in 2^-17 steps, monotone in x, since each of its three
-// roundings is. From kNoPart on (t = 41, -inf, NaN) it has no part in the mass.
+// roundings is. From kNoPart on (t = 41, -inf) it has no part in the mass.
 constexpr uint32_t kStepBits = 23, kNoPart = 41u << 17;
 __device__ __forceinline__ uint32_t steps_of(float x, const Scale& s) {
-    const float d = x == s.top ? 0.f : s.top - x;  // also where both are +inf
-    return __float_as_uint(fmaf(d, s.hi, 64.f)) - 0x42800000u;
+    return __float_as_uint(fmaf(s.top - x, s.hi, 64.f)) - 0x42800000u;
 }
 // Its mass w in units of 2^-42, given that it has a part.
 __device__ __forceinline__ u64 mass_of(float x, const Scale& s) {
-    const bool same = x == s.top;
-    const float d = same ? 0.f : s.top - x;
+    const float d = s.top - x;
     // the rounding error of the difference, then of the product
-    const float bb = d - s.top, err = same ? 0.f : (s.top - (d - bb)) - (x + bb);
+    const float bb = d - s.top, err = (s.top - (d - bb)) - (x + bb);
     const float th = d * s.hi;
     const float tl = fmaf(d, s.hi, -th) + fmaf(d, s.lo, err * s.hi);
     const float whole = th + 12582912.f;  // 1.5 * 2^23: rounds to a whole number n <= 41, in the low bits
@@ -191,7 +191,8 @@ static_assert(offset_slice(16) % 16 == 0, "alignment of the slice");
 // up to `tie`.
 struct Row {
     const float* x;
-    int n, base;  // members and first index
+    int n, base;  // logits and first index
+    int len;      // logits of a thread
     Scale scale;
     uint32_t limit;
     u64 border;
@@ -200,177 +201,189 @@ struct Row {
 };
 constexpr int kCodeBits = kStepBits + 32;
 __device__ __forceinline__ u64 code_of(uint32_t steps, float x) { return ((u64)steps << 32) | (uint32_t)~value_bits(x); }
+// Steps below this are kept for certain: the border's own are limit - 1.
+__device__ __forceinline__ uint32_t sure_steps(const Row& r) { return r.border == ~0ull ? r.limit : r.limit - 1; }
 __device__ __forceinline__ bool kept(const Row& r, u64 code, uint32_t index) {
     return code < r.border || (code == r.border && index <= r.tie);
 }
-// f(i, x, code) for each member of the row's slice in the kept set whose code
-// begins with `prefix` (bits from `shift` up).
-template <class F>
-__device__ __forceinline__ void each_member(const Row& row, u64 prefix, int shift, F f) {
-    for (int i0 = threadIdx.x; i0 < row.n; i0 += 4 * kThreads) {
+// Each thread takes consecutive logits, an odd number of them so that a warp's
+// 32 lie in 32 banks; the slice is filled up with -inf to a whole number of
+// threads.
+__host__ __device__ __forceinline__ int per_thread(int n) { return ((n + kThreads - 1) / kThreads) | 1; }
+
+// The mass of the thread's logits with steps in [from, to), counted in `hist`
+// by bin where that is given; f(i, x, steps) for those with steps in [to,
+// row.limit). The masses of four are taken together, without a branch between
+// them: one's chain is some 30 operations.
+template <bool COUNT, class F>
+__device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to, uint32_t* hist, F f) {
+    const int i0 = threadIdx.x * row.len, i1 = i0 + row.len;
+    const uint32_t span = to > from ? to - from : 0, few = row.limit > to ? row.limit - to : 0;
+    u64 sum = 0;
+    for (int i = i0; i < i1; i += 4) {
         float x[4];
         uint32_t steps[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = i0 + j * kThreads < row.n ? row.x[i0 + j * kThreads] : -INFINITY;
-        bool any = false;
+        bool in = false, near = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            x[j] = i + j < i1 ? row.x[i + j] : -INFINITY;
             steps[j] = steps_of(x[j], row.scale);
-            any |= steps[j] < row.limit;
+            in |= steps[j] - from < span;
+            near |= steps[j] - to < few;
         }
-        if (!any) continue;
+        if (in) {
+            u64 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const u64 code = code_of(steps[j], x[j]);
-            const int i = i0 + j * kThreads;
-            if (steps[j] < row.limit && (code >> shift) == prefix && kept(row, code, row.base + i)) f(i, x[j], code);
+            for (int j = 0; j < 4; ++j) w[j] = mass_of(x[j], row.scale);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sum += steps[j] - from < span ? w[j] : 0;
+                if (COUNT && steps[j] - from < span) atomicAdd(&hist[steps[j] >> (kStepBits - 11)], 1u);
+            }
+        }
+        if (near) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (steps[j] - to < few) f(i + j, x[j], steps[j]);
         }
     }
+    return sum;
+}
+// f(i, x, code) for each of the thread's members of the kept set with steps
+// from `from` on.
+template <class F>
+__device__ __forceinline__ void each_member(const Row& row, uint32_t from, F f) {
+    sweep<false>(row, from, from, nullptr, [&](int i, float x, uint32_t steps) {
+        const u64 code = code_of(steps, x);
+        if (kept(row, code, row.base + i)) f(i, x, code);
+    });
 }
 
-struct Found {
-    uint32_t members;  // of the bin in which the target is reached (0: it is not)
-    uint32_t bin;
-    u64 bin_mass, before_mass;
-    u64 before_count;
-    u64 all;  // sum of the threads' `own`
+// A run of 2^width codes from `from` on.
+struct Range {
+    u64 from;
+    int width;
+    __device__ __forceinline__ bool has(u64 code) const { return ((code - from) >> width) == 0; }
+    __device__ __forceinline__ int shift() const { return max(width - 11, 0); }  // codes of a bin, as a power of two
+    __device__ __forceinline__ uint32_t bin(u64 code) const { return (uint32_t)((code - from) >> shift()); }
 };
 
-// The bin of the cluster's histogram in which the count, or the mass, reaches
-// the target; a mass target of 0 stands for `part` of the sum of `own`.
-__device__ __forceinline__ Found locate(Row& row, bool by_mass, bool with_mass, u64& target, float part, u64 own,
-                                        Shared& sh, uint32_t rank, int C) {
+enum Search { kByCount, kByMass, kByBounds };
+
+// The bin of the cluster's histogram in which the target is reached: in
+// sh.bin_count (0: it is not reached), sh.bin, sh.bin_mass and, with what lies
+// before the bin, sh.before. `own` is summed over the threads and added to
+// `all`. kByMass starts from `all`. kByBounds takes `part` of `all` as the target,
+// and finds the first bin in which the bins' largest possible masses reach it
+// and the first (sh.bin_to) in which their smallest do.
+template <Search S>
+__device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 own, u64& all, Shared& sh, uint32_t rank,
+                                       int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int bins = kBins / C;  // that this CTA sums
     u64* red_mass = reinterpret_cast<u64*>(reinterpret_cast<uint8_t*>(&sh) + offset_sums());
     uint32_t* red_count = reinterpret_cast<uint32_t*>(red_mass + bins);
-    if (C > 1) cluster_sync();
-    else __syncthreads();
-    u64 pm = 0, pc = 0;
-    for (int i = tid; i < bins; i += kThreads) {
-        u64 m = 0;
-        uint32_t c = 0;
-        if (C > 1) {
-            for (int r = 0; r < C; ++r) {
-                c += ld_remote32(remote(&sh.hist.count[rank * bins + i], r));
-                if (with_mass) m += ld_remote64(remote(&sh.hist.mass[rank * bins + i], r));
-            }
-            red_mass[i] = m;
-            red_count[i] = c;
-        } else {
-            c = sh.hist.count[i];
-            m = sh.hist.mass[i];
-        }
-        pm += m;
-        pc += c;
-    }
-    pm = warp_sum(pm);
-    pc = warp_sum(pc);
     own = warp_sum(own);
-    if (lane == 0) {
-        sh.warp_mass[warp] = pm;
-        sh.warp_count[warp] = pc;
-        sh.warp_all[warp] = own;
+    if (lane == 0) sh.warp_sum[0][warp] = own;
+    if (tid == 0) {
+        sh.bin_count = 0;
+        sh.bin_to = kBins - 1;
     }
-    if (tid == 0) sh.bin_count = 0;
     __syncthreads();
     row.turn ^= 1;
     if (tid < C) {
-        u64 m = 0, c = 0, a = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            m += sh.warp_mass[w];
-            c += sh.warp_count[w];
-            a += sh.warp_all[w];
-        }
-        st_remote64(remote(&sh.part_mass[row.turn][rank], tid), m);
-        st_remote32(remote(&sh.part_count[row.turn][rank], tid), (uint32_t)c);
-        st_remote64(remote(&sh.part_all[row.turn][rank], tid), a);
+        u64 a = 0;
+        for (int w = 0; w < kWarps; ++w) a += sh.warp_sum[0][w];
+        st_remote64(remote(&sh.part[row.turn][rank], tid), a);
     }
     cluster_sync();
-    Found found;
-    found.all = 0;
-    for (int r = 0; r < C; ++r) found.all += sh.part_all[row.turn][r];
-    if (by_mass && target == 0) {
-        target = part > 0.f ? share(part, found.all, true) : 0;
+    if (C > 1) {
+        for (int i = tid; i < bins; i += kThreads) {
+            u64 m = 0;
+            uint32_t c = 0;
+            for (int r = 0; r < C; ++r) {
+                c += ld_remote32(remote(&sh.hist.count[rank * bins + i], r));
+                if (S == kByMass) m += ld_remote64(remote(&sh.hist.mass[rank * bins + i], r));
+            }
+            red_mass[i] = m;
+            red_count[i] = c;
+        }
+        cluster_sync();
+    }
+    for (int r = 0; r < C; ++r) all += sh.part[row.turn][r];
+    if (S == kByBounds) {
+        target = part > 0.f ? share(part, all, true) : 0;
         target = target > 1 ? target : 1;
     }
-    // the CTA whose bins hold it
-    int q = 0;
-    u64 bm = 0, bc = 0;
-    for (; q < C - 1; ++q) {
-        const u64 m = sh.part_mass[row.turn][q], c = sh.part_count[row.turn][q];
-        if ((by_mass ? bm + m : bc + c) >= target) break;
-        bm += m;
-        bc += c;
-    }
-    // the bin: each thread sums `per` of that CTA's bins, a scan finds the
-    // thread, the thread the bin
-    const uint32_t mass_at = C > 1 ? remote(red_mass, q) : smem_u32(sh.hist.mass);
-    const uint32_t count_at = C > 1 ? remote(red_count, q) : smem_u32(sh.hist.count);
-    const int per = (bins + kThreads - 1) / kThreads;
-    u64 sm = 0, sc = 0;
-    for (int j = 0; j < per; ++j) {
-        const int i = tid * per + j;
-        if (i < bins) {
-            sc += ld_remote32(count_at + 4u * i);
-            if (with_mass) sm += ld_remote64(mass_at + 8u * i);
-        }
-    }
-    u64 im = sm, ic = sc;
+    // four bins a thread (they lie in one CTA), their sums scanned
+    static_assert(kBins == 4 * kThreads, "four bins a thread");
+    const int b0 = 4 * tid, q = b0 / bins, at = b0 - q * bins;
+    const uint32_t count_at = (C > 1 ? remote(red_count, q) : smem_u32(sh.hist.count)) + 4u * at;
+    const uint32_t mass_at = (C > 1 ? remote(red_mass, q) : smem_u32(sh.hist.mass)) + 8u * at;
+    uint32_t c[4];
+    u64 v[2][4], sum[2] = {0, 0};  // what is searched; kByBounds: largest, smallest
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 a = __shfl_up_sync(0xffffffffu, im, o), b = __shfl_up_sync(0xffffffffu, ic, o);
-        if (lane >= o) {
-            im += a;
-            ic += b;
+    for (int j = 0; j < 4; ++j) {
+        c[j] = ld_remote32(count_at + 4u * j);
+        v[0][j] = S == kByMass ? ld_remote64(mass_at + 8u * j) : c[j];
+        v[1][j] = 0;
+        if (S == kByBounds) {
+            // 2^(42 - t) at the bin's ends, t off by the rounding of the steps
+            const float t = (float)(b0 + j) * (1.f / 32.f);
+            v[0][j] = c[j] * __float2ull_ru(exp2f((float)kMassBits - t) * 1.0001f);
+            v[1][j] = c[j] * __float2ull_rd(exp2f((float)kMassBits - t - 1.f / 32.f) * 0.9999f);
+        }
+        sum[0] += v[0][j];
+        sum[1] += v[1][j];
+    }
+    u64 upto[2] = {sum[0], sum[1]};
+#pragma unroll
+    for (int k = 0; k < (S == kByBounds ? 2 : 1); ++k) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 a = __shfl_up_sync(0xffffffffu, upto[k], o);
+            if (lane >= o) upto[k] += a;
         }
     }
+    __syncthreads();
     if (lane == 31) {
-        sh.warp_mass[warp] = im;
-        sh.warp_count[warp] = ic;
+        sh.warp_sum[0][warp] = upto[0];
+        sh.warp_sum[1][warp] = upto[1];
     }
     __syncthreads();
-    bm += im - sm;
-    bc += ic - sc;
-    for (int w = 0; w < warp; ++w) {
-        bm += sh.warp_mass[w];
-        bc += sh.warp_count[w];
-    }
-    if (sc && (by_mass ? bm < target && target <= bm + sm : bc < target && target <= bc + sc)) {
-        for (int j = 0; j < per; ++j) {
-            const int i = tid * per + j;
-            const uint32_t c = ld_remote32(count_at + 4u * i);
-            const u64 m = with_mass ? ld_remote64(mass_at + 8u * i) : 0;
-            if (c && (by_mass ? bm + m : bc + c) >= target) {
-                sh.bin = q * bins + i;
-                sh.bin_mass = m;
-                sh.bin_count = c;
-                sh.before_mass = bm;
-                sh.before_count = bc;
-                break;
+#pragma unroll
+    for (int k = 0; k < (S == kByBounds ? 2 : 1); ++k) {
+        u64 before = (S == kByMass ? all : 0) + upto[k] - sum[k];
+        for (int w = 0; w < warp; ++w) before += sh.warp_sum[k][w];
+        if (before < target && target <= before + sum[k]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (before < target && target <= before + v[k][j]) {
+                    if (k == 0) {
+                        sh.bin = b0 + j;
+                        sh.bin_count = c[j];
+                        sh.bin_mass = v[0][j];
+                        sh.before = before;
+                    } else {
+                        sh.bin_to = b0 + j;
+                    }
+                }
+                before += v[k][j];
             }
-            bm += m;
-            bc += c;
         }
     }
     __syncthreads();
-    found.members = sh.bin_count;
-    found.bin = sh.bin;
-    found.bin_mass = sh.bin_mass;
-    found.before_mass = sh.before_mass;
-    found.before_count = sh.before_count;
-    return found;
 }
 
-// Gathers the members that begin with `prefix` in the first CTA, which ranks
-// them and finds the last one that is kept: the count-th (0: the last of all)
-// and, with by_mass, the first up to which the mass reaches `goal`, or where
-// that is 0 `part` of the mass up to the count-th. False when there are more
-// than kList. `mass` receives their mass up to the border.
-__device__ __forceinline__ bool settle(Row& row, u64 prefix, int shift, u64 count, bool by_mass, u64 goal, float part,
-                                       u64& mass, Shared& sh, uint32_t rank, int C) {
+// Gathers the range's members in the first CTA, which ranks them and finds the
+// last one that is kept: the count-th (0: the last of all) and, with by_mass,
+// the first up to which the mass reaches `goal`, or where that is 0 `part` of
+// the mass up to the count-th. False when there are more than kList.
+__device__ __forceinline__ bool settle(Row& row, const Range range, u64 count, bool by_mass, u64 goal, float part,
+                                       Shared& sh, uint32_t rank, int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    each_member(row, prefix, shift, [&](int i, float x, u64 code) {
+    each_member(row, (uint32_t)(range.from >> 32), [&](int i, float x, u64 code) {
+        if (!range.has(code)) return;
         const uint32_t at = atom_add_remote32(remote(&sh.listed, 0), 1u);
         if (at < kList) {
             st_remote64(remote(&sh.list.code[at], 0), code);
@@ -408,9 +421,9 @@ __device__ __forceinline__ bool settle(Row& row, u64 prefix, int shift, u64 coun
                 const u64 v = __shfl_up_sync(0xffffffffu, upto, o);
                 if (lane >= o) upto += v;
             }
-            if (lane == 31) sh.warp_mass[warp] = upto;
+            if (lane == 31) sh.warp_sum[0][warp] = upto;
             named_bar_sync(1, kList);
-            for (int w = 0; w < warp; ++w) upto += sh.warp_mass[w];
+            for (int w = 0; w < warp; ++w) upto += sh.warp_sum[0][w];
             sh.list.sums[tid] = upto;
             named_bar_sync(1, kList);
             const uint32_t last = (count ? (uint32_t)min(count, (u64)members) : members) - 1;
@@ -422,7 +435,6 @@ __device__ __forceinline__ bool settle(Row& row, u64 prefix, int shift, u64 coun
             if ((uint32_t)tid < members && here) {
                 sh.border = sh.list.code[sh.list.order[tid]];
                 sh.tie_limit = sh.list.index[sh.list.order[tid]];
-                sh.bin_mass = upto;
             }
         }
     }
@@ -430,7 +442,6 @@ __device__ __forceinline__ bool settle(Row& row, u64 prefix, int shift, u64 coun
     if (fits) {
         row.border = ld_remote64(remote(&sh.border, 0));
         row.tie = ld_remote32(remote(&sh.tie_limit, 0));
-        mass = ld_remote64(remote(&sh.bin_mass, 0));
         row.limit = min(row.limit, (uint32_t)(row.border >> 32) + 1);
         cluster_sync();
     }
@@ -439,122 +450,129 @@ __device__ __forceinline__ bool settle(Row& row, u64 prefix, int shift, u64 coun
 
 // Narrows the row to its first k members (k > 0), and of those to the shortest
 // run that reaches `part` of their mass (by_p). `top` is the thread's largest
-// logit.
-__device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, float top, Shared& sh, uint32_t rank,
-                                       int C) {
+// logit. The mass of the thread's logits with steps below `summed`, all of
+// them kept, is left in `below`.
+__device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, float top, uint32_t& summed, u64& below,
+                                       Shared& sh, uint32_t rank, int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    bool bounded = false;
-    u64 total = 0;  // mass of the first k, once known
+    auto clear = [&] {
+        for (int i = tid; i < kBins; i += kThreads) {
+            sh.hist.mass[i] = 0;
+            sh.hist.count[i] = 0;
+        }
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+    };
     for (int stage = k > 0 ? 0 : 1; stage < (by_p ? 2 : 1); ++stage) {
         const bool by_mass = stage == 1;
-        u64 target = by_mass ? 0 : (u64)k;
-        if (by_mass && total) {
-            target = part > 0.f ? share(part, total, true) : 0;
-            target = target > 1 ? target : 1;
+        u64 target = (u64)k, all = 0;
+        Range range = {0, kCodeBits};
+        clear();
+        if (!by_mass) {
+            const uint32_t steps = steps_of(top, row.scale);
+            if (steps < row.limit) atomicAdd(&sh.hist.count[range.bin(code_of(steps, top))], 1u);
+            locate<kByCount>(row, target, 0.f, 0, all, sh, rank, C);
+            if (sh.bin_count) {
+                row.limit = min(row.limit, (sh.bin + 1) << (kStepBits - 11));
+                if (settle(row, range, (u64)k, by_p, 0, part, sh, rank, C)) return;
+            }
+            clear();
+        } else {
+            u64 near = 0;
+            u64 own = sweep<true>(row, 0, sure_steps(row), sh.hist.count, [&](int i, float x, uint32_t steps) {
+                if (!kept(row, code_of(steps, x), row.base + i)) return;
+                near += mass_of(x, row.scale);
+                atomicAdd(&sh.hist.count[steps >> (kStepBits - 11)], 1u);
+            });
+            own += near;
+            locate<kByBounds>(row, target, part, own, all, sh, rank, C);
+            const uint32_t b1 = sh.bin, b2 = sh.bin_to;
+            range.width = kCodeBits - 11 + (b2 > b1 ? 32 - __clz((int)(b2 - b1)) : 0);
+            range.from = (u64)b1 << (kCodeBits - 11);
+            row.limit = min(row.limit, (b2 + 1) << (kStepBits - 11));
+            summed = b1 << (kStepBits - 11);
+            all = 0;
+            clear();
         }
-        u64 before = 0, prefix = 0, in_bin = 0;
-        uint32_t members = 0, bin = 0;
-        int shift = kCodeBits;
-        bool done = false;
-        for (int level = bounded ? 0 : -1; level < 5 && !done; ++level) {
-            for (int i = tid; i < kBins; i += kThreads) {
-                sh.hist.mass[i] = 0;
-                sh.hist.count[i] = 0;
-            }
-            if (tid == 0) sh.listed = 0;
-            __syncthreads();
-            const int low = level < 0 ? kCodeBits - 11 : shift - 11;
-            const bool with_mass = by_mass || (by_p && level >= 0);
-            auto enter = [&](int, float x, u64 code) {
-                const uint32_t at = (uint32_t)(code >> low) & (kBins - 1u);
+        for (bool again = false;; again = true) {
+            const int shift = range.shift();
+            auto enter = [&](int i, float x, uint32_t steps) {
+                const u64 code = code_of(steps, x);
+                if (!range.has(code) || !kept(row, code, row.base + i)) return;
+                const uint32_t at = range.bin(code);
                 atomicAdd(&sh.hist.count[at], 1u);
-                if (with_mass) atomicAdd(&sh.hist.mass[at], mass_of(x, row.scale));
+                if (by_mass) atomicAdd(&sh.hist.mass[at], mass_of(x, row.scale));
             };
-            u64 own = 0;
-            if (level < 0) {
-                const uint32_t steps = steps_of(top, row.scale);
-                if (steps < row.limit) enter(0, top, code_of(steps, top));
-                if (by_mass) each_member(row, 0, kCodeBits, [&](int, float x, u64) { own += mass_of(x, row.scale); });
-            } else {
-                each_member(row, prefix, shift, enter);
-            }
-            const Found f = locate(row, by_mass, with_mass, target, part, own, sh, rank, C);
-            if (level < 0) {
-                bounded = true;
-                if (f.members == 0) continue;
-                row.limit = min(row.limit, (f.bin + 1) << (kStepBits - 11));
-                // the members are the first of all: both searches at once
-                done = settle(row, 0, kCodeBits, k > 0 ? (u64)k : 0, by_p, by_mass ? target : 0, part, total, sh, rank, C);
-                if (done) return;
-                continue;
-            }
-            if (f.members == 0) {  // the set does not reach the target (first level only): all of it is kept
-                done = true;
-                if (!by_mass) {
-                    total = 0;
-                    for (int r = 0; r < C; ++r) total += sh.part_mass[row.turn][r];
-                }
-                continue;
-            }
-            target -= by_mass ? f.before_mass : f.before_count;
-            prefix = (prefix << 11) | f.bin;
-            shift = low;
-            before += f.before_mass;
-            members = f.members;
-            bin = f.bin;
-            in_bin = f.bin_mass;
+            const uint32_t first = (uint32_t)(range.from >> 32);
+            const u64 own = sweep<false>(row, by_mass && !again ? 0 : first, first, nullptr, enter);
+            if (by_mass && !again) below = own;
+            if (by_mass) locate<kByMass>(row, target, 0.f, own, all, sh, rank, C);
+            else locate<kByCount>(row, target, 0.f, 0, all, sh, rank, C);
+            const uint32_t members = sh.bin_count, bin = sh.bin;
+            if (members == 0) break;  // fewer than k: all are kept
+            if (!by_mass) target -= sh.before;
+            range.from += (u64)bin << shift;
+            range.width = shift;
             if (by_mass ? members == 1 : target == members) {  // all of the bin is kept
-                const u64 bound = shift == 0 ? prefix : (prefix << shift) | ((1ull << shift) - 1ull);
+                const u64 bound = range.from + ((1ull << shift) - 1ull);
                 if (bound < row.border) {
                     row.border = bound;
                     row.tie = 0xffffffffu;
                     row.limit = min(row.limit, (uint32_t)(bound >> 32) + 1);
                 }
-                total = before + in_bin;
-                done = true;
-            } else if (members <= kList) {
-                u64 mass;
-                settle(row, prefix, shift, by_mass ? 0 : target, by_mass, target, part, mass, sh, rank, C);
-                total = before + mass;
-                done = true;
+                break;
             }
-        }
-        if (done) continue;
-        // more than kList members of one value: all of one mass, in index order
-        const u64 each = mass_of(bits_value(~(uint32_t)prefix), row.scale);
-        const u64 need = by_mass ? (target + each - 1) / each : target;
-        const uint32_t mine = sh.hist.count[bin];
-        uint32_t lower = 0;
-        for (uint32_t r = 0; r < rank; ++r) lower += ld_remote32(remote(&sh.hist.count[bin], r));
-        if (lower < need && need <= (u64)lower + mine) {
-            // warp by warp in index order
-            const int chunk = ((row.n + kWarps - 1) / kWarps + 31) / 32 * 32;
-            const int i0 = warp * chunk, i1 = min(i0 + chunk, row.n);
-            auto tied = [&](int i) {
-                if (i >= i1) return false;
-                const u64 code = code_of(steps_of(row.x[i], row.scale), row.x[i]);
-                return code == prefix && kept(row, code, row.base + i);
-            };
-            uint32_t n = 0;
-            for (int i = i0; i < i1; i += 32) n += __popc(__ballot_sync(0xffffffffu, tied(i + lane)));
-            if (lane == 0) sh.warp_count[warp] = n;
-            __syncthreads();
-            u64 at = lower;
-            for (int w = 0; w < warp; ++w) at += sh.warp_count[w];
-            for (int i = i0; i < i1; i += 32) {
-                const uint32_t set = __ballot_sync(0xffffffffu, tied(i + lane));
-                const u64 place = at + __popc(set & ((2u << lane) - 1u));
-                if (((set >> lane) & 1u) && place == need)
-                    for (int r = 0; r < C; ++r) st_remote32(remote(&sh.tie_limit, r), row.base + i + lane);
-                at += __popc(set);
+            const u64 rest = by_mass ? target - sh.before : target;
+            if (members <= kList) {
+                settle(row, range, by_mass ? 0 : rest, by_mass, rest, 0.f, sh, rank, C);
+                break;
             }
+            if (shift == 0) {
+                // more than kList members of one value: all of one mass, in
+                // index order
+                const u64 each = mass_of(bits_value(~(uint32_t)range.from), row.scale);
+                const u64 need = by_mass ? (rest + each - 1) / each : rest;
+                const uint32_t mine = sh.hist.count[bin];
+                uint32_t lower = 0;
+                for (uint32_t r = 0; r < rank; ++r) lower += ld_remote32(remote(&sh.hist.count[bin], r));
+                if (lower < need && need <= (u64)lower + mine) {
+                    // thread by thread, as they lie
+                    const int i0 = min(tid * row.len, row.n), i1 = min(i0 + row.len, row.n);
+                    auto tied = [&](int i) {
+                        const u64 code = code_of(steps_of(row.x[i], row.scale), row.x[i]);
+                        return code == range.from && kept(row, code, row.base + i);
+                    };
+                    uint32_t n = 0;
+                    for (int i = i0; i < i1; ++i) n += tied(i);
+                    uint32_t upto = n;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += v;
+                    }
+                    __syncthreads();
+                    if (lane == 31) sh.warp_sum[0][warp] = upto;
+                    __syncthreads();
+                    u64 place = (u64)lower + upto - n;
+                    for (int w = 0; w < warp; ++w) place += sh.warp_sum[0][w];
+                    if (place < need && need <= place + n) {
+                        int i = i0;
+                        for (;; ++i)
+                            if (tied(i) && ++place == need) break;
+                        for (int r = 0; r < C; ++r) st_remote32(remote(&sh.tie_limit, r), row.base + i);
+                    }
+                }
+                cluster_sync();
+                row.border = range.from;
+                row.tie = sh.tie_limit;
+                row.limit = min(row.limit, (uint32_t)(row.border >> 32) + 1);
+                cluster_sync();
+                break;
+            }
+            all = sh.before;
+            __syncthreads();  // all have read what was found
+            clear();
         }
-        cluster_sync();
-        row.border = prefix;
-        row.tie = sh.tie_limit;
-        row.limit = min(row.limit, (uint32_t)(prefix >> 32) + 1);
-        total = before + need * each;
-        cluster_sync();
     }
 }
 
@@ -582,6 +600,7 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     row.base = (int)rank * p.slice;
     row.n = max(0, min(p.slice, p.V - row.base));
     row.x = xs;
+    row.len = per_thread(p.slice);
     row.border = ~0ull;
     row.tie = 0xffffffffu;
     row.limit = kNoPart;
@@ -620,16 +639,17 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
         }
     }
     for (int i = nv * kVec + tid; i < row.n; i += kThreads) see(clean(load_logit<DT>(src, i)), i);
-    const float own_top = best ? bits_value((uint32_t)(best >> 32)) : -INFINITY;
+    for (int i = row.n + tid; i < row.len * kThreads; i += kThreads) xs[i] = -INFINITY;
+    float own_top = best ? bits_value((uint32_t)(best >> 32)) : -INFINITY;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const u64 other = __shfl_xor_sync(0xffffffffu, best, o);
         best = other > best ? other : best;
     }
-    if (lane == 0) sh.warp_mass[warp] = best;
+    if (lane == 0) sh.warp_sum[0][warp] = best;
     __syncthreads();
     if (tid < C) {
-        for (int w = 0; w < kWarps; ++w) best = sh.warp_mass[w] > best ? sh.warp_mass[w] : best;
+        for (int w = 0; w < kWarps; ++w) best = sh.warp_sum[0][w] > best ? sh.warp_sum[0][w] : best;
         st_remote64(remote(&sh.best[rank], tid), best);
     }
     cluster_sync();
@@ -650,27 +670,38 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
 
     const float top_p = p.top_p ? p.top_p[m] : 1.f;
     const bool by_p = top_p < 1.f;
-    if ((k > 0 && k < p.V) || by_p) narrow(row, k < p.V ? max(k, 0) : 0, by_p, top_p, own_top, sh, rank, C);
+    if (row.scale.top == INFINITY) {
+        // infinities share the mass: equal logits before nothing
+        for (int i = tid; i < row.n; i += kThreads) xs[i] = xs[i] == INFINITY ? 0.f : -INFINITY;
+        own_top = own_top == INFINITY ? 0.f : -INFINITY;
+        row.scale.top = 0.f;
+        __syncthreads();
+    }
+    uint32_t summed = 0;
+    u64 below = 0;
+    if ((k > 0 && k < p.V) || by_p) narrow(row, k < p.V ? max(k, 0) : 0, by_p, top_p, own_top, summed, below, sh, rank, C);
 
-    // The kept mass in index order: each thread takes consecutive logits, an
-    // odd number of them so that a warp's 32 lie in 32 banks.
+    // The kept mass in index order. Whether w >= min_p is asked only where t
+    // is within 2^-10 of -log2(min_p).
+    uint32_t sure = sure_steps(row);
+    u64 least = 0;
     const float min_p = p.min_p ? fminf(p.min_p[m], 1.f) : 0.f;
-    const u64 least = min_p > 0.f ? __float2ull_ru(min_p * (float)(1ull << kMassBits)) : 0ull;
-    auto mass_at = [&](int i) -> u64 {
-        const float x = xs[i];
-        const uint32_t steps = steps_of(x, row.scale);
+    if (min_p > 0.f) {
+        least = __float2ull_ru(min_p * (float)(1ull << kMassBits));
+        const uint32_t t = (uint32_t)(fminf(-log2f(min_p), 41.f) * (float)(1 << (kStepBits - 6)));
+        sure = min(sure, t > 128 ? t - 128 : 0);
+        row.limit = min(row.limit, t + 129);
+    }
+    auto mass_at = [&](int i, float x, uint32_t steps) -> u64 {
         if (steps >= row.limit || !kept(row, code_of(steps, x), row.base + i)) return 0;
         const u64 w = mass_of(x, row.scale);
         return w >= least ? w : 0;
     };
-    const int len = ((row.n + kThreads - 1) / kThreads) | 1;
-    const int i0 = min(tid * len, row.n), i1 = min(i0 + len, row.n);
-    u64 own = 0;
-    {
-        int i = i0;
-        for (; i + 4 <= i1; i += 4) own += (mass_at(i) + mass_at(i + 1)) + (mass_at(i + 2) + mass_at(i + 3));
-        for (; i < i1; ++i) own += mass_at(i);
-    }
+    u64 near = 0;
+    const uint32_t from = summed <= sure ? summed : 0;
+    u64 own = sweep<false>(row, from, sure, nullptr, [&](int i, float x, uint32_t steps) { near += mass_at(i, x, steps); });
+    own += near + (from ? below : 0);
+    const int i0 = min(tid * row.len, row.n), i1 = min(i0 + row.len, row.n);
     u64 upto = own;  // of the warp's threads up to this one
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -678,21 +709,21 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
         if (lane >= o) upto += v;
     }
     __syncthreads();
-    if (lane == 31) sh.warp_mass[warp] = upto;
+    if (lane == 31) sh.warp_sum[0][warp] = upto;
     __syncthreads();
     row.turn ^= 1;
     if (tid < C) {
         u64 sum = 0;
-        for (int i = 0; i < kWarps; ++i) sum += sh.warp_mass[i];
-        st_remote64(remote(&sh.part_mass[row.turn][rank], tid), sum);
+        for (int i = 0; i < kWarps; ++i) sum += sh.warp_sum[0][i];
+        st_remote64(remote(&sh.part[row.turn][rank], tid), sum);
     }
     cluster_sync();
     u64 before = 0, all = 0;
     for (int r = 0; r < C; ++r) {
-        if (r < (int)rank) before += sh.part_mass[row.turn][r];
-        all += sh.part_mass[row.turn][r];
+        if (r < (int)rank) before += sh.part[row.turn][r];
+        all += sh.part[row.turn][r];
     }
-    for (int i = 0; i < warp; ++i) before += sh.warp_mass[i];
+    for (int i = 0; i < warp; ++i) before += sh.warp_sum[0][i];
     const float u = p.u[m];
     const u64 goal = !(u > 0.f) ? 0ull : u < 1.f ? share(u, all, false) : all - 1;
     // the thread whose logits hold the first cumulated mass above the goal,
@@ -702,9 +733,9 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     if (holder == 0) return;
     const int who = __ffs(holder) - 1;
     before = __shfl_sync(0xffffffffu, before, who);
-    const int from = __shfl_sync(0xffffffffu, i0, who), to = __shfl_sync(0xffffffffu, i1, who);
-    for (int i = from; i < to; i += 32) {
-        const u64 one = i + lane < to ? mass_at(i + lane) : 0ull;
+    const int begin = __shfl_sync(0xffffffffu, i0, who), to = __shfl_sync(0xffffffffu, i1, who);
+    for (int i = begin; i < to; i += 32) {
+        const u64 one = i + lane < to ? mass_at(i + lane, xs[i + lane], steps_of(xs[i + lane], row.scale)) : 0ull;
         u64 sum = one;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -724,7 +755,7 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
 
 cudaError_t launch_sample(const SampleParams& p, int M, int dtype, cudaStream_t stream) {
     void (*kern)(SampleParams) = dtype == 0 ? sample_kernel<0> : sample_kernel<1>;
-    const int smem = offset_slice(p.C) + p.slice * 4;
+    const int smem = offset_slice(p.C) + per_thread(p.slice) * kThreads * 4;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess && p.C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
