@@ -274,15 +274,6 @@ int moe_sample(const void* logits, int dtype, int M, int V, int64_t row_stride, 
     p.prob = prob;
     p.row_stride = row_stride;
     p.V = V;
-    // CTAs a row: enough to hold it, and more while the grid stays within one
-    // CTA an SM and each still has 2,048 logits; rows beyond that in slices of
-    // which two fit an SM
-    p.C = 1;
-    auto slice = [&] { return (int)(((V + p.C - 1) / p.C + 7) / 8 * 8); };
-    while (slice() > moe::kSampleMaxSlice) p.C *= 2;
-    while (p.C < 16 && M * p.C * 2 <= dev.sms && V / (p.C * 2) >= 2048) p.C *= 2;
-    while (p.C < 16 && M * p.C > dev.sms && slice() > moe::kSampleHalfSlice) p.C *= 2;
-    p.slice = slice();
     return launched(moe::launch_sample(p, M, dtype, static_cast<cudaStream_t>(stream)), 1);
 }
 

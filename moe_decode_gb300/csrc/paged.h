@@ -38,9 +38,7 @@ struct AppendParams {
 };
 
 constexpr int kSampleThreads = 512;
-constexpr int kSampleBins = 2048;
-constexpr int kSampleMaxSlice = 45056;   // logits of a row that one CTA holds
-constexpr int kSampleHalfSlice = 20480;  // and one of two CTAs of an SM
+constexpr int kSampleMaxSlice = 45056;  // logits of a row that one CTA holds
 
 struct SampleParams {
     const void* logits;
@@ -95,6 +93,7 @@ constexpr int attn_part_floats(int rows, int head_dim) { return rows * (head_dim
 
 cudaError_t launch_paged_plan(const PlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_paged_append(const AppendParams& p, int sms, cudaStream_t stream);
-cudaError_t launch_sample(const SampleParams& p, int M, int dtype, cudaStream_t stream);
+// Chooses p.C and p.slice.
+cudaError_t launch_sample(SampleParams p, int M, int dtype, cudaStream_t stream);
 
 }  // namespace moe

@@ -16,20 +16,22 @@
 //
 // Top-k. The largest logits of the threads, one each, are members too, so the
 // bin in which k of them are reached cannot lie before the last member's: a
-// histogram (2048 bins of the code, summed across the cluster through
+// histogram (512 bins of the code, summed across the cluster through
 // distributed shared memory) that takes one atomic a thread, not one a logit.
 // Nothing beyond its bin needs more than a subtraction, a product and a
 // comparison from then on. Where at most kList members are left the first CTA
 // ranks them, with top-p at once.
 //
 // Top-p otherwise. One sweep sums the masses and counts the members of each
-// bin; a bin's masses differ by 2% at most, so the counts bound the border to
-// a few bins. A second sweep sums the masses before those exactly, and the
-// histogram (count and mass) of those alone, in 2048 parts.
+// bin; their counts and mean places bound the masses to 10^-3, and so the
+// border to a bin or two. A second sweep sums the masses before those exactly,
+// with a histogram (count and mass) of those alone, in 512 parts.
 //
 // Either way the last member's bin is split again until it has at most kList
 // members, which are ranked, or is one value, whose members count in index
 // order.
+#include <atomic>
+
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -39,7 +41,8 @@ namespace {
 using u64 = unsigned long long;
 constexpr int kThreads = kSampleThreads;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = kSampleBins;
+constexpr int kBinBits = 9, kBins = 1 << kBinBits;
+static_assert(kBins == kThreads, "a thread looks at one bin");
 constexpr int kList = 128;
 constexpr int kMassBits = 42;
 static_assert(kList * 4 == kThreads, "four threads rank a member");
@@ -81,19 +84,23 @@ __device__ __forceinline__ uint32_t atom_add_remote32(uint32_t a, uint32_t v) {
 }
 
 struct Shared {
-    union {
-        struct {
+    // histograms: members of each bin, and the sum of their places in it or of
+    // their masses. Two, used in turn: a CTA that is a barrier ahead clears the
+    // other than the one still being read.
+    struct {
+        uint32_t count[kBins];
+        union {
+            uint32_t place[kBins];
             u64 mass[kBins];
-            uint32_t count[kBins];
-        } hist;
-        struct {  // members of the border's bin (first CTA of the cluster)
-            u64 code[kList];
-            u64 mass[kList];
-            uint32_t index[kList];
-            uint16_t order[kList];
-            u64 sums[kList];
-        } list;
-    };
+        };
+    } hist[2];
+    struct {  // members of the border's bin (first CTA of the cluster)
+        u64 code[kList];
+        u64 mass[kList];
+        uint32_t index[kList];
+        uint16_t order[kList];
+        u64 sums[kList];
+    } list;
     u64 best[16];       // each CTA's largest logit and its index
     // each CTA's share of a cluster sum, in two sets used in turn: a CTA that
     // is a barrier ahead writes the other set than the one still being read
@@ -178,13 +185,15 @@ __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
-// Shared memory of a CTA: Shared, then the sums over the cluster of the bins
-// that the CTA owns (clusters of two or more; a single CTA's histogram is the
-// sum), then the slice.
-__host__ __device__ constexpr int owned_bins(int C) { return C > 1 ? kBins / C : 0; }
-__host__ __device__ constexpr int offset_sums() { return (int)((sizeof(Shared) + 15) & ~size_t(15)); }
-__host__ __device__ constexpr int offset_slice(int C) { return offset_sums() + owned_bins(C) * 12; }
-static_assert(offset_slice(16) % 16 == 0, "alignment of the slice");
+// Shared memory of a CTA: Shared, then the slice.
+__host__ __device__ constexpr int offset_slice() { return (int)((sizeof(Shared) + 15) & ~size_t(15)); }
+
+// A member into the histogram of all codes: its bin is an eighth of a unit of t.
+__device__ __forceinline__ void enter_bin(Shared& sh, int turn, uint32_t steps) {
+    const uint32_t bin = steps >> (kStepBits - kBinBits);
+    atomicAdd(&sh.hist[turn].count[bin], 1u);
+    atomicAdd(&sh.hist[turn].place[bin], (steps >> (kStepBits - kBinBits - 8)) & 255u);
+}
 
 // The row's slice that this CTA holds, and what bounds the kept set so far:
 // steps below `limit`, codes up to `border`, of those equal to it the indices
@@ -197,7 +206,7 @@ struct Row {
     uint32_t limit;
     u64 border;
     uint32_t tie;
-    int turn;  // which set of cluster sums is next
+    int turn;  // which histogram and set of cluster sums are in use
 };
 constexpr int kCodeBits = kStepBits + 32;
 __device__ __forceinline__ u64 code_of(uint32_t steps, float x) { return ((u64)steps << 32) | (uint32_t)~value_bits(x); }
@@ -206,27 +215,28 @@ __device__ __forceinline__ uint32_t sure_steps(const Row& r) { return r.border =
 __device__ __forceinline__ bool kept(const Row& r, u64 code, uint32_t index) {
     return code < r.border || (code == r.border && index <= r.tie);
 }
-// Each thread takes consecutive logits, an odd number of them so that a warp's
-// 32 lie in 32 banks; the slice is filled up with -inf to a whole number of
-// threads.
-__host__ __device__ __forceinline__ int per_thread(int n) { return ((n + kThreads - 1) / kThreads) | 1; }
+// Each thread takes consecutive logits, an odd number of 16-byte words so that
+// eight lanes' words lie in all the banks; the slice is filled up with -inf to
+// a whole number of threads.
+__host__ __device__ __forceinline__ int per_thread(int n) { return (((n + 4 * kThreads - 1) / (4 * kThreads)) | 1) * 4; }
 
-// The mass of the thread's logits with steps in [from, to), counted in `hist`
-// by bin where that is given; f(i, x, steps) for those with steps in [to,
-// row.limit). The masses of four are taken together, without a branch between
-// them: one's chain is some 30 operations.
+// The mass of the thread's logits with steps in [from, to); f(i, x, steps) for
+// those with steps in [to, row.limit). COUNT: each of the former also goes
+// into the histogram, into its bin's number of members and the sum of their
+// places within the bin. The masses of four are taken together, without a
+// branch between them: one's chain is some 30 operations.
 template <bool COUNT, class F>
-__device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to, uint32_t* hist, F f) {
+__device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to, Shared& sh, F f) {
     const int i0 = threadIdx.x * row.len, i1 = i0 + row.len;
     const uint32_t span = to > from ? to - from : 0, few = row.limit > to ? row.limit - to : 0;
     u64 sum = 0;
     for (int i = i0; i < i1; i += 4) {
-        float x[4];
+        const float4 q = *reinterpret_cast<const float4*>(row.x + i);
+        const float x[4] = {q.x, q.y, q.z, q.w};
         uint32_t steps[4];
         bool in = false, near = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            x[j] = i + j < i1 ? row.x[i + j] : -INFINITY;
             steps[j] = steps_of(x[j], row.scale);
             in |= steps[j] - from < span;
             near |= steps[j] - to < few;
@@ -238,7 +248,7 @@ __device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to,
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sum += steps[j] - from < span ? w[j] : 0;
-                if (COUNT && steps[j] - from < span) atomicAdd(&hist[steps[j] >> (kStepBits - 11)], 1u);
+                if (COUNT && steps[j] - from < span) enter_bin(sh, row.turn, steps[j]);
             }
         }
         if (near) {
@@ -252,8 +262,8 @@ __device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to,
 // f(i, x, code) for each of the thread's members of the kept set with steps
 // from `from` on.
 template <class F>
-__device__ __forceinline__ void each_member(const Row& row, uint32_t from, F f) {
-    sweep<false>(row, from, from, nullptr, [&](int i, float x, uint32_t steps) {
+__device__ __forceinline__ void each_member(const Row& row, uint32_t from, Shared& sh, F f) {
+    sweep<false>(row, from, from, sh, [&](int i, float x, uint32_t steps) {
         const u64 code = code_of(steps, x);
         if (kept(row, code, row.base + i)) f(i, x, code);
     });
@@ -263,9 +273,10 @@ __device__ __forceinline__ void each_member(const Row& row, uint32_t from, F f) 
 struct Range {
     u64 from;
     int width;
+    int shift;  // codes of a bin, as a power of two
     __device__ __forceinline__ bool has(u64 code) const { return ((code - from) >> width) == 0; }
-    __device__ __forceinline__ int shift() const { return max(width - 11, 0); }  // codes of a bin, as a power of two
-    __device__ __forceinline__ uint32_t bin(u64 code) const { return (uint32_t)((code - from) >> shift()); }
+    __device__ __forceinline__ uint32_t bin(u64 code) const { return (uint32_t)((code - from) >> shift); }
+    __device__ __forceinline__ void split() { shift = max(width - kBinBits, 0); }
 };
 
 enum Search { kByCount, kByMass, kByBounds };
@@ -273,16 +284,13 @@ enum Search { kByCount, kByMass, kByBounds };
 // The bin of the cluster's histogram in which the target is reached: in
 // sh.bin_count (0: it is not reached), sh.bin, sh.bin_mass and, with what lies
 // before the bin, sh.before. `own` is summed over the threads and added to
-// `all`. kByMass starts from `all`. kByBounds takes `part` of `all` as the target,
-// and finds the first bin in which the bins' largest possible masses reach it
-// and the first (sh.bin_to) in which their smallest do.
+// `all`. kByMass starts from `all`. kByBounds takes `part` of `all` as the
+// target, and finds the first bin in which the bins' largest possible masses
+// reach it and the first (sh.bin_to) in which their smallest do.
 template <Search S>
 __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 own, u64& all, Shared& sh, uint32_t rank,
                                        int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int bins = kBins / C;  // that this CTA sums
-    u64* red_mass = reinterpret_cast<u64*>(reinterpret_cast<uint8_t*>(&sh) + offset_sums());
-    uint32_t* red_count = reinterpret_cast<uint32_t*>(red_mass + bins);
     own = warp_sum(own);
     if (lane == 0) sh.warp_sum[0][warp] = own;
     if (tid == 0) {
@@ -290,51 +298,47 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
         sh.bin_to = kBins - 1;
     }
     __syncthreads();
-    row.turn ^= 1;
     if (tid < C) {
         u64 a = 0;
         for (int w = 0; w < kWarps; ++w) a += sh.warp_sum[0][w];
         st_remote64(remote(&sh.part[row.turn][rank], tid), a);
     }
     cluster_sync();
-    if (C > 1) {
-        for (int i = tid; i < bins; i += kThreads) {
-            u64 m = 0;
-            uint32_t c = 0;
-            for (int r = 0; r < C; ++r) {
-                c += ld_remote32(remote(&sh.hist.count[rank * bins + i], r));
-                if (S == kByMass) m += ld_remote64(remote(&sh.hist.mass[rank * bins + i], r));
-            }
-            red_mass[i] = m;
-            red_count[i] = c;
-        }
-        cluster_sync();
+    // one bin a thread, over the cluster: all the loads before the first sum
+    uint32_t c[16];
+    u64 w[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        c[r] = r < C ? ld_remote32(remote(&sh.hist[row.turn].count[tid], r)) : 0;
+        w[r] = 0;
+        if (S == kByMass && r < C) w[r] = ld_remote64(remote(&sh.hist[row.turn].mass[tid], r));
+        if (S == kByBounds && r < C) w[r] = ld_remote32(remote(&sh.hist[row.turn].place[tid], r));
+    }
+#pragma unroll
+    for (int r = 1; r < 16; ++r) {
+        c[0] += c[r];
+        w[0] += w[r];
     }
     for (int r = 0; r < C; ++r) all += sh.part[row.turn][r];
     if (S == kByBounds) {
         target = part > 0.f ? share(part, all, true) : 0;
         target = target > 1 ? target : 1;
     }
-    // four bins a thread (they lie in one CTA), their sums scanned
-    static_assert(kBins == 4 * kThreads, "four bins a thread");
-    const int b0 = 4 * tid, q = b0 / bins, at = b0 - q * bins;
-    const uint32_t count_at = (C > 1 ? remote(red_count, q) : smem_u32(sh.hist.count)) + 4u * at;
-    const uint32_t mass_at = (C > 1 ? remote(red_mass, q) : smem_u32(sh.hist.mass)) + 8u * at;
-    uint32_t c[4];
-    u64 v[2][4], sum[2] = {0, 0};  // what is searched; kByBounds: largest, smallest
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        c[j] = ld_remote32(count_at + 4u * j);
-        v[0][j] = S == kByMass ? ld_remote64(mass_at + 8u * j) : c[j];
-        v[1][j] = 0;
-        if (S == kByBounds) {
-            // 2^(42 - t) at the bin's ends, t off by the rounding of the steps
-            const float t = (float)(b0 + j) * (1.f / 32.f);
-            v[0][j] = c[j] * __float2ull_ru(exp2f((float)kMassBits - t) * 1.0001f);
-            v[1][j] = c[j] * __float2ull_rd(exp2f((float)kMassBits - t - 1.f / 32.f) * 0.9999f);
+    u64 sum[2] = {S == kByMass ? w[0] : c[0], 0};  // what is searched; kByBounds: largest, smallest
+    if (S == kByBounds) {
+        sum[0] = 0;
+        if (c[0]) {
+            // The mean of t, in parts of the bin, is known to 1/256. The mass
+            // of one falls from `first` to `first` 2^(-1/8) within the bin and
+            // is convex in t, so the mean mass is at least that of the mean t
+            // and at most the chord's there. 2^-16: t is off by its rounding.
+            const float first = exp2f((float)kMassBits - (float)tid * (1.f / 8.f));
+            const float mean = (float)w[0] / ((float)c[0] * 256.f);
+            const float most = first * (1.f - 0.08299595f * mean) * (1.f + 1.f / 65536.f);
+            const float least = first * exp2f((mean + 1.f / 256.f) * (-1.f / 8.f)) * (1.f - 1.f / 65536.f);
+            sum[0] = c[0] * __float2ull_ru(most);
+            sum[1] = c[0] * __float2ull_rd(least);
         }
-        sum[0] += v[0][j];
-        sum[1] += v[1][j];
     }
     u64 upto[2] = {sum[0], sum[1]};
 #pragma unroll
@@ -356,19 +360,13 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
         u64 before = (S == kByMass ? all : 0) + upto[k] - sum[k];
         for (int w = 0; w < warp; ++w) before += sh.warp_sum[k][w];
         if (before < target && target <= before + sum[k]) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (before < target && target <= before + v[k][j]) {
-                    if (k == 0) {
-                        sh.bin = b0 + j;
-                        sh.bin_count = c[j];
-                        sh.bin_mass = v[0][j];
-                        sh.before = before;
-                    } else {
-                        sh.bin_to = b0 + j;
-                    }
-                }
-                before += v[k][j];
+            if (k == 0) {
+                sh.bin = tid;
+                sh.bin_count = c[0];
+                sh.bin_mass = sum[0];
+                sh.before = before;
+            } else {
+                sh.bin_to = tid;
             }
         }
     }
@@ -382,7 +380,7 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
 __device__ __forceinline__ bool settle(Row& row, const Range range, u64 count, bool by_mass, u64 goal, float part,
                                        Shared& sh, uint32_t rank, int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    each_member(row, (uint32_t)(range.from >> 32), [&](int i, float x, u64 code) {
+    each_member(row, (uint32_t)(range.from >> 32), sh, [&](int i, float x, u64 code) {
         if (!range.has(code)) return;
         const uint32_t at = atom_add_remote32(remote(&sh.listed, 0), 1u);
         if (at < kList) {
@@ -456,9 +454,10 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
                                        Shared& sh, uint32_t rank, int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto clear = [&] {
+        row.turn ^= 1;
         for (int i = tid; i < kBins; i += kThreads) {
-            sh.hist.mass[i] = 0;
-            sh.hist.count[i] = 0;
+            sh.hist[row.turn].count[i] = 0;
+            sh.hist[row.turn].mass[i] = 0;  // (and so the places)
         }
         if (tid == 0) sh.listed = 0;
         __syncthreads();
@@ -466,45 +465,46 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
     for (int stage = k > 0 ? 0 : 1; stage < (by_p ? 2 : 1); ++stage) {
         const bool by_mass = stage == 1;
         u64 target = (u64)k, all = 0;
-        Range range = {0, kCodeBits};
+        Range range = {0, kCodeBits, kCodeBits - kBinBits};
         clear();
         if (!by_mass) {
             const uint32_t steps = steps_of(top, row.scale);
-            if (steps < row.limit) atomicAdd(&sh.hist.count[range.bin(code_of(steps, top))], 1u);
+            if (steps < row.limit) atomicAdd(&sh.hist[row.turn].count[range.bin(code_of(steps, top))], 1u);
             locate<kByCount>(row, target, 0.f, 0, all, sh, rank, C);
             if (sh.bin_count) {
-                row.limit = min(row.limit, (sh.bin + 1) << (kStepBits - 11));
+                row.limit = min(row.limit, (sh.bin + 1) << (kStepBits - kBinBits));
                 if (settle(row, range, (u64)k, by_p, 0, part, sh, rank, C)) return;
             }
             clear();
         } else {
             u64 near = 0;
-            u64 own = sweep<true>(row, 0, sure_steps(row), sh.hist.count, [&](int i, float x, uint32_t steps) {
+            u64 own = sweep<true>(row, 0, sure_steps(row), sh, [&](int i, float x, uint32_t steps) {
                 if (!kept(row, code_of(steps, x), row.base + i)) return;
                 near += mass_of(x, row.scale);
-                atomicAdd(&sh.hist.count[steps >> (kStepBits - 11)], 1u);
+                enter_bin(sh, row.turn, steps);
             });
             own += near;
             locate<kByBounds>(row, target, part, own, all, sh, rank, C);
             const uint32_t b1 = sh.bin, b2 = sh.bin_to;
-            range.width = kCodeBits - 11 + (b2 > b1 ? 32 - __clz((int)(b2 - b1)) : 0);
-            range.from = (u64)b1 << (kCodeBits - 11);
-            row.limit = min(row.limit, (b2 + 1) << (kStepBits - 11));
-            summed = b1 << (kStepBits - 11);
+            range.width = kCodeBits - kBinBits + (b2 > b1 ? 32 - __clz((int)(b2 - b1)) : 0);
+            range.from = (u64)b1 << (kCodeBits - kBinBits);
+            row.limit = min(row.limit, (b2 + 1) << (kStepBits - kBinBits));
+            summed = b1 << (kStepBits - kBinBits);
             all = 0;
             clear();
         }
         for (bool again = false;; again = true) {
-            const int shift = range.shift();
+            range.split();
+            const int shift = range.shift;
             auto enter = [&](int i, float x, uint32_t steps) {
                 const u64 code = code_of(steps, x);
                 if (!range.has(code) || !kept(row, code, row.base + i)) return;
                 const uint32_t at = range.bin(code);
-                atomicAdd(&sh.hist.count[at], 1u);
-                if (by_mass) atomicAdd(&sh.hist.mass[at], mass_of(x, row.scale));
+                atomicAdd(&sh.hist[row.turn].count[at], 1u);
+                if (by_mass) atomicAdd(&sh.hist[row.turn].mass[at], mass_of(x, row.scale));
             };
             const uint32_t first = (uint32_t)(range.from >> 32);
-            const u64 own = sweep<false>(row, by_mass && !again ? 0 : first, first, nullptr, enter);
+            const u64 own = sweep<false>(row, by_mass && !again ? 0 : first, first, sh, enter);
             if (by_mass && !again) below = own;
             if (by_mass) locate<kByMass>(row, target, 0.f, own, all, sh, rank, C);
             else locate<kByCount>(row, target, 0.f, 0, all, sh, rank, C);
@@ -532,9 +532,9 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
                 // index order
                 const u64 each = mass_of(bits_value(~(uint32_t)range.from), row.scale);
                 const u64 need = by_mass ? (rest + each - 1) / each : rest;
-                const uint32_t mine = sh.hist.count[bin];
+                const uint32_t mine = sh.hist[row.turn].count[bin];
                 uint32_t lower = 0;
-                for (uint32_t r = 0; r < rank; ++r) lower += ld_remote32(remote(&sh.hist.count[bin], r));
+                for (uint32_t r = 0; r < rank; ++r) lower += ld_remote32(remote(&sh.hist[row.turn].count[bin], r));
                 if (lower < need && need <= (u64)lower + mine) {
                     // thread by thread, as they lie
                     const int i0 = min(tid * row.len, row.n), i1 = min(i0 + row.len, row.n);
@@ -583,13 +583,19 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
     return x;
 }
 // NaN counts as -inf, -0 as +0.
-__device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
+__device__ __forceinline__ float clean(float x) { return fmaxf(x, -INFINITY) + 0.f; }
+
+// The most shared memory of a CTA: the longest slice fills 23 words of 16 bytes
+// a thread.
+constexpr int kSampleSmem = offset_slice() + 23 * 16 * kThreads;
+static_assert(kSampleSmem <= 232448 && kSampleMaxSlice <= 22 * 4 * kThreads, "shared memory of a CTA");
+constexpr size_t kSampleSmemOfTwo = 113 * 1024;
 
 template <int DT>
 __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared& sh = *reinterpret_cast<Shared*>(dyn);
-    float* xs = reinterpret_cast<float*>(dyn + offset_slice(p.C));
+    float* xs = reinterpret_cast<float*>(dyn + offset_slice());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int C = p.C, m = blockIdx.x / C;
@@ -607,11 +613,14 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     row.turn = 0;
     // the slice into shared memory; its largest logit, lowest index first
     const int64_t start = (int64_t)m * p.row_stride + row.base;
-    u64 best = 0;
-    auto see = [&](float x, int i) {
+    float own_top = -INFINITY;
+    int own_at = 0;
+    auto see = [&](float x, int i) {  // (a thread's indices ascend)
         xs[i] = x;
-        const u64 k = ((u64)value_bits(x) << 32) | (uint32_t)~(uint32_t)(row.base + i);
-        best = k > best ? k : best;
+        if (x > own_top) {
+            own_top = x;
+            own_at = i;
+        }
     };
     const uint8_t* src = static_cast<const uint8_t*>(p.logits) + start * (DT == 0 ? 4 : 2);
     constexpr int kVec = DT == 0 ? 4 : 8;
@@ -640,7 +649,7 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     }
     for (int i = nv * kVec + tid; i < row.n; i += kThreads) see(clean(load_logit<DT>(src, i)), i);
     for (int i = row.n + tid; i < row.len * kThreads; i += kThreads) xs[i] = -INFINITY;
-    float own_top = best ? bits_value((uint32_t)(best >> 32)) : -INFINITY;
+    u64 best = row.n > 0 ? ((u64)value_bits(own_top) << 32) | (uint32_t)~(uint32_t)(row.base + own_at) : 0;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const u64 other = __shfl_xor_sync(0xffffffffu, best, o);
@@ -699,7 +708,7 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     };
     u64 near = 0;
     const uint32_t from = summed <= sure ? summed : 0;
-    u64 own = sweep<false>(row, from, sure, nullptr, [&](int i, float x, uint32_t steps) { near += mass_at(i, x, steps); });
+    u64 own = sweep<false>(row, from, sure, sh, [&](int i, float x, uint32_t steps) { near += mass_at(i, x, steps); });
     own += near + (from ? below : 0);
     const int i0 = min(tid * row.len, row.n), i1 = min(i0 + row.len, row.n);
     u64 upto = own;  // of the warp's threads up to this one
@@ -753,24 +762,52 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
 
 }  // namespace
 
-cudaError_t launch_sample(const SampleParams& p, int M, int dtype, cudaStream_t stream) {
+// CTAs a row. Rows that can all be on the GPU at once are spread over as many
+// CTAs as can (a cluster of 8 of one CTA an SM fits 15 times on a GB300, of two
+// an SM 36 times: 16 rows of 157,184 logits in 9.7 us, 20 when one has to
+// wait), each with at least 2,048 logits; more rows in slices of which two fit
+// an SM.
+cudaError_t launch_sample(SampleParams p, int M, int dtype, cudaStream_t stream) {
     void (*kern)(SampleParams) = dtype == 0 ? sample_kernel<0> : sample_kernel<1>;
-    const int smem = offset_slice(p.C) + per_thread(p.slice) * kThreads * 4;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && p.C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(M * p.C));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.C;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    auto shape = [&](int C) {
+        p.C = C;
+        p.slice = ((p.V + C - 1) / C + 7) / 8 * 8;
+        cfg.dynamicSmemBytes = (size_t)offset_slice() + (size_t)per_thread(p.slice) * kThreads * 4;
+        attr[0].val.clusterDim.x = (unsigned)C;
+        cfg.gridDim = dim3((unsigned)((int64_t)M * C));
+        return p.slice <= kSampleMaxSlice;
+    };
+    // clusters of 2^i CTAs, j + 1 CTAs an SM, that are on the GPU at once
+    // (asked once; 0: not yet)
+    static std::atomic<int> active[5][2];
+    int best = 0;
+    for (int i = 4; i >= 0 && best == 0; --i) {
+        if (!shape(1 << i) || (i > 0 && p.V / (1 << i) < 2048)) continue;
+        std::atomic<int>& known = active[i][cfg.dynamicSmemBytes <= kSampleSmemOfTwo ? 1 : 0];
+        int n = known.load(std::memory_order_relaxed);
+        if (n == 0) {
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            if (e != cudaSuccess) return e;
+            known.store(n, std::memory_order_relaxed);
+        }
+        if (M <= n) best = 1 << i;
+    }
+    for (int C = 1; C <= 16 && best == 0; C *= 2)
+        if (shape(C) && (cfg.dynamicSmemBytes <= kSampleSmemOfTwo || C == 16)) best = C;
+    shape(best);
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
