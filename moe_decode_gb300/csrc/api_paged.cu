@@ -76,16 +76,18 @@ EncodeTiled encode_tiled() {
     return f;
 }
 
-// Tensor map of a cache: (d, token of the block, head, block), boxes of 64
-// dimensions by `box` tokens in the 128-byte swizzle.
-bool cache_map(CUtensorMap* m, const moe_kv_cache* c, void* base, int64_t bs, int64_t ts, int64_t hs, int box) {
+// Tensor map of a cache: (64 dimensions, token of the block, which 64, head,
+// block), boxes of `panels` times 64 dimensions by `box` tokens in the 128-byte
+// swizzle.
+bool cache_map(CUtensorMap* m, const moe_kv_cache* c, void* base, int64_t bs, int64_t ts, int64_t hs, int box,
+               int panels) {
     EncodeTiled enc = encode_tiled();
     if (!enc) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size, (cuuint64_t)c->kv_heads,
+    const cuuint64_t dims[5] = {64, (cuuint64_t)c->block_size, (cuuint64_t)(c->head_dim / 64), (cuuint64_t)c->kv_heads,
                                 (cuuint64_t)c->n_blocks};
-    const cuuint64_t strides[3] = {(cuuint64_t)ts * 2, (cuuint64_t)hs * 2, (cuuint64_t)bs * 2};
-    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
-    return enc(m, c->dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims,
+    const cuuint64_t strides[4] = {(cuuint64_t)ts * 2, 128, (cuuint64_t)hs * 2, (cuuint64_t)bs * 2};
+    const cuuint32_t boxes[5] = {64, (cuuint32_t)box, (cuuint32_t)panels, 1, 1}, steps[5] = {1, 1, 1, 1, 1};
+    return enc(m, c->dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, base, dims,
                strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -183,7 +185,7 @@ int moe_paged_append(const void* k_new, int64_t k_token_stride, int64_t k_head_s
 size_t moe_paged_attention_workspace_bytes(int q_heads, const moe_kv_cache* cache) {
     if (check_cache(cache) != MOE_OK) return 0;
     if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 32) return 0;
-    return MOE_PAGED_WORKSPACE_BYTES +
+    return MOE_PAGED_WORKSPACE_BYTES + 2 * MOE_MAX_GRID * sizeof(moe::AttnJoin) +
            (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows + moe::kAttnChunkRows, cache->head_dim) *
                sizeof(float);
 }
@@ -222,7 +224,8 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     p.q_start = q_start;
     p.seq = seq_lens;
     p.ctrl = static_cast<unsigned*>(ws);
-    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MOE_PAGED_WORKSPACE_BYTES);
+    p.joins = reinterpret_cast<moe::AttnJoin*>(static_cast<uint8_t*>(ws) + MOE_PAGED_WORKSPACE_BYTES);
+    p.part = reinterpret_cast<float*>(p.joins + 2 * MOE_MAX_GRID);
     p.chunk_part = p.part + (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows, cache->head_dim);
     p.q_token = q_token_stride;
     p.q_head = q_head_stride;
@@ -236,16 +239,22 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     p.n_blocks = cache->n_blocks;
     // copies of the largest power of two that divides the block: none ends
     // beyond a block, and a tile is a whole number of them
-    p.box = std::min(cache->block_size & -cache->block_size, moe::kAttnTile);
+    p.box_shift = std::min(__builtin_ctz((unsigned)cache->block_size), 7);
+    p.box = 1 << p.box_shift;
     p.window = window;
     p.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)cache->head_dim)) * 1.44269504088896341f;
     p.timeout_ns = (unsigned long long)g_opt.timeout_ns;
-    CUtensorMap k, v;
-    if (!cache_map(&k, cache, cache->k, cache->k_block_stride, cache->k_token_stride, cache->k_head_stride, p.box) ||
-        !cache_map(&v, cache, cache->v, cache->v_block_stride, cache->v_token_stride, cache->v_head_stride, p.box))
-        return MOE_ECUDA;
+    CUtensorMap maps[4];
+    for (int i = 0; i < (moe::attn_may_chunk(p) ? 4 : 2); ++i) {
+        const int panels = i < 2 ? cache->head_dim / 64 : 1;
+        const bool ok = i % 2 == 0 ? cache_map(&maps[i], cache, cache->k, cache->k_block_stride, cache->k_token_stride,
+                                               cache->k_head_stride, p.box, panels)
+                                   : cache_map(&maps[i], cache, cache->v, cache->v_block_stride, cache->v_token_stride,
+                                               cache->v_head_stride, p.box, panels);
+        if (!ok) return MOE_ECUDA;
+    }
     int n = 0;
-    const cudaError_t e = moe::launch_attn(p, &k, &v, cache->head_dim, cache->dtype, static_cast<cudaStream_t>(stream), &n);
+    const cudaError_t e = moe::launch_attn(p, maps, cache->head_dim, cache->dtype, static_cast<cudaStream_t>(stream), &n);
     return launched(e, n);
 }
 

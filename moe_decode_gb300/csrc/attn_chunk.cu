@@ -140,7 +140,10 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     pdl_wait();
     pdl_launch_dependents();
     const Place at = attn_place<Many, kThreads>(p, blockIdx.x, scan, found);
-    if (at.begin >= at.end) return;
+    if (at.begin >= at.end) {
+        if (tid == 0) p.joins[kAttnMaxGrid + blockIdx.x].rows = 0;
+        return;
+    }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_base))
                      : "memory");
@@ -155,52 +158,39 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == kLoadWarp) {
-            Walk<Many> walk(p, at);
             // lane i brings the tile's i-th box, if a row sees any of it; K of a
             // tile, then V
-            const int boxes = kAttnTile / p.box;
             int stage = 0, issued = 0;
             uint32_t parity = 1;
             bool ok = true;
-            for (; ok && walk.next(); walk.done()) {
-                if (walk.over && lane == 0)
-                    atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
-                const int32_t* table = p.tables + (int64_t)walk.r * p.max_blocks;
-                for (int t = walk.t0; ok && t < walk.t1; ++t) {
-                    const int key = (walk.tile0 + t) * kAttnTile + lane * p.box;
-                    bool take = lane < boxes && key < walk.hi && key + p.box > walk.lo;
-                    int block = 0, off = 0;
+            TileFeed<Many> feed(p, at, lane);
+            auto cur = feed.box(), next = cur;
+            for (bool more = feed.any; ok && more; cur = next) {
+                more = feed.advance();
+                if (more) next = feed.box();
+                const bool take = attn_take(p, cur.wanted, cur.block);
+                const int n = __popc(__ballot_sync(0xffffffffu, take));
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    ok = __all_sync(0xffffffffu, ok && attn_wait(empty + 8 * stage, parity, p, flag));
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 2));
+                    __syncwarp();
                     if (take) {
-                        const int page = key / p.block_size;
-                        off = key - page * p.block_size;
-                        block = table[page];
-                        if ((unsigned)block >= (unsigned)p.n_blocks) {
-                            atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
-                            take = false;
-                        }
+                        const uint32_t dst = base + S::kOffKv + stage * S::kTile + lane * p.box * 128;
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            attn_copy(dst + x * S::kPanel, kv ? &vmap : &kmap, x, cur.token, cur.head, cur.block,
+                                      full + 8 * stage);
                     }
-                    const int n = __popc(__ballot_sync(0xffffffffu, take));
-    #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        ok = __all_sync(0xffffffffu, ok && attn_wait(empty + 8 * stage, parity, p, flag));
-                        if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 2));
-                        __syncwarp();
-                        if (take) {
-                            const uint32_t dst = base + S::kOffKv + stage * S::kTile + lane * p.box * 128;
-    #pragma unroll
-                            for (int x = 0; x < D / 64; ++x)
-                                attn_copy(dst + x * S::kPanel, kv ? &vmap : &kmap, 64 * x, off, walk.head, block,
-                                          full + 8 * stage);
-                        }
-                        ++issued;
-                        if (++stage == S::kStages) {
-                            stage = 0;
-                            parity ^= 1u;
-                        }
+                    ++issued;
+                    if (++stage == S::kStages) {
+                        stage = 0;
+                        parity ^= 1u;
                     }
                 }
             }
+            if (lane == 0) p.joins[kAttnMaxGrid + blockIdx.x] = attn_span<Many>(p, at, blockIdx.x);
             if (!ok && lane == 0) {
                 // copies may be in flight: see the last ones land (again bounded)
                 for (int i = max(0, issued - S::kStages); i < issued; ++i) {

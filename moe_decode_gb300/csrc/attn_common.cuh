@@ -7,7 +7,9 @@
 // that the heads that share keys share the read. A unit is one tile of
 // kAttnTile keys of one item. All units of the call in the order request, kv
 // head, row tile, key tile are divided evenly: of G CTAs (or as many as there
-// are units) CTA c takes the units [cU/G, (c+1)U/G), whatever the lengths. An item whose units all lie in one CTA is
+// are units) CTA c takes the units [cU/G, (c+1)U/G), whatever the lengths. An
+// item's first units stand for what it costs beside its tiles (queries, joining
+// warps, output): a batch of short requests would otherwise be unevenly spread. An item whose units all lie in one CTA is
 // finished there; of one that spans CTAs each leaves its part (unnormalised
 // sums, largest score, sum of weights) in the workspace, and a second kernel
 // joins the parts in the order of the keys.
@@ -91,22 +93,23 @@ struct RowTiles {
 };
 
 // Units of a request for one kv head.
-template <int ROWS>
+template <class Class>
 __device__ __forceinline__ int64_t attn_request_units(const AttnParams& p, const Request& q) {
     int64_t u = 0;
-    for (RowTiles<ROWS> t(p, q); t.more(); t.next()) u += t.tiles();
+    for (RowTiles<Class::kRows> t(p, q); t.more(); t.next()) u += Class::kItem + t.tiles();
     return u;
 }
 
-// Which kernel takes a request.
+// Which kernel takes a request, the rows of its items, and the units that an
+// item costs beside its tiles.
 struct Few {
-    static constexpr int kRows = kAttnRows;
+    static constexpr int kRows = kAttnRows, kItem = 1;
     static __device__ __forceinline__ bool mine(const AttnParams& p, const Request& q) {
         return q.n > 0 && q.n * p.group <= kAttnFewRows;
     }
 };
 struct Many {
-    static constexpr int kRows = kAttnChunkRows;
+    static constexpr int kRows = kAttnChunkRows, kItem = 2;
     static __device__ __forceinline__ bool mine(const AttnParams& p, const Request& q) {
         return q.n * p.group > kAttnFewRows;
     }
@@ -126,7 +129,6 @@ struct Place {
 // two.
 template <class Class, int THREADS>
 __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_t* scan, int64_t* found) {
-    constexpr int ROWS = Class::kRows;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + THREADS - 1) / THREADS;
     const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
@@ -135,7 +137,7 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_
     for (int r = r0; r < r1; ++r) {
         const Request q = attn_request(p, r);
         bad |= q.bad;
-        if (Class::mine(p, q)) own += attn_request_units<ROWS>(p, q) * p.kv_heads;
+        if (Class::mine(p, q)) own += attn_request_units<Class>(p, q) * p.kv_heads;
     }
     if (bad) atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
     int64_t sum = own;
@@ -163,7 +165,7 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_
     if (own > 0 && before <= at.begin && at.begin < before + own) {
         for (int r = r0; r < r1; ++r) {
             const Request q = attn_request(p, r);
-            const int64_t u = Class::mine(p, q) ? attn_request_units<ROWS>(p, q) * p.kv_heads : 0;
+            const int64_t u = Class::mine(p, q) ? attn_request_units<Class>(p, q) * p.kv_heads : 0;
             if (at.begin < before + u) {
                 found[0] = r;
                 found[1] = at.begin - before;
@@ -186,7 +188,7 @@ struct Walk {
     const AttnParams& p;
     int64_t unit, end;  // next unit of the range
     int r, head, row0;
-    int skip;           // tiles of the item at hand before the range
+    int skip;           // units of the item at hand before the range
     Request q;
     // the item at hand
     int rows, lo, hi, tile0, tiles;
@@ -197,11 +199,11 @@ struct Walk {
         : p(params), unit(at.begin), end(at.end), r(at.request), head(0), row0(0), skip(0) {
         if (unit >= end) return;
         q = attn_request(p, r);
-        const int64_t per_head = attn_request_units<ROWS>(p, q);
+        const int64_t per_head = attn_request_units<Class>(p, q);
         head = (int)(at.rest / per_head);
         int64_t rest = at.rest - head * per_head;
         RowTiles<ROWS> t(p, q);
-        for (; rest >= t.tiles(); t.next()) rest -= t.tiles();
+        for (; rest >= Class::kItem + t.tiles(); t.next()) rest -= Class::kItem + t.tiles();
         row0 = t.row0;
         skip = (int)rest;
     }
@@ -211,16 +213,16 @@ struct Walk {
         tile0 = lo / kAttnTile;
         tiles = attn_tiles(lo, hi);
     }
-    // The next item into the fields; false at the end of the range.
+    // The next item with tiles in the range into the fields; false at the end.
     __device__ __forceinline__ bool next() {
         if (unit >= end) return false;
         item();
-        t0 = skip;
-        t1 = (int)min((int64_t)tiles, t0 + (end - unit));
-        return true;
+        t0 = max(skip - Class::kItem, 0);
+        t1 = (int)min((int64_t)tiles, skip - Class::kItem + (end - unit));
+        return t1 > t0;  // (only the last item may have none)
     }
     __device__ __forceinline__ void done() {
-        unit += t1 - t0;
+        unit += Class::kItem + tiles - skip;
         skip = 0;
         if (unit >= end) return;
         row0 += ROWS;
@@ -238,6 +240,30 @@ struct Walk {
     __device__ __forceinline__ int part() const { return t0 > 0 ? 0 : 1; }
 };
 
+// What the join kernel needs of the item at the end of the CTA's range, if it
+// goes on past it. One thread, after the walk.
+template <class Class>
+__device__ __forceinline__ AttnJoin attn_span(const AttnParams& p, const Place& at, int cta) {
+    AttnJoin j = {};
+    if (at.begin >= at.end || at.end >= at.total) return j;
+    Walk<Class> walk(p, at);
+    while (walk.next()) {
+        if (walk.t1 < walk.tiles) {
+            if (walk.t0 > 0) return j;  // began earlier
+            // the CTA of its last unit u: the largest k with kU/G <= u
+            const int64_t u = walk.unit - walk.skip + Class::kItem + walk.tiles - 1;
+            j.parts = (int)(((u + 1) * at.ctas - 1) / at.total) - cta + 1;
+            j.rows = walk.rows;
+            j.token0 = walk.q.q0;
+            j.row0 = walk.row0;
+            j.head = walk.head;
+            return j;
+        }
+        walk.done();
+    }
+    return j;
+}
+
 // Waits for the phase with parity `parity`, at most timeout_ns; false, with
 // the status and `flag` set, when it ran out or another wait of the CTA did.
 __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const AttnParams& p, volatile int* flag) {
@@ -254,16 +280,68 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const A
     return true;
 }
 
-// One box of a cache's tensor map (dimensions d, token of the block, head,
-// block) into shared memory: `box` keys by 64 dimensions, 128 bytes a key in
-// the 128-byte swizzle. x (0 or 64) is 16-byte aligned in either case.
-__device__ __forceinline__ void attn_copy(uint32_t dst, const CUtensorMap* map, int x, int token, int head, int block,
-                                          uint32_t bar) {
+// One box of a cache's tensor map (64 dimensions, token of the block, which 64,
+// head, block) into shared memory: `box` keys, 128 bytes a key in the 128-byte
+// swizzle, one panel of 64 dimensions after another. The innermost coordinate
+// is always 0.
+__device__ __forceinline__ void attn_copy(uint32_t dst, const CUtensorMap* map, int panel, int token, int head,
+                                          int block, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(token), "r"(head), "r"(block), "r"(bar)
+        "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(token), "r"(panel), "r"(head), "r"(block), "r"(bar)
         : "memory");
+}
+
+// The producers' order of tiles: the box that this lane brings of the tile at
+// hand. The block number is asked for one tile ahead of its use.
+template <class Class>
+struct TileFeed {
+    Walk<Class> walk;
+    int t, lane;
+    bool any;  // whether the range has a tile
+    __device__ __forceinline__ TileFeed(const AttnParams& p, const Place& at, int l) : walk(p, at), t(0), lane(l) {
+        any = walk.next();
+        if (any) start();
+    }
+    __device__ __forceinline__ void start() {
+        t = walk.t0;
+        if (walk.over && lane == 0)
+            atomicCAS(reinterpret_cast<int*>(walk.p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
+    }
+    struct Box {
+        int block, token, head;
+        bool wanted;  // a row sees some of it
+    };
+    __device__ __forceinline__ Box box() const {
+        const AttnParams& p = walk.p;
+        Box b;
+        const int key = (walk.tile0 + t) * kAttnTile + lane * p.box;
+        b.wanted = any && lane < kAttnTile / p.box && key < walk.hi && key + p.box > walk.lo;
+        b.head = walk.head;
+        b.block = b.token = 0;
+        if (b.wanted) {
+            const int page = key / p.block_size;
+            b.token = key - page * p.block_size;
+            b.block = p.tables[(int64_t)walk.r * p.max_blocks + page];
+        }
+        return b;
+    }
+    __device__ __forceinline__ bool advance() {  // false after the last tile
+        if (++t < walk.t1) return true;
+        walk.done();
+        if (!walk.next()) return false;
+        start();
+        return true;
+    }
+};
+// Whether the box is copied: wanted and in a block that there is.
+__device__ __forceinline__ bool attn_take(const AttnParams& p, bool wanted, int block) {
+    if (wanted && (unsigned)block >= (unsigned)p.n_blocks) {
+        atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
+        return false;
+    }
+    return wanted;
 }
 
 // Two fp32 into one register of the type, `lo` in the low half (one rounding).

@@ -14,8 +14,7 @@ constexpr int kWarpKeys = kAttnTile / kKeyWarps;
 
 template <int D>
 struct DecodeShape {
-    static constexpr int kPanel = kAttnTile * 128;           // 64 dimensions of a tile's keys
-    static constexpr int kHalf = kPanel * (D / 64);          // K (or V) of a tile
+    static constexpr int kHalf = kAttnTile * D * 2;          // K (or V) of a tile
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kQ = kRows * D * 2;
@@ -72,55 +71,40 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     pdl_wait();
     pdl_launch_dependents();
     const Place at = attn_place<Few, kThreads>(p, blockIdx.x, scan, found);
-    if (at.begin >= at.end) return;
+    if (at.begin >= at.end) {
+        if (tid == 0) p.joins[blockIdx.x].rows = 0;
+        return;
+    }
     volatile int* flag = &abort_flag;
-    Walk<Few> walk(p, at);
 
     if (warp == kConsumers) {
         // producer: lane i brings the tile's i-th box, if a row sees any of it
-        const int boxes = kAttnTile / p.box;
         int stage = 0, issued = 0;
         uint32_t parity = 1;
         bool ok = true;
-        for (; ok && walk.next(); walk.done()) {
-            if (walk.over && lane == 0)
-                atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
-            const int32_t* table = p.tables + (int64_t)walk.r * p.max_blocks;
-            for (int t = walk.t0; t < walk.t1; ++t) {
-                const int key = (walk.tile0 + t) * kAttnTile + lane * p.box;
-                bool take = lane < boxes && key < walk.hi && key + p.box > walk.lo;
-                int block = 0, off = 0;
-                if (take) {
-                    const int page = key / p.block_size;
-                    off = key - page * p.block_size;
-                    block = table[page];
-                    if ((unsigned)block >= (unsigned)p.n_blocks) {
-                        atomicCAS(reinterpret_cast<int*>(p.ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
-                        take = false;
-                    }
-                }
-                ok = attn_wait(empty + 8 * stage, parity, p, flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const int n = __popc(__ballot_sync(0xffffffffu, take));
-                if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 4));
-                __syncwarp();
-                if (take) {
-                    const uint32_t dst = base + stage * S::kStage + lane * p.box * 128;
-#pragma unroll
-                    for (int x = 0; x < D / 64; ++x) {
-                        attn_copy(dst + x * S::kPanel, &kmap, 64 * x, off, walk.head, block, full + 8 * stage);
-                        attn_copy(dst + S::kHalf + x * S::kPanel, &vmap, 64 * x, off, walk.head, block,
-                                  full + 8 * stage);
-                    }
-                }
-                ++issued;
-                if (++stage == S::kStages) {
-                    stage = 0;
-                    parity ^= 1u;
-                }
+        TileFeed<Few> feed(p, at, lane);
+        auto cur = feed.box(), next = cur;
+        for (bool more = feed.any; more; cur = next) {
+            more = feed.advance();
+            if (more) next = feed.box();
+            ok = __all_sync(0xffffffffu, attn_wait(empty + 8 * stage, parity, p, flag));
+            if (!ok) break;
+            const bool take = attn_take(p, cur.wanted, cur.block);
+            const int n = __popc(__ballot_sync(0xffffffffu, take));
+            if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 4));
+            __syncwarp();
+            if (take) {
+                const uint32_t dst = base + stage * S::kStage + lane * p.box * D * 2;
+                attn_copy(dst, &kmap, 0, cur.token, cur.head, cur.block, full + 8 * stage);
+                attn_copy(dst + S::kHalf, &vmap, 0, cur.token, cur.head, cur.block, full + 8 * stage);
+            }
+            ++issued;
+            if (++stage == S::kStages) {
+                stage = 0;
+                parity ^= 1u;
             }
         }
+        if (lane == 0) p.joins[blockIdx.x] = attn_span<Few>(p, at, blockIdx.x);
         if (!ok && lane == 0) {
             // copies may be in flight: see the last ones land (again bounded)
             for (int i = max(0, issued - S::kStages); i < issued; ++i) {
@@ -133,8 +117,19 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
         return;
     }
 
+    Walk<Few> walk(p, at);
     const int quad = lane >> 2, pair = lane & 3;
     const int set = warp / kKeyWarps, kw = warp % kKeyWarps;  // rows [16 set, 16 set + 16), a quarter of the keys
+    // a key's row in a stage: boxes of `box` keys, in each the panels of 64
+    // dimensions one after another
+    const int panel = p.box * 128;
+    auto key_at = [&](int key) { return (key >> p.box_shift) * (p.box * D * 2) + (key & (p.box - 1)) * 128; };
+    int k_at[2], v_at[2];  // rows that this lane names to ldmatrix, of 16 keys each
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        k_at[h] = key_at(kw * kWarpKeys + h * 16 + ((lane >> 4) << 3) + (lane & 7));
+        v_at[h] = key_at(kw * kWarpKeys + h * 16 + (lane & 15));
+    }
     int stage = 0;
     uint32_t parity = 0;
     uint8_t* qs = sm + S::kOffQ;
@@ -175,7 +170,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
         for (int t = walk.t0; t < walk.t1; ++t) {
             if (!attn_wait(full + 8 * stage, parity, p, flag)) break;
             const int key0 = (walk.tile0 + t) * kAttnTile + kw * kWarpKeys;
-            const uint32_t ks = base + stage * S::kStage + kw * kWarpKeys * 128, vs = ks + S::kHalf;
+            const uint32_t ks = base + stage * S::kStage, vs = ks + S::kHalf;
             if (active && key0 < walk.hi && key0 + kWarpKeys > walk.lo) {
                 const bool ragged = key0 < walk.lo || key0 + kWarpKeys > walk.hi;
                 if (ragged) {
@@ -184,12 +179,12 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                     // each before its own reads)
                     const int key = key0 + lane;
                     if (key < walk.lo || key >= walk.hi) {
-                        uint8_t* v = sm + stage * S::kStage + S::kHalf + (kw * kWarpKeys + lane) * 128;
+                        uint8_t* v = sm + stage * S::kStage + S::kHalf + key_at(kw * kWarpKeys + lane);
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
-                                *reinterpret_cast<uint4*>(v + x * S::kPanel + c * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(v + x * panel + c * 16) = make_uint4(0, 0, 0, 0);
                     }
                     __syncwarp();
                 }
@@ -207,8 +202,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 16 keys each
-                        const int row = h * 16 + ((lane >> 4) << 3) + (lane & 7), c = 2 * (k & 3) + ((lane >> 3) & 1);
-                        ldsm_x4(ks + (k >> 2) * S::kPanel + row * 128 + ((c ^ (row & 7)) << 4), kb[h]);
+                        const int c = 2 * (k & 3) + ((lane >> 3) & 1);
+                        ldsm_x4(ks + k_at[h] + (k >> 2) * panel + ((c ^ (lane & 7)) << 4), kb[h]);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -264,8 +259,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         uint32_t vb[4];
-                        const int row = h * 16 + (lane & 15), c = 2 * (i & 3) + (lane >> 4);
-                        ldsm_x4_trans(vs + (i >> 2) * S::kPanel + row * 128 + ((c ^ (row & 7)) << 4), vb);
+                        const int c = 2 * (i & 3) + (lane >> 4);
+                        ldsm_x4_trans(vs + v_at[h] + (i >> 2) * panel + ((c ^ (lane & 7)) << 4), vb);
                         mma_16816<DT>(o[2 * i], pa[h], vb[0], vb[1]);
                         mma_16816<DT>(o[2 * i + 1], pa[h], vb[2], vb[3]);
                     }
@@ -360,44 +355,27 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     }
 }
 
-// Joins the parts of the item of CTA c that goes on past the CTA's end (there
-// is at most one that begins there), part after part in the order of the
-// keys: kAttnRows rows from row `from` on.
-template <int D, int DT, class Class>
-__device__ __forceinline__ void join(const AttnParams& p, const float* parts, int c, int from, int64_t* scan,
-                                     int64_t* found) {
-    constexpr int ROWS = Class::kRows;
+// Joins the parts of the item that spans from CTA c, part after part in the
+// order of the keys (the part 1 of CTA c, then the part 0 of the CTAs after it):
+// kAttnRows rows from row `from` on.
+template <int D, int DT, int ROWS>
+__device__ __forceinline__ void join(const AttnParams& p, const AttnJoin& j, const float* parts, int c, int from) {
     const int tid = threadIdx.x;
-    const Place at = attn_place<Class, 128>(p, c, scan, found);
-    if (at.begin >= at.end || at.end >= at.total) return;
-    Walk<Class> walk(p, at);
-    // the last item of the range
-    bool spans = false;
-    while (walk.next()) {
-        spans = walk.t0 == 0 && walk.t1 < walk.tiles;
-        if (walk.unit + (walk.t1 - walk.t0) >= walk.end) break;
-        walk.done();
-    }
-    if (!spans || from >= walk.rows) return;
-    // its parts: CTA c's part 1, then part 0 of the CTAs up to that of its
-    // last unit u, the largest k with kU/G <= u
-    const int64_t u = at.end + (walk.tiles - walk.t1) - 1;
-    const int n = (int)(((u + 1) * at.ctas - 1) / at.total) - c + 1;
     constexpr int kFloats = attn_part_floats(ROWS, D);
     const float* first = parts + ((int64_t)c * 2 + 1) * kFloats;
     const float* rest = parts + (int64_t)c * 2 * kFloats;  // part 0 of CTA c + k at k * 2 * kFloats
     auto part_of = [&](int k) { return k == 0 ? first : rest + (int64_t)k * 2 * kFloats; };
     constexpr int kPer = D / 8;
-    const int to = min(from + kAttnRows, walk.rows);
+    const int to = min(from + kAttnRows, j.rows);
     for (int i = tid + from * kPer; i < to * kPer; i += 128) {
         const int row = i / kPer, d = (i % kPer) * 8;
         float mx = -INFINITY, sum = 0.f;
 #pragma unroll 4
-        for (int k = 0; k < n; ++k) mx = fmaxf(mx, reinterpret_cast<const float2*>(part_of(k) + ROWS * D)[row].x);
+        for (int k = 0; k < j.parts; ++k) mx = fmaxf(mx, reinterpret_cast<const float2*>(part_of(k) + ROWS * D)[row].x);
         const float ref = mx == -INFINITY ? 0.f : mx;
         float v[8] = {};
 #pragma unroll 4
-        for (int k = 0; k < n; ++k) {
+        for (int k = 0; k < j.parts; ++k) {
             const float* f = part_of(k);
             const float2 ml = reinterpret_cast<const float2*>(f + ROWS * D)[row];
             const float w = exp2_approx(ml.x - ref);
@@ -408,8 +386,8 @@ __device__ __forceinline__ void join(const AttnParams& p, const float* parts, in
             v[4] += w * y.x; v[5] += w * y.y; v[6] += w * y.z; v[7] += w * y.w;
         }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int R = walk.row0 + row, t = R / p.group, h = walk.head * p.group + (R - t * p.group);
-        const int64_t at_row = (int64_t)(walk.q.q0 + t) * p.heads + h;
+        const int R = j.row0 + row, t = R / p.group, h = j.head * p.group + (R - t * p.group);
+        const int64_t at_row = (int64_t)(j.token0 + t) * p.heads + h;
         uint4 o;
         o.x = pack2<DT>(v[0] * inv, v[1] * inv);
         o.y = pack2<DT>(v[2] * inv, v[3] * inv);
@@ -425,22 +403,25 @@ __device__ __forceinline__ void join(const AttnParams& p, const float* parts, in
 // kernel's (only there when that kernel ran).
 template <int D, int DT>
 __global__ __launch_bounds__(128) void attn_join_kernel(const __grid_constant__ AttnParams p) {
-    __shared__ int64_t scan[4], found[2];
     pdl_wait();
     pdl_launch_dependents();
+    const int c = blockIdx.x;
     if (blockIdx.y > 0) {
-        join<D, DT, Many>(p, p.chunk_part, blockIdx.x, (blockIdx.y - 1) * kAttnRows, scan, found);
+        const int from = ((int)blockIdx.y - 1) * kAttnRows;
+        const AttnJoin j = p.joins[kAttnMaxGrid + c];
+        if (from < j.rows) join<D, DT, kAttnChunkRows>(p, j, p.chunk_part, c, from);
         return;
     }
+    const AttnJoin j = p.joins[c];
     const int lane = threadIdx.x & 31;
     const int last = min(max(p.q_start[p.B], 0), p.T);
-    for (int64_t i = (int64_t)last * p.heads + blockIdx.x * 4 + (threadIdx.x >> 5); i < (int64_t)p.T * p.heads;
+    if (j.rows > 0) join<D, DT, kAttnRows>(p, j, p.part, c, 0);
+    for (int64_t i = (int64_t)last * p.heads + c * 4 + (threadIdx.x >> 5); i < (int64_t)p.T * p.heads;
          i += (int64_t)gridDim.x * 4) {
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) reinterpret_cast<uint32_t*>(p.out + i * D)[32 * x + lane] = 0u;
         if (p.lse && lane == 0) p.lse[i] = -INFINITY;
     }
-    join<D, DT, Few>(p, p.part, blockIdx.x, 0, scan, found);
 }
 
 template <class... Args>
@@ -463,33 +444,30 @@ cudaError_t launch(void (*kern)(Args...), dim3 grid, int threads, int smem, cuda
 }
 
 template <int D, int DT>
-cudaError_t launch_typed(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream,
-                         int* launches) {
-    cudaError_t e =
-        launch(attn_decode_kernel<D, DT>, dim3((unsigned)p.G), kThreads, DecodeShape<D>::kBytes, stream, p, k, v);
+cudaError_t launch_typed(const AttnParams& p, const CUtensorMap* maps, cudaStream_t stream, int* launches) {
+    cudaError_t e = launch(attn_decode_kernel<D, DT>, dim3((unsigned)p.G), kThreads, DecodeShape<D>::kBytes, stream, p,
+                           maps[0], maps[1]);
     if (e != cudaSuccess) return e;
     ++*launches;
-    const bool many = (int64_t)p.T * p.group > kAttnFewRows;
-    if (many) {
-        e = launch_attn_chunk(p, &k, &v, D, DT, stream);
+    const bool chunk = attn_may_chunk(p);
+    if (chunk) {
+        e = launch_attn_chunk(p, &maps[2], &maps[3], D, DT, stream);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
-    e = launch(attn_join_kernel<D, DT>, dim3((unsigned)p.G, many ? 1 + kAttnChunkRows / kAttnRows : 1), 128, 0, stream, p);
+    e = launch(attn_join_kernel<D, DT>, dim3((unsigned)p.G, chunk ? 1 + kAttnChunkRows / kAttnRows : 1), 128, 0, stream, p);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
 
 }  // namespace
 
-cudaError_t launch_attn(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
-                        cudaStream_t stream, int* launches) {
-    const CUtensorMap& k = *static_cast<const CUtensorMap*>(k_map);
-    const CUtensorMap& v = *static_cast<const CUtensorMap*>(v_map);
+cudaError_t launch_attn(const AttnParams& p, const void* maps, int head_dim, int dtype, cudaStream_t stream,
+                        int* launches) {
+    const CUtensorMap* m = static_cast<const CUtensorMap*>(maps);
     *launches = 0;
-    if (head_dim == 128)
-        return dtype == 0 ? launch_typed<128, 0>(p, k, v, stream, launches) : launch_typed<128, 1>(p, k, v, stream, launches);
-    return dtype == 0 ? launch_typed<64, 0>(p, k, v, stream, launches) : launch_typed<64, 1>(p, k, v, stream, launches);
+    if (head_dim == 128) return dtype == 0 ? launch_typed<128, 0>(p, m, stream, launches) : launch_typed<128, 1>(p, m, stream, launches);
+    return dtype == 0 ? launch_typed<64, 0>(p, m, stream, launches) : launch_typed<64, 1>(p, m, stream, launches);
 }
 
 }  // namespace moe

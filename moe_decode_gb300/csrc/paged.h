@@ -61,6 +61,15 @@ constexpr int kAttnChunkRows = 256; // and of the chunk kernel
 constexpr int kAttnFewRows = 64;
 constexpr int kAttnMaxGrid = 256;   // CTAs of a launch (workspace sizing)
 
+// The part of an item that spans CTAs, left by the CTA in which it begins.
+struct AttnJoin {
+    int rows;    // 0: no item spans from this CTA
+    int parts;   // CTAs that hold a part of it
+    int token0;  // first token row of the request
+    int row0, head;
+    int pad[3];
+};
+
 struct AttnParams {
     const uint16_t* q;
     uint16_t* out;
@@ -71,21 +80,25 @@ struct AttnParams {
     unsigned* ctrl;
     float* part;        // partial results of items that span CTAs, [G][2]
     float* chunk_part;  // and those of the chunk kernel's
+    AttnJoin* joins;    // [2][kAttnMaxGrid]: of the decode kernel, of the chunk kernel
     int64_t q_token, q_head;
     int T, B, heads, kv_heads, group;
     int max_blocks, block_size, n_blocks;
-    int box;     // keys that one copy brings
+    int box, box_shift;  // keys that one copy brings, as a power of two
     int window;
     int G;       // CTAs
     float scale_log2;  // scale * log2(e)
     unsigned long long timeout_ns;
 };
 
-// Key and value maps are CUtensorMaps. The decode kernel and the join
-// of all parts; the chunk kernel (between the two, where any request may have
-// many rows).
-cudaError_t launch_attn(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
-                        cudaStream_t stream, int* launches);
+// Whether any request of the call may have many rows.
+inline bool attn_may_chunk(const AttnParams& p) { return (int64_t)p.T * p.group > kAttnFewRows; }
+// The decode kernel, the chunk kernel (where any request may have many rows)
+// and the join of all parts. maps: CUtensorMaps of K and V whose boxes hold all
+// dimensions of `box` keys, then of K and V in boxes of 64 dimensions (for the
+// chunk kernel alone).
+cudaError_t launch_attn(const AttnParams& p, const void* maps, int head_dim, int dtype, cudaStream_t stream,
+                        int* launches);
 cudaError_t launch_attn_chunk(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
                               cudaStream_t stream);
 // Floats of one partial result of `rows` rows.
