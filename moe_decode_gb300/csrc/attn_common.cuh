@@ -312,6 +312,9 @@ struct TileFeed {
     struct Box {
         int block, token, head;
         bool wanted;  // a row sees some of it
+        // with the item's first tile: its rows, the first of them, and the
+        // request's first token row (else rows is 0)
+        int rows, row0, token0;
     };
     __device__ __forceinline__ Box box() const {
         const AttnParams& p = walk.p;
@@ -319,6 +322,9 @@ struct TileFeed {
         const int key = (walk.tile0 + t) * kAttnTile + lane * p.box;
         b.wanted = any && lane < kAttnTile / p.box && key < walk.hi && key + p.box > walk.lo;
         b.head = walk.head;
+        b.rows = any && t == walk.t0 ? walk.rows : 0;
+        b.row0 = walk.row0;
+        b.token0 = walk.q.q0;
         b.block = b.token = 0;
         if (b.wanted) {
             const int page = key / p.block_size;

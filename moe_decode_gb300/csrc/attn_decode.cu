@@ -17,14 +17,24 @@ struct DecodeShape {
     static constexpr int kHalf = kAttnTile * D * 2;          // K (or V) of a tile
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kQ = kRows * D * 2;
+    static constexpr int kQRow = D * 2 + 16;                 // eight rows' 16-byte pieces in different banks
+    static constexpr int kQ = kRows * kQRow;                 // queries of an item, of two in turn
     static constexpr int kMerge = kRows * (D + 4) * 4;
     static constexpr int kOffQ = kStages * kStage;
-    static constexpr int kOffMerge = kOffQ + kQ;
+    static constexpr int kOffMerge = kOffQ + 2 * kQ;
     static constexpr int kOffStat = kOffMerge + kMerge;      // largest score and sum of each warp's rows
     static constexpr int kOffBar = kOffStat + kKeyWarps * kRows * 8;
-    static constexpr int kBytes = kOffBar + 256 + 1024;      // and room to align
+    static constexpr int kOffMisc = kOffBar + 16 * (kStages + 2);
+    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + 16 + 8;
+    static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
+
+// One row of queries (16-byte aligned at both ends) into shared memory.
+__device__ __forceinline__ void copy_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
 template <int DT>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -53,18 +63,26 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                                                                    const __grid_constant__ CUtensorMap kmap,
                                                                    const __grid_constant__ CUtensorMap vmap) {
     using S = DecodeShape<D>;
-    extern __shared__ uint8_t dyn[];
-    __shared__ int64_t scan[kThreads / 32], found[2];
-    __shared__ int abort_flag;
-    const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-    uint8_t* sm = dyn + (base - smem_u32(dyn));
+    // (no static shared memory: this begins on a 1024-byte boundary, which the
+    // swizzle counts from)
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t base = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // barriers: key/value stages and queries, each full and empty
     const uint32_t full = base + S::kOffBar, empty = full + 8 * S::kStages;
+    const uint32_t q_full = empty + 8 * S::kStages, q_empty = q_full + 16;
+    int64_t* scan = reinterpret_cast<int64_t*>(sm + S::kOffMisc);
+    int64_t* found = scan + kThreads / 32;
+    int& abort_flag = *reinterpret_cast<int*>(found + 2);
     if (tid == 0) {
         abort_flag = 0;
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, kConsumers);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 1);
+            mbar_init(q_empty + 8 * i, kConsumers);
         }
         fence_mbar_init();
     }
@@ -80,13 +98,27 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     if (warp == kConsumers) {
         // producer: lane i brings the tile's i-th box, if a row sees any of it
         int stage = 0, issued = 0;
-        uint32_t parity = 1;
+        uint32_t parity = 1, items = 0;
         bool ok = true;
         TileFeed<Few> feed(p, at, lane);
         auto cur = feed.box(), next = cur;
         for (bool more = feed.any; more; cur = next) {
             more = feed.advance();
             if (more) next = feed.box();
+            if (cur.rows > 0) {
+                // the item's queries, a row a lane
+                const uint32_t i = items & 1u;
+                ok = __all_sync(0xffffffffu, attn_wait(q_empty + 8 * i, ((items >> 1) & 1u) ^ 1u, p, flag));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * i, (uint32_t)(cur.rows * D * 2));
+                __syncwarp();
+                if (lane < cur.rows) {
+                    const int R = cur.row0 + lane, t = R / p.group, h = cur.head * p.group + (R - t * p.group);
+                    copy_row(base + S::kOffQ + i * S::kQ + lane * S::kQRow,
+                             p.q + (cur.token0 + t) * p.q_token + h * p.q_head, D * 2, q_full + 8 * i);
+                }
+                ++items;
+            }
             ok = __all_sync(0xffffffffu, attn_wait(empty + 8 * stage, parity, p, flag));
             if (!ok) break;
             const bool take = attn_take(p, cur.wanted, cur.block);
@@ -113,6 +145,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                        global_timer_ns() - t0 < p.timeout_ns) {
                 }
             }
+            for (uint32_t i = items > 2 ? items - 2 : 0; i < items; ++i) {
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(q_full + 8 * (i & 1u), (i >> 1) & 1u) && global_timer_ns() - t0 < p.timeout_ns) {
+                }
+            }
         }
         return;
     }
@@ -132,23 +169,14 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     }
     int stage = 0;
     uint32_t parity = 0;
-    uint8_t* qs = sm + S::kOffQ;
-    const uint32_t q_addr = base + S::kOffQ + set * 16 * (D * 2);
+    uint32_t items = 0;
     float2* stat = reinterpret_cast<float2*>(sm + S::kOffStat);  // [key warp][row]
     float* merge = reinterpret_cast<float*>(sm + S::kOffMerge);  // [row][D + 4]
     for (; walk.next(); walk.done()) {
-        // the item's rows into shared memory, 16-byte pieces swizzled like the
-        // keys; rows past the end are zeros
-        for (int i = tid; i < kRows * (D / 8); i += kConsumers * 32) {
-            const int row = i / (D / 8), c = i % (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < walk.rows) {
-                const int R = walk.row0 + row, t = R / p.group, h = walk.head * p.group + (R - t * p.group);
-                v = *reinterpret_cast<const uint4*>(p.q + (walk.q.q0 + t) * p.q_token + h * p.q_head + c * 8);
-            }
-            *reinterpret_cast<uint4*>(qs + row * (D * 2) + ((c ^ (row & 7)) << 4)) = v;
-        }
-        named_bar_sync(1, kConsumers * 32);
+        // (rows past the item's last hold anything; a row's results depend on
+        // no other row)
+        const uint32_t q_addr = base + S::kOffQ + (items & 1u) * S::kQ + (set * 16 + (lane & 15)) * S::kQRow + (lane >> 4) * 16;
+        bool ok = attn_wait(q_full + 8 * (items & 1u), (items >> 1) & 1u, p, flag);
         const bool active = set * 16 < walk.rows;
         // the last key that each of this thread's two rows sees, and the first
         int last[2], from[2];
@@ -168,7 +196,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
         for (int t = walk.t0; t < walk.t1; ++t) {
-            if (!attn_wait(full + 8 * stage, parity, p, flag)) break;
+            ok = ok && attn_wait(full + 8 * stage, parity, p, flag);
+            if (!ok) break;
             const int key0 = (walk.tile0 + t) * kAttnTile + kw * kWarpKeys;
             const uint32_t ks = base + stage * S::kStage, vs = ks + S::kHalf;
             if (active && key0 < walk.hi && key0 + kWarpKeys > walk.lo) {
@@ -196,10 +225,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t qa[4], kb[2][4];
-                    {
-                        const int row = lane & 15, c = 2 * k + (lane >> 4);
-                        ldsm_x4(q_addr + row * (D * 2) + ((c ^ (row & 7)) << 4), qa);
-                    }
+                    ldsm_x4(q_addr + k * 32, qa);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 16 keys each
                         const int c = 2 * (k & 3) + ((lane >> 3) & 1);
@@ -273,6 +299,9 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 parity ^= 1u;
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty + 8 * (items & 1u));
+        ++items;
         // join the warps that share the rows: each scales to the largest score
         // of all, then they add up one after another
 #pragma unroll
