@@ -103,7 +103,7 @@ __device__ __forceinline__ int64_t attn_request_units(const AttnParams& p, const
 // Which kernel takes a request, the rows of its items, and the units that an
 // item costs beside its tiles.
 struct Few {
-    static constexpr int kRows = kAttnRows, kItem = 1;
+    static constexpr int kRows = kAttnRows, kItem = 2;
     static __device__ __forceinline__ bool mine(const AttnParams& p, const Request& q) {
         return q.n > 0 && q.n * p.group <= kAttnFewRows;
     }
