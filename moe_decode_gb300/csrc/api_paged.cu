@@ -185,7 +185,7 @@ int moe_paged_append(const void* k_new, int64_t k_token_stride, int64_t k_head_s
 size_t moe_paged_attention_workspace_bytes(int q_heads, const moe_kv_cache* cache) {
     if (check_cache(cache) != MOE_OK) return 0;
     if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 32) return 0;
-    return MOE_PAGED_WORKSPACE_BYTES + 2 * MOE_MAX_GRID * sizeof(moe::AttnJoin) +
+    return MOE_PAGED_WORKSPACE_BYTES + 3 * MOE_MAX_GRID * sizeof(unsigned) +
            (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows + moe::kAttnChunkRows, cache->head_dim) *
                sizeof(float);
 }
@@ -224,8 +224,8 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     p.q_start = q_start;
     p.seq = seq_lens;
     p.ctrl = static_cast<unsigned*>(ws);
-    p.joins = reinterpret_cast<moe::AttnJoin*>(static_cast<uint8_t*>(ws) + MOE_PAGED_WORKSPACE_BYTES);
-    p.part = reinterpret_cast<float*>(p.joins + 2 * MOE_MAX_GRID);
+    p.arrived = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + MOE_PAGED_WORKSPACE_BYTES);
+    p.part = reinterpret_cast<float*>(p.arrived + 3 * MOE_MAX_GRID);
     p.chunk_part = p.part + (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows, cache->head_dim);
     p.q_token = q_token_stride;
     p.q_head = q_head_stride;

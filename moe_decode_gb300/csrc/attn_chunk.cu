@@ -113,6 +113,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     extern __shared__ uint8_t dyn[];
     __shared__ int64_t scan[kThreads / 32], found[2];
     __shared__ int abort_flag;
+    __shared__ int join_info[2][3];  // first CTA, parts, whether this one is the last
     __shared__ uint32_t tmem_base;
     const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
     uint8_t* sm = dyn + (base - smem_u32(dyn));
@@ -137,11 +138,13 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
         mbar_init(drained, 1);
         fence_mbar_init();
     }
-    pdl_wait();
+    // The decode kernel runs before this one, and lets it start once its own
+    // wait for what came before is over; none of its results are needed here,
+    // so the two overlap. The wait at the end keeps the order for what follows.
     pdl_launch_dependents();
     const Place at = attn_place<Many, kThreads>(p, blockIdx.x, scan, found);
     if (at.begin >= at.end) {
-        if (tid == 0) p.joins[kAttnMaxGrid + blockIdx.x].rows = 0;
+        pdl_wait();
         return;
     }
     if (warp == kMmaWarp) {
@@ -190,7 +193,6 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                     }
                 }
             }
-            if (lane == 0) p.joins[kAttnMaxGrid + blockIdx.x] = attn_span<Many>(p, at, blockIdx.x);
             if (!ok && lane == 0) {
                 // copies may be in flight: see the last ones land (again bounded)
                 for (int i = max(0, issued - S::kStages); i < issued; ++i) {
@@ -420,6 +422,21 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 if (!whole) reinterpret_cast<float2*>(part + kAttnChunkRows * D)[part_row] = make_float2(m, l);
                 else if (p.lse) p.lse[at_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
+            if (!whole) {
+                named_bar_sync(1 + slot, kSlotRows);
+                if ((tid & (kSlotRows - 1)) == 0) {
+                    const Span span = attn_span(walk, at);
+                    join_info[slot][0] = span.cta;
+                    join_info[slot][1] = span.parts;
+                    join_info[slot][2] = attn_last(p.arrived + (1 + slot) * kAttnMaxGrid + span.cta, span.parts);
+                }
+                named_bar_sync(1 + slot, kSlotRows);
+                if (join_info[slot][2])
+                    attn_join<D, DT, kAttnChunkRows, kSlotRows, 8>(
+                        p, p.chunk_part, Span{join_info[slot][0], join_info[slot][1]}, slot * kSlotRows,
+                        min((slot + 1) * kSlotRows, walk.rows), walk.row0, walk.head, walk.q.q0, tid & (kSlotRows - 1));
+                named_bar_sync(1 + slot, kSlotRows);
+            }
             // O is read: the next item's first product may write it
             tc_fence_before();
         }
@@ -427,6 +444,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_wait();
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }

@@ -11,8 +11,8 @@
 // item's first units stand for what it costs beside its tiles (queries, joining
 // warps, output): a batch of short requests would otherwise be unevenly spread. An item whose units all lie in one CTA is
 // finished there; of one that spans CTAs each leaves its part (unnormalised
-// sums, largest score, sum of weights) in the workspace, and a second kernel
-// joins the parts in the order of the keys.
+// sums, largest score, sum of weights) in the workspace, and the CTA that comes
+// last joins the parts, in the order of the keys whoever it is.
 #pragma once
 #include <cuda.h>
 
@@ -240,28 +240,99 @@ struct Walk {
     __device__ __forceinline__ int part() const { return t0 > 0 ? 0 : 1; }
 };
 
-// What the join kernel needs of the item at the end of the CTA's range, if it
-// goes on past it. One thread, after the walk.
+// The CTA in which an item's first tile lies, and how many CTAs hold its tiles
+// (the CTA of unit u is the largest k with kU/G <= u).
+struct Span {
+    int cta, parts;
+};
 template <class Class>
-__device__ __forceinline__ AttnJoin attn_span(const AttnParams& p, const Place& at, int cta) {
-    AttnJoin j = {};
-    if (at.begin >= at.end || at.end >= at.total) return j;
-    Walk<Class> walk(p, at);
-    while (walk.next()) {
-        if (walk.t1 < walk.tiles) {
-            if (walk.t0 > 0) return j;  // began earlier
-            // the CTA of its last unit u: the largest k with kU/G <= u
-            const int64_t u = walk.unit - walk.skip + Class::kItem + walk.tiles - 1;
-            j.parts = (int)(((u + 1) * at.ctas - 1) / at.total) - cta + 1;
-            j.rows = walk.rows;
-            j.token0 = walk.q.q0;
-            j.row0 = walk.row0;
-            j.head = walk.head;
-            return j;
+__device__ __forceinline__ Span attn_span(const Walk<Class>& walk, const Place& at) {
+    const int64_t u = walk.unit - walk.skip + Class::kItem;
+    Span s;
+    s.cta = (int)(((u + 1) * at.ctas - 1) / at.total);
+    s.parts = (int)(((u + walk.tiles) * at.ctas - 1) / at.total) - s.cta + 1;
+    return s;
+}
+
+// One thread of a CTA whose part is in place (its threads' stores are behind a
+// barrier): whether all the others are. The last one to come leaves the count
+// at zero for the next call.
+__device__ __forceinline__ bool attn_last(unsigned* arrived, int parts) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(arrived) : "memory");
+    if (old != (unsigned)parts - 1) return false;
+    asm volatile("st.relaxed.gpu.global.u32 [%0], 0;" ::"l"(arrived) : "memory");
+    return true;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+__device__ __forceinline__ float exp2_approx(float x);
+
+// Joins the parts of an item, in the order of the keys (the part 1 of the CTA
+// that it begins in, then the part 0 of the CTAs after it): THREADS threads,
+// the rows [from, to). A thread takes U pieces of 8 dimensions at a time, all
+// their loads of a part in flight together: bound by the L2's latency, a slot
+// of 128 rows of 128 in two parts takes 2 us with U = 8.
+template <int D, int DT, int ROWS, int THREADS, int U>
+__device__ __forceinline__ void attn_join(const AttnParams& p, const float* parts, const Span& span, int from, int to,
+                                          int row0, int head, int token0, int tid) {
+    constexpr int kFloats = attn_part_floats(ROWS, D), kPer = D / 8;
+    const float* first = parts + ((int64_t)span.cta * 2 + 1) * kFloats;
+    const float* rest = parts + (int64_t)span.cta * 2 * kFloats;  // part 0 of the k-th CTA at k * 2 * kFloats
+    auto part_of = [&](int k) { return k == 0 ? first : rest + (int64_t)k * 2 * kFloats; };
+    auto stat_of = [&](int k, int row) { return __ldcg(reinterpret_cast<const float2*>(part_of(k) + ROWS * D) + row); };
+    const int end = to * kPer;
+    for (int i0 = tid + from * kPer; i0 < end; i0 += U * THREADS) {
+        // (past the end the last piece again, not stored)
+        float mx[U], sum[U], v[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mx[u] = -INFINITY;
+            sum[u] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
         }
-        walk.done();
+#pragma unroll 2
+        for (int k = 0; k < span.parts; ++k)
+#pragma unroll
+            for (int u = 0; u < U; ++u) mx[u] = fmaxf(mx[u], stat_of(k, min(i0 + u * THREADS, end - 1) / kPer).x);
+        for (int k = 0; k < span.parts; ++k) {
+            float2 ml[U];
+            float4 x[U], y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = min(i0 + u * THREADS, end - 1);
+                const float4* f = reinterpret_cast<const float4*>(part_of(k) + (int64_t)i * 8);
+                ml[u] = stat_of(k, i / kPer);
+                x[u] = __ldcg(f);
+                y[u] = __ldcg(f + 1);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = exp2_approx(ml[u].x - (mx[u] == -INFINITY ? 0.f : mx[u]));
+                sum[u] += w * ml[u].y;
+                v[u][0] += w * x[u].x; v[u][1] += w * x[u].y; v[u][2] += w * x[u].z; v[u][3] += w * x[u].w;
+                v[u][4] += w * y[u].x; v[u][5] += w * y[u].y; v[u][6] += w * y[u].z; v[u][7] += w * y[u].w;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * THREADS;
+            if (i >= end) break;
+            const int row = i / kPer, d = (i % kPer) * 8;
+            const float inv = sum[u] > 0.f ? 1.f / sum[u] : 0.f;
+            const int R = row0 + row, t = R / p.group, h = head * p.group + (R - t * p.group);
+            const int64_t at_row = (int64_t)(token0 + t) * p.heads + h;
+            uint4 o;
+            o.x = pack2<DT>(v[u][0] * inv, v[u][1] * inv);
+            o.y = pack2<DT>(v[u][2] * inv, v[u][3] * inv);
+            o.z = pack2<DT>(v[u][4] * inv, v[u][5] * inv);
+            o.w = pack2<DT>(v[u][6] * inv, v[u][7] * inv);
+            *reinterpret_cast<uint4*>(p.out + at_row * D + d) = o;
+            if (d == 0 && p.lse) p.lse[at_row] = sum[u] > 0.f ? (mx[u] + log2f(sum[u])) * kLn2 : -INFINITY;
+        }
     }
-    return j;
 }
 
 // Waits for the phase with parity `parity`, at most timeout_ns; false, with

@@ -1,6 +1,5 @@
 // Attention of few query rows over the paged cache: decoding streams, verify
-// chains and short chunks, and the kernel that joins the parts of items that
-// span CTAs.
+// chains and short chunks.
 #include "attn_common.cuh"
 
 namespace moe {
@@ -25,7 +24,7 @@ struct DecodeShape {
     static constexpr int kOffStat = kOffMerge + kMerge;      // largest score and sum of each warp's rows
     static constexpr int kOffBar = kOffStat + kKeyWarps * kRows * 8;
     static constexpr int kOffMisc = kOffBar + 16 * (kStages + 2);
-    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + 16 + 8;
+    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + 16 + 16;
     static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -74,6 +73,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     int64_t* scan = reinterpret_cast<int64_t*>(sm + S::kOffMisc);
     int64_t* found = scan + kThreads / 32;
     int& abort_flag = *reinterpret_cast<int*>(found + 2);
+    volatile int* join_info = &abort_flag + 1;  // first CTA, parts, whether this one is the last
     if (tid == 0) {
         abort_flag = 0;
         for (int s = 0; s < S::kStages; ++s) {
@@ -89,10 +89,14 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     pdl_wait();
     pdl_launch_dependents();
     const Place at = attn_place<Few, kThreads>(p, blockIdx.x, scan, found);
-    if (at.begin >= at.end) {
-        if (tid == 0) p.joins[blockIdx.x].rows = 0;
-        return;
+    // padding rows
+    for (int64_t i = (int64_t)min(max(p.q_start[p.B], 0), p.T) * p.heads + blockIdx.x + (int64_t)p.G * warp;
+         i < (int64_t)p.T * p.heads; i += (int64_t)p.G * (kThreads / 32)) {
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) reinterpret_cast<uint32_t*>(p.out + i * D)[32 * x + lane] = 0u;
+        if (p.lse && lane == 0) p.lse[i] = -INFINITY;
     }
+    if (at.begin >= at.end) return;
     volatile int* flag = &abort_flag;
 
     if (warp == kConsumers) {
@@ -136,7 +140,6 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 parity ^= 1u;
             }
         }
-        if (lane == 0) p.joins[blockIdx.x] = attn_span<Few>(p, at, blockIdx.x);
         if (!ok && lane == 0) {
             // copies may be in flight: see the last ones land (again bounded)
             for (int i = max(0, issued - S::kStages); i < issued; ++i) {
@@ -379,77 +382,21 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 if (c == 0) reinterpret_cast<float2*>(part + kRows * D)[row] = stat[row];
             }
         }
-        // the next item writes the rows and the statistics after its own barrier
+        // the next item writes the rows and the statistics after this barrier
         named_bar_sync(1, kConsumers * 32);
-    }
-}
-
-// Joins the parts of the item that spans from CTA c, part after part in the
-// order of the keys (the part 1 of CTA c, then the part 0 of the CTAs after it):
-// kAttnRows rows from row `from` on.
-template <int D, int DT, int ROWS>
-__device__ __forceinline__ void join(const AttnParams& p, const AttnJoin& j, const float* parts, int c, int from) {
-    const int tid = threadIdx.x;
-    constexpr int kFloats = attn_part_floats(ROWS, D);
-    const float* first = parts + ((int64_t)c * 2 + 1) * kFloats;
-    const float* rest = parts + (int64_t)c * 2 * kFloats;  // part 0 of CTA c + k at k * 2 * kFloats
-    auto part_of = [&](int k) { return k == 0 ? first : rest + (int64_t)k * 2 * kFloats; };
-    constexpr int kPer = D / 8;
-    const int to = min(from + kAttnRows, j.rows);
-    for (int i = tid + from * kPer; i < to * kPer; i += 128) {
-        const int row = i / kPer, d = (i % kPer) * 8;
-        float mx = -INFINITY, sum = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < j.parts; ++k) mx = fmaxf(mx, reinterpret_cast<const float2*>(part_of(k) + ROWS * D)[row].x);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float v[8] = {};
-#pragma unroll 4
-        for (int k = 0; k < j.parts; ++k) {
-            const float* f = part_of(k);
-            const float2 ml = reinterpret_cast<const float2*>(f + ROWS * D)[row];
-            const float w = exp2_approx(ml.x - ref);
-            sum += w * ml.y;
-            const float4 x = *reinterpret_cast<const float4*>(f + row * D + d);
-            const float4 y = *reinterpret_cast<const float4*>(f + row * D + d + 4);
-            v[0] += w * x.x; v[1] += w * x.y; v[2] += w * x.z; v[3] += w * x.w;
-            v[4] += w * y.x; v[5] += w * y.y; v[6] += w * y.z; v[7] += w * y.w;
+        if (!whole) {
+            if (tid == 0) {
+                const Span span = attn_span(walk, at);
+                join_info[0] = span.cta;
+                join_info[1] = span.parts;
+                join_info[2] = attn_last(p.arrived + span.cta, span.parts);
+            }
+            named_bar_sync(1, kConsumers * 32);
+            if (join_info[2])
+                attn_join<D, DT, kRows, kConsumers * 32, 2>(p, p.part, Span{join_info[0], join_info[1]}, 0, walk.rows,
+                                                         walk.row0, walk.head, walk.q.q0, tid);
+            named_bar_sync(1, kConsumers * 32);
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int R = j.row0 + row, t = R / p.group, h = j.head * p.group + (R - t * p.group);
-        const int64_t at_row = (int64_t)(j.token0 + t) * p.heads + h;
-        uint4 o;
-        o.x = pack2<DT>(v[0] * inv, v[1] * inv);
-        o.y = pack2<DT>(v[2] * inv, v[3] * inv);
-        o.z = pack2<DT>(v[4] * inv, v[5] * inv);
-        o.w = pack2<DT>(v[6] * inv, v[7] * inv);
-        *reinterpret_cast<uint4*>(p.out + at_row * D + d) = o;
-        if (d == 0 && p.lse) p.lse[at_row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
-    }
-}
-
-// Padding rows, and the parts of both kernels: block (c, 0) joins the decode
-// kernel's of CTA c, block (c, 1 + i) rows [32 i, 32 i + 32) of the chunk
-// kernel's (only there when that kernel ran).
-template <int D, int DT>
-__global__ __launch_bounds__(128) void attn_join_kernel(const __grid_constant__ AttnParams p) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int c = blockIdx.x;
-    if (blockIdx.y > 0) {
-        const int from = ((int)blockIdx.y - 1) * kAttnRows;
-        const AttnJoin j = p.joins[kAttnMaxGrid + c];
-        if (from < j.rows) join<D, DT, kAttnChunkRows>(p, j, p.chunk_part, c, from);
-        return;
-    }
-    const AttnJoin j = p.joins[c];
-    const int lane = threadIdx.x & 31;
-    const int last = min(max(p.q_start[p.B], 0), p.T);
-    if (j.rows > 0) join<D, DT, kAttnRows>(p, j, p.part, c, 0);
-    for (int64_t i = (int64_t)last * p.heads + c * 4 + (threadIdx.x >> 5); i < (int64_t)p.T * p.heads;
-         i += (int64_t)gridDim.x * 4) {
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) reinterpret_cast<uint32_t*>(p.out + i * D)[32 * x + lane] = 0u;
-        if (p.lse && lane == 0) p.lse[i] = -INFINITY;
     }
 }
 
@@ -478,14 +425,10 @@ cudaError_t launch_typed(const AttnParams& p, const CUtensorMap* maps, cudaStrea
                            maps[0], maps[1]);
     if (e != cudaSuccess) return e;
     ++*launches;
-    const bool chunk = attn_may_chunk(p);
-    if (chunk) {
+    if (attn_may_chunk(p)) {
         e = launch_attn_chunk(p, &maps[2], &maps[3], D, DT, stream);
-        if (e != cudaSuccess) return e;
-        ++*launches;
+        if (e == cudaSuccess) ++*launches;
     }
-    e = launch(attn_join_kernel<D, DT>, dim3((unsigned)p.G, chunk ? 1 + kAttnChunkRows / kAttnRows : 1), 128, 0, stream, p);
-    if (e == cudaSuccess) ++*launches;
     return e;
 }
 

@@ -61,15 +61,6 @@ constexpr int kAttnChunkRows = 256; // and of the chunk kernel
 constexpr int kAttnFewRows = 64;
 constexpr int kAttnMaxGrid = 256;   // CTAs of a launch (workspace sizing)
 
-// The part of an item that spans CTAs, left by the CTA in which it begins.
-struct AttnJoin {
-    int rows;    // 0: no item spans from this CTA
-    int parts;   // CTAs that hold a part of it
-    int token0;  // first token row of the request
-    int row0, head;
-    int pad[3];
-};
-
 struct AttnParams {
     const uint16_t* q;
     uint16_t* out;
@@ -80,7 +71,9 @@ struct AttnParams {
     unsigned* ctrl;
     float* part;        // partial results of items that span CTAs, [G][2]
     float* chunk_part;  // and those of the chunk kernel's
-    AttnJoin* joins;    // [2][kAttnMaxGrid]: of the decode kernel, of the chunk kernel
+    // parts that are in place of the item that spans from CTA c, [3][kAttnMaxGrid]:
+    // of the decode kernel, of the chunk kernel's two slots. Zero between calls.
+    unsigned* arrived;
     int64_t q_token, q_head;
     int T, B, heads, kv_heads, group;
     int max_blocks, block_size, n_blocks;
@@ -93,8 +86,8 @@ struct AttnParams {
 
 // Whether any request of the call may have many rows.
 inline bool attn_may_chunk(const AttnParams& p) { return (int64_t)p.T * p.group > kAttnFewRows; }
-// The decode kernel, the chunk kernel (where any request may have many rows)
-// and the join of all parts. maps: CUtensorMaps of K and V whose boxes hold all
+// The decode kernel and the chunk kernel (where any request may have many
+// rows). maps: CUtensorMaps of K and V whose boxes hold all
 // dimensions of `box` keys, then of K and V in boxes of 64 dimensions (for the
 // chunk kernel alone).
 cudaError_t launch_attn(const AttnParams& p, const void* maps, int head_dim, int dtype, cudaStream_t stream,
