@@ -358,7 +358,7 @@ int moe_paged_append(const void* k_new, int64_t k_token_stride, int64_t k_head_s
 /* Attention of the step's new tokens over the paged cache, which already
  * holds their keys and values. q [T, q_heads, head_dim] by its strides
  * (elements, multiples of 8), q_heads a multiple of kv_heads (at most 32
- * times); query head h reads kv head h / (q_heads / kv_heads). Row t of
+ * times), T * q_heads / kv_heads < 2^28; query head h reads kv head h / (q_heads / kv_heads). Row t of
  * request b sits at position p = seq_lens[b] - (q_start[b + 1] -
  * q_start[b]) + t - q_start[b] and sees the keys j <= p, with window > 0
  * only those with j > p - window:

@@ -199,7 +199,7 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     if (rc) return rc;
     if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 32) return MOE_ESHAPE;
     const int group = q_heads / cache->kv_heads;
-    if (T < 0 || (int64_t)T * group > 0x3fffffffLL) return MOE_ESHAPE;
+    if (T < 0 || (int64_t)T * group >= (1 << 28)) return MOE_ESHAPE;
     if (B < 1 || B > MOE_PAGED_MAX_REQUESTS || max_blocks < 1 || window < 0) return MOE_ESHAPE;
     if (!(scale == scale) || std::isinf(scale)) return MOE_EINVAL;
     if (!block_tables || !q_start || !seq_lens) return MOE_EINVAL;
@@ -234,6 +234,7 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     p.heads = q_heads;
     p.kv_heads = cache->kv_heads;
     p.group = group;
+    p.group_magic = ((1ull << 36) + group - 1) / group;
     p.max_blocks = max_blocks;
     p.block_size = cache->block_size;
     p.n_blocks = cache->n_blocks;

@@ -279,7 +279,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             if (slot * kSlotRows >= walk.rows) continue;
             const int R = walk.row0 + slot * kSlotRows + row;
             const bool real = slot * kSlotRows + row < walk.rows;
-            const int tok = R / p.group, head = walk.head * p.group + (R - tok * p.group);
+            const int tok = token_of(p, R), head = walk.head * p.group + (R - tok * p.group);
             // the row into shared memory, 16-byte pieces in the swizzle; rows
             // past the end are zeros
             {
@@ -303,9 +303,9 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             const int from = p.window > 0 ? at_pos - p.window + 1 : 0;
             const int slot_row0 = walk.row0 + slot * kSlotRows;
             const int slot_rows = min(kSlotRows, walk.rows - slot * kSlotRows);
-            const int all_to = min(walk.q.pos0 + slot_row0 / p.group + 1, walk.hi);
+            const int all_to = min(walk.q.pos0 + token_of(p, slot_row0) + 1, walk.hi);
             const int all_from =
-                p.window > 0 ? walk.q.pos0 + (slot_row0 + slot_rows - 1) / p.group - p.window + 1 : 0;
+                p.window > 0 ? walk.q.pos0 + token_of(p, slot_row0 + slot_rows - 1) - p.window + 1 : 0;
             float m = -INFINITY;  // reference of the weights, in log2
             float l = 0.f;
             for (int j = 0; j < n; ++j) {

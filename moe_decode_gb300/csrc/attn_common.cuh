@@ -24,6 +24,18 @@ namespace moe {
 
 constexpr float kLn2 = 0.693147180559945f;
 
+// The token of a query row within its request.
+__device__ __forceinline__ int token_of(const AttnParams& p, int row) {
+    return (int)(((unsigned long long)(unsigned)row * p.group_magic) >> 36);
+}
+
+// a * b / c, in 32 bits where that suffices (a 64-bit division takes some 400
+// cycles, and a call with few units waits for each).
+__device__ __forceinline__ int64_t scaled(int64_t a, int b, int64_t c) {
+    if (a < (1 << 22) && c < (1 << 22)) return (uint32_t)a * (uint32_t)b / (uint32_t)c;  // b <= 256 CTAs
+    return a * b / c;
+}
+
 struct Request {
     int q0, n;     // first token row, tokens
     int pos0;      // position of the first token (negative: rows that see nothing)
@@ -45,7 +57,7 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int r) {
 // them, inside the block table; `over` where a row sees past it.
 __device__ __forceinline__ void attn_keys(const AttnParams& p, const Request& q, int row0, int rows, int& lo, int& hi,
                                           bool& over) {
-    const int first = q.pos0 + row0 / p.group, last = q.pos0 + (row0 + rows - 1) / p.group;
+    const int first = q.pos0 + token_of(p, row0), last = q.pos0 + token_of(p, row0 + rows - 1);
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
     over = last + 1 > cap;
     hi = (int)min((int64_t)last + 1, cap);
@@ -70,13 +82,13 @@ struct RowTiles {
     int step, step_rem;
     int64_t cap;
     __device__ __forceinline__ RowTiles(const AttnParams& params, const Request& q)
-        : p(params), pos0(q.pos0), rows(q.n * params.group), first(0), first_rem(0), step(ROWS / params.group),
-          step_rem(ROWS % params.group), cap((int64_t)params.max_blocks * params.block_size) {}
+        : p(params), pos0(q.pos0), rows(q.n * params.group), first(0), first_rem(0), step(token_of(params, ROWS)),
+          step_rem(ROWS - token_of(params, ROWS) * params.group), cap((int64_t)params.max_blocks * params.block_size) {}
     __device__ __forceinline__ bool more() const { return row0 < rows; }
     __device__ __forceinline__ int tiles() const {
         int last = first + step + (first_rem + step_rem >= p.group ? 1 : 0);  // token of the next tile's first row
-        if ((first_rem + step_rem) % p.group == 0) --last;                    // which may begin there
-        if (row0 + ROWS >= rows) last = (rows - 1) / p.group;
+        if (first_rem + step_rem == 0 || first_rem + step_rem == p.group) --last;  // which may begin there
+        if (row0 + ROWS >= rows) last = token_of(p, rows - 1);
         const int hi = (int)min((int64_t)pos0 + last + 1, cap);
         const int lo = p.window > 0 ? max(pos0 + first - p.window + 1, 0) : 0;
         return attn_tiles(lo, hi);
@@ -160,8 +172,8 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_
         at.total += scan[w];
     }
     at.ctas = (int)min((int64_t)p.G, at.total);
-    at.begin = cta < at.ctas ? at.total * cta / at.ctas : at.total;
-    at.end = cta < at.ctas ? at.total * (cta + 1) / at.ctas : at.total;
+    at.begin = cta < at.ctas ? scaled(at.total, cta, at.ctas) : at.total;
+    at.end = cta < at.ctas ? scaled(at.total, cta + 1, at.ctas) : at.total;
     if (own > 0 && before <= at.begin && at.begin < before + own) {
         for (int r = r0; r < r1; ++r) {
             const Request q = attn_request(p, r);
@@ -200,10 +212,14 @@ struct Walk {
         if (unit >= end) return;
         q = attn_request(p, r);
         const int64_t per_head = attn_request_units<Class>(p, q);
-        head = (int)(at.rest / per_head);
+        head = at.rest < (1 << 30) && per_head < (1 << 30) ? (int)((uint32_t)at.rest / (uint32_t)per_head)
+                                                           : (int)(at.rest / per_head);
         int64_t rest = at.rest - head * per_head;
         RowTiles<ROWS> t(p, q);
-        for (; rest >= Class::kItem + t.tiles(); t.next()) rest -= Class::kItem + t.tiles();
+        for (int u = Class::kItem + t.tiles(); rest >= u; u = Class::kItem + t.tiles()) {
+            rest -= u;
+            t.next();
+        }
         row0 = t.row0;
         skip = (int)rest;
     }
@@ -245,12 +261,16 @@ struct Walk {
 struct Span {
     int cta, parts;
 };
+__device__ __forceinline__ int cta_of(int64_t unit, const Place& at) {
+    if (at.total < (1 << 22)) return (int)(((uint32_t)(unit + 1) * (uint32_t)at.ctas - 1) / (uint32_t)at.total);
+    return (int)(((unit + 1) * at.ctas - 1) / at.total);
+}
 template <class Class>
 __device__ __forceinline__ Span attn_span(const Walk<Class>& walk, const Place& at) {
     const int64_t u = walk.unit - walk.skip + Class::kItem;
     Span s;
-    s.cta = (int)(((u + 1) * at.ctas - 1) / at.total);
-    s.parts = (int)(((u + walk.tiles) * at.ctas - 1) / at.total) - s.cta + 1;
+    s.cta = cta_of(u, at);
+    s.parts = cta_of(u + walk.tiles - 1, at) - s.cta + 1;
     return s;
 }
 
@@ -322,7 +342,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const float* part
             if (i >= end) break;
             const int row = i / kPer, d = (i % kPer) * 8;
             const float inv = sum[u] > 0.f ? 1.f / sum[u] : 0.f;
-            const int R = row0 + row, t = R / p.group, h = head * p.group + (R - t * p.group);
+            const int R = row0 + row, t = token_of(p, R), h = head * p.group + (R - t * p.group);
             const int64_t at_row = (int64_t)(token0 + t) * p.heads + h;
             uint4 o;
             o.x = pack2<DT>(v[u][0] * inv, v[u][1] * inv);

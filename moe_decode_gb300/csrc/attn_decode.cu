@@ -18,7 +18,7 @@ struct DecodeShape {
     static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kQRow = D * 2 + 16;                 // eight rows' 16-byte pieces in different banks
     static constexpr int kQ = kRows * kQRow;                 // queries of an item, of two in turn
-    static constexpr int kMerge = kRows * (D + 4) * 4;
+    static constexpr int kMerge = kRows * D * 4;
     static constexpr int kOffQ = kStages * kStage;
     static constexpr int kOffMerge = kOffQ + 2 * kQ;
     static constexpr int kOffStat = kOffMerge + kMerge;      // largest score and sum of each warp's rows
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * i, (uint32_t)(cur.rows * D * 2));
                 __syncwarp();
                 if (lane < cur.rows) {
-                    const int R = cur.row0 + lane, t = R / p.group, h = cur.head * p.group + (R - t * p.group);
+                    const int R = cur.row0 + lane, t = token_of(p, R), h = cur.head * p.group + (R - t * p.group);
                     copy_row(base + S::kOffQ + i * S::kQ + lane * S::kQRow,
                              p.q + (cur.token0 + t) * p.q_token + h * p.q_head, D * 2, q_full + 8 * i);
                 }
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     uint32_t parity = 0;
     uint32_t items = 0;
     float2* stat = reinterpret_cast<float2*>(sm + S::kOffStat);  // [key warp][row]
-    float* merge = reinterpret_cast<float*>(sm + S::kOffMerge);  // [row][D + 4]
+    float* merge = reinterpret_cast<float*>(sm + S::kOffMerge);  // [row][D], groups of 8 columns swizzled by the row
     for (; walk.next(); walk.done()) {
         // (rows past the item's last hold anything; a row's results depend on
         // no other row)
@@ -186,12 +186,12 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int row = set * 16 + b * 8 + quad;
-            const int pos = walk.q.pos0 + (walk.row0 + row) / p.group;
+            const int pos = walk.q.pos0 + token_of(p, walk.row0 + row);
             last[b] = row < walk.rows ? min(pos, walk.hi - 1) : -1;
             from[b] = p.window > 0 ? pos - p.window + 1 : 0;
         }
-        const int all_to = min(walk.q.pos0 + walk.row0 / p.group + 1, walk.hi);
-        const int all_from = p.window > 0 ? walk.q.pos0 + (walk.row0 + walk.rows - 1) / p.group - p.window + 1 : 0;
+        const int all_to = min(walk.q.pos0 + token_of(p, walk.row0) + 1, walk.hi);
+        const int all_from = p.window > 0 ? walk.q.pos0 + token_of(p, walk.row0 + walk.rows - 1) - p.window + 1 : 0;
         float o[D / 8][4];
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -337,19 +337,23 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
         for (int w = 0; w < kKeyWarps; ++w) {
             if (kw == w && active) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b) {
+                    // (eight loads before the first store: the compiler cannot
+                    // tell the swizzled addresses apart)
+                    float* row = merge + (set * 16 + b * 8 + quad) * D + 2 * pair;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        float2* to = reinterpret_cast<float2*>(merge + (set * 16 + b * 8 + quad) * (D + 4) + i * 8 +
-                                                               2 * pair);
-                        float2 v = make_float2(o[i][2 * b], o[i][2 * b + 1]);
-                        if (w > 0) {
-                            const float2 u = *to;
-                            v.x += u.x;
-                            v.y += u.y;
-                        }
-                        *to = v;
+                    for (int i0 = 0; i0 < D / 8; i0 += 8) {
+                        float2 u[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            u[i] = w > 0 ? *reinterpret_cast<const float2*>(row + ((i0 + i) ^ (quad & 3)) * 8)
+                                         : make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<float2*>(row + ((i0 + i) ^ (quad & 3)) * 8) =
+                                make_float2(u[i].x + o[i0 + i][2 * b], u[i].y + o[i0 + i][2 * b + 1]);
                     }
+                }
             }
             // (everyone has read the statistics by the first of these)
             if (w == kKeyWarps - 1 && kw == 0 && pair == 0)
@@ -362,12 +366,12 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
         float* part = p.part + ((int64_t)blockIdx.x * 2 + walk.part()) * attn_part_floats(kRows, D);
         for (int i = tid; i < walk.rows * (D / 8); i += kConsumers * 32) {
             const int row = i / (D / 8), c = i % (D / 8);
-            const float4 x = *reinterpret_cast<const float4*>(merge + row * (D + 4) + c * 8);
-            const float4 y = *reinterpret_cast<const float4*>(merge + row * (D + 4) + c * 8 + 4);
+            const float4 x = *reinterpret_cast<const float4*>(merge + row * D + (c ^ (row & 3)) * 8);
+            const float4 y = *reinterpret_cast<const float4*>(merge + row * D + (c ^ (row & 3)) * 8 + 4);
             if (whole) {
                 const float2 ml = stat[row];
                 const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
-                const int R = walk.row0 + row, t = R / p.group, h = walk.head * p.group + (R - t * p.group);
+                const int R = walk.row0 + row, t = token_of(p, R), h = walk.head * p.group + (R - t * p.group);
                 const int64_t at_row = (int64_t)(walk.q.q0 + t) * p.heads + h;
                 uint4 v;
                 v.x = pack2<DT>(x.x * inv, x.y * inv);

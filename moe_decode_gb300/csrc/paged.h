@@ -76,6 +76,7 @@ struct AttnParams {
     unsigned* arrived;
     int64_t q_token, q_head;
     int T, B, heads, kv_heads, group;
+    unsigned long long group_magic;  // ceil(2^36 / group): x / group = x * magic >> 36 for x < 2^28
     int max_blocks, block_size, n_blocks;
     int box, box_shift;  // keys that one copy brings, as a power of two
     int window;
