@@ -45,7 +45,7 @@ constexpr int kBinBits = 9, kBins = 1 << kBinBits;
 static_assert(kBins == kThreads, "a thread looks at one bin");
 constexpr int kList = 128;
 constexpr int kMassBits = 42;
-static_assert(kList * 4 == kThreads, "four threads rank a member");
+static_assert(kList * 4 <= kThreads, "four threads rank a member");
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -84,16 +84,15 @@ __device__ __forceinline__ uint32_t atom_add_remote32(uint32_t a, uint32_t v) {
 }
 
 struct Shared {
-    // histograms: members of each bin, and the sum of their places in it or of
-    // their masses. Two, used in turn: a CTA that is a barrier ahead clears the
-    // other than the one still being read.
+    // a histogram: members of each bin, and the sum of their places in it or of
+    // their masses; and the same over the cluster
     struct {
         uint32_t count[kBins];
         union {
             uint32_t place[kBins];
             u64 mass[kBins];
         };
-    } hist[2];
+    } hist, all;
     struct {  // members of the border's bin (first CTA of the cluster)
         u64 code[kList];
         u64 mass[kList];
@@ -101,6 +100,7 @@ struct Shared {
         uint16_t order[kList];
         u64 sums[kList];
     } list;
+    uint16_t queue[kWarps][32 + 128];  // indices that a warp has put aside
     u64 best[16];       // each CTA's largest logit and its index
     // each CTA's share of a cluster sum, in two sets used in turn: a CTA that
     // is a barrier ahead writes the other set than the one still being read
@@ -189,10 +189,10 @@ __device__ __forceinline__ T warp_sum(T v) {
 __host__ __device__ constexpr int offset_slice() { return (int)((sizeof(Shared) + 15) & ~size_t(15)); }
 
 // A member into the histogram of all codes: its bin is an eighth of a unit of t.
-__device__ __forceinline__ void enter_bin(Shared& sh, int turn, uint32_t steps) {
+__device__ __forceinline__ void enter_bin(Shared& sh, uint32_t steps) {
     const uint32_t bin = steps >> (kStepBits - kBinBits);
-    atomicAdd(&sh.hist[turn].count[bin], 1u);
-    atomicAdd(&sh.hist[turn].place[bin], (steps >> (kStepBits - kBinBits - 8)) & 255u);
+    atomicAdd(&sh.hist.count[bin], 1u);
+    atomicAdd(&sh.hist.place[bin], (steps >> (kStepBits - kBinBits - 8)) & 255u);
 }
 
 // The row's slice that this CTA holds, and what bounds the kept set so far:
@@ -206,7 +206,7 @@ struct Row {
     uint32_t limit;
     u64 border;
     uint32_t tie;
-    int turn;  // which histogram and set of cluster sums are in use
+    int turn;  // which set of cluster sums is in use
 };
 constexpr int kCodeBits = kStepBits + 32;
 __device__ __forceinline__ u64 code_of(uint32_t steps, float x) { return ((u64)steps << 32) | (uint32_t)~value_bits(x); }
@@ -221,14 +221,28 @@ __device__ __forceinline__ bool kept(const Row& r, u64 code, uint32_t index) {
 __host__ __device__ __forceinline__ int per_thread(int n) { return (((n + 4 * kThreads - 1) / (4 * kThreads)) | 1) * 4; }
 
 // The mass of the thread's logits with steps in [from, to); f(i, x, steps) for
-// those with steps in [to, row.limit). COUNT: each of the former also goes
-// into the histogram, into its bin's number of members and the sum of their
-// places within the bin. The masses of four are taken together, without a
-// branch between them: one's chain is some 30 operations.
-template <bool COUNT, class F>
+// those with steps in [to, row.limit), in the thread itself (OWN) or in any of
+// its warp. COUNT: each of the former also goes into the histogram, into its
+// bin's number of members and the sum of their places within the bin. The
+// masses of four are taken together, without a branch between them: one's chain
+// is some 30 operations. The others are few, but hardly any 128 logits have
+// none, so they are queued and taken 32 at a time.
+template <bool COUNT, bool OWN, class F>
 __device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to, Shared& sh, F f) {
+    const int lane = threadIdx.x & 31;
     const int i0 = threadIdx.x * row.len, i1 = i0 + row.len;
     const uint32_t span = to > from ? to - from : 0, few = row.limit > to ? row.limit - to : 0;
+    uint16_t* queue = sh.queue[threadIdx.x >> 5];
+    int queued = 0;
+    auto flush = [&] {
+        __syncwarp();
+        for (int n = lane; n < queued; n += 32) {
+            const int i = queue[n];
+            f(i, row.x[i], steps_of(row.x[i], row.scale));
+        }
+        __syncwarp();
+        queued = 0;
+    };
     u64 sum = 0;
     for (int i = i0; i < i1; i += 4) {
         const float4 q = *reinterpret_cast<const float4*>(row.x + i);
@@ -248,22 +262,34 @@ __device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to,
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sum += steps[j] - from < span ? w[j] : 0;
-                if (COUNT && steps[j] - from < span) enter_bin(sh, row.turn, steps[j]);
+                if (COUNT && steps[j] - from < span) enter_bin(sh, steps[j]);
             }
         }
-        if (near) {
+        if (OWN) {
+            if (near) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (steps[j] - to < few) f(i + j, x[j], steps[j]);
+                for (int j = 0; j < 4; ++j)
+                    if (steps[j] - to < few) f(i + j, x[j], steps[j]);
+            }
+        } else if (__any_sync(0xffffffffu, near)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool one = steps[j] - to < few;
+                const uint32_t set = __ballot_sync(0xffffffffu, one);
+                if (one) queue[queued + __popc(set & ((1u << lane) - 1u))] = (uint16_t)(i + j);
+                queued += __popc(set);
+            }
+            if (queued >= 32) flush();
         }
     }
+    if (!OWN) flush();
     return sum;
 }
-// f(i, x, code) for each of the thread's members of the kept set with steps
-// from `from` on.
+// f(i, x, code) for each of the slice's members of the kept set with steps from
+// `from` on.
 template <class F>
 __device__ __forceinline__ void each_member(const Row& row, uint32_t from, Shared& sh, F f) {
-    sweep<false>(row, from, from, sh, [&](int i, float x, uint32_t steps) {
+    sweep<false, false>(row, from, from, sh, [&](int i, float x, uint32_t steps) {
         const u64 code = code_of(steps, x);
         if (kept(row, code, row.base + i)) f(i, x, code);
     });
@@ -304,40 +330,46 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
         st_remote64(remote(&sh.part[row.turn][rank], tid), a);
     }
     cluster_sync();
-    // one bin a thread, over the cluster: all the loads before the first sum
-    uint32_t c[16];
-    u64 w[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        c[r] = r < C ? ld_remote32(remote(&sh.hist[row.turn].count[tid], r)) : 0;
-        w[r] = 0;
-        if (S == kByMass && r < C) w[r] = ld_remote64(remote(&sh.hist[row.turn].mass[tid], r));
-        if (S == kByBounds && r < C) w[r] = ld_remote32(remote(&sh.hist[row.turn].place[tid], r));
+    // Each CTA sums 512 / C bins and leaves the sums in all CTAs: a thread reads
+    // one bin of one CTA and writes one sum to one. (Every CTA reading all of the
+    // others' bins took 14,000 cycles with masses and C = 16: distributed shared
+    // memory brings some 10 bytes a clock.)
+    {
+        const int r = tid & (C - 1), bin = (int)rank * (kBins / C) + tid / C;
+        uint32_t n = ld_remote32(remote(&sh.hist.count[bin], r));
+        u64 v = S == kByMass     ? ld_remote64(remote(&sh.hist.mass[bin], r))
+                : S == kByBounds ? ld_remote32(remote(&sh.hist.place[bin], r))
+                                 : 0;
+        for (int o = C / 2; o; o >>= 1) {
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+            if (S != kByCount) v += __shfl_xor_sync(0xffffffffu, v, o);
+        }
+        st_remote32(remote(&sh.all.count[bin], r), n);
+        if (S == kByMass) st_remote64(remote(&sh.all.mass[bin], r), v);
+        if (S == kByBounds) st_remote32(remote(&sh.all.place[bin], r), (uint32_t)v);
     }
-#pragma unroll
-    for (int r = 1; r < 16; ++r) {
-        c[0] += c[r];
-        w[0] += w[r];
-    }
+    cluster_sync();
+    const uint32_t count = sh.all.count[tid];
+    const u64 value = S == kByMass ? sh.all.mass[tid] : S == kByBounds ? sh.all.place[tid] : 0;
     for (int r = 0; r < C; ++r) all += sh.part[row.turn][r];
     if (S == kByBounds) {
         target = part > 0.f ? share(part, all, true) : 0;
         target = target > 1 ? target : 1;
     }
-    u64 sum[2] = {S == kByMass ? w[0] : c[0], 0};  // what is searched; kByBounds: largest, smallest
+    u64 sum[2] = {S == kByMass ? value : count, 0};  // what is searched; kByBounds: largest, smallest
     if (S == kByBounds) {
         sum[0] = 0;
-        if (c[0]) {
+        if (count) {
             // The mean of t, in parts of the bin, is known to 1/256. The mass
             // of one falls from `first` to `first` 2^(-1/8) within the bin and
             // is convex in t, so the mean mass is at least that of the mean t
             // and at most the chord's there. 2^-16: t is off by its rounding.
             const float first = exp2f((float)kMassBits - (float)tid * (1.f / 8.f));
-            const float mean = (float)w[0] / ((float)c[0] * 256.f);
+            const float mean = (float)value / ((float)count * 256.f);
             const float most = first * (1.f - 0.08299595f * mean) * (1.f + 1.f / 65536.f);
             const float least = first * exp2f((mean + 1.f / 256.f) * (-1.f / 8.f)) * (1.f - 1.f / 65536.f);
-            sum[0] = c[0] * __float2ull_ru(most);
-            sum[1] = c[0] * __float2ull_rd(least);
+            sum[0] = count * __float2ull_ru(most);
+            sum[1] = count * __float2ull_rd(least);
         }
     }
     u64 upto[2] = {sum[0], sum[1]};
@@ -362,7 +394,7 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
         if (before < target && target <= before + sum[k]) {
             if (k == 0) {
                 sh.bin = tid;
-                sh.bin_count = c[0];
+                sh.bin_count = count;
                 sh.bin_mass = sum[0];
                 sh.before = before;
             } else {
@@ -393,21 +425,21 @@ __device__ __forceinline__ bool settle(Row& row, const Range range, u64 count, b
     const uint32_t members = ld_remote32(remote(&sh.listed, 0));
     const bool fits = members <= kList;
     if (rank == 0 && fits) {
-        // four threads count the members before one
+        // four threads or more count the members before one
         {
-            const uint32_t i = tid >> 2;
+            const int team = members <= 32 ? 16 : members <= 64 ? 8 : 4;
+            const uint32_t i = tid / team;
             uint32_t place = 0;
             if (i < members) {
                 const u64 code = sh.list.code[i];
                 const uint32_t index = sh.list.index[i];
-                for (uint32_t j = tid & 3; j < members; j += 4) {
+                for (uint32_t j = tid & (team - 1); j < members; j += team) {
                     const u64 other = sh.list.code[j];
                     place += other < code || (other == code && sh.list.index[j] < index);
                 }
             }
-            place += __shfl_xor_sync(0xffffffffu, place, 1);
-            place += __shfl_xor_sync(0xffffffffu, place, 2);
-            if (i < members && (tid & 3) == 0) sh.list.order[place] = (uint16_t)i;
+            for (int o = team / 2; o; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+            if (i < members && (tid & (team - 1)) == 0) sh.list.order[place] = (uint16_t)i;
         }
         __syncthreads();
         // mass up to each place
@@ -456,8 +488,8 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
     auto clear = [&] {
         row.turn ^= 1;
         for (int i = tid; i < kBins; i += kThreads) {
-            sh.hist[row.turn].count[i] = 0;
-            sh.hist[row.turn].mass[i] = 0;  // (and so the places)
+            sh.hist.count[i] = 0;
+            sh.hist.mass[i] = 0;  // (and so the places)
         }
         if (tid == 0) sh.listed = 0;
         __syncthreads();
@@ -469,19 +501,19 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
         clear();
         if (!by_mass) {
             const uint32_t steps = steps_of(top, row.scale);
-            if (steps < row.limit) atomicAdd(&sh.hist[row.turn].count[range.bin(code_of(steps, top))], 1u);
+            if (steps < row.limit) atomicAdd(&sh.hist.count[range.bin(code_of(steps, top))], 1u);
             locate<kByCount>(row, target, 0.f, 0, all, sh, rank, C);
             if (sh.bin_count) {
                 row.limit = min(row.limit, (sh.bin + 1) << (kStepBits - kBinBits));
-                if (settle(row, range, (u64)k, by_p, 0, part, sh, rank, C)) return;
+                if (k <= kList && settle(row, range, (u64)k, by_p, 0, part, sh, rank, C)) return;
             }
             clear();
         } else {
             u64 near = 0;
-            u64 own = sweep<true>(row, 0, sure_steps(row), sh, [&](int i, float x, uint32_t steps) {
+            u64 own = sweep<true, true>(row, 0, sure_steps(row), sh, [&](int i, float x, uint32_t steps) {
                 if (!kept(row, code_of(steps, x), row.base + i)) return;
                 near += mass_of(x, row.scale);
-                enter_bin(sh, row.turn, steps);
+                enter_bin(sh, steps);
             });
             own += near;
             locate<kByBounds>(row, target, part, own, all, sh, rank, C);
@@ -500,11 +532,11 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
                 const u64 code = code_of(steps, x);
                 if (!range.has(code) || !kept(row, code, row.base + i)) return;
                 const uint32_t at = range.bin(code);
-                atomicAdd(&sh.hist[row.turn].count[at], 1u);
-                if (by_mass) atomicAdd(&sh.hist[row.turn].mass[at], mass_of(x, row.scale));
+                atomicAdd(&sh.hist.count[at], 1u);
+                if (by_mass) atomicAdd(&sh.hist.mass[at], mass_of(x, row.scale));
             };
             const uint32_t first = (uint32_t)(range.from >> 32);
-            const u64 own = sweep<false>(row, by_mass && !again ? 0 : first, first, sh, enter);
+            const u64 own = sweep<false, false>(row, by_mass && !again ? 0 : first, first, sh, enter);
             if (by_mass && !again) below = own;
             if (by_mass) locate<kByMass>(row, target, 0.f, own, all, sh, rank, C);
             else locate<kByCount>(row, target, 0.f, 0, all, sh, rank, C);
@@ -532,9 +564,9 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
                 // index order
                 const u64 each = mass_of(bits_value(~(uint32_t)range.from), row.scale);
                 const u64 need = by_mass ? (rest + each - 1) / each : rest;
-                const uint32_t mine = sh.hist[row.turn].count[bin];
+                const uint32_t mine = sh.hist.count[bin];
                 uint32_t lower = 0;
-                for (uint32_t r = 0; r < rank; ++r) lower += ld_remote32(remote(&sh.hist[row.turn].count[bin], r));
+                for (uint32_t r = 0; r < rank; ++r) lower += ld_remote32(remote(&sh.hist.count[bin], r));
                 if (lower < need && need <= (u64)lower + mine) {
                     // thread by thread, as they lie
                     const int i0 = min(tid * row.len, row.n), i1 = min(i0 + row.len, row.n);
@@ -601,6 +633,12 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     const int C = p.C, m = blockIdx.x / C;
     pdl_wait();
     pdl_launch_dependents();
+    // (asked for before the logits: each would otherwise be waited for on its own)
+    const float T = p.temperature ? p.temperature[m] : 1.f;
+    const int k = p.top_k ? p.top_k[m] : 0;
+    const float top_p = p.top_p ? p.top_p[m] : 1.f;
+    const float min_p = p.min_p ? p.min_p[m] : 0.f;
+    const float u = p.u[m];
 
     Row row;
     row.base = (int)rank * p.slice;
@@ -665,8 +703,6 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     best = 0;
     for (int r = 0; r < C; ++r) best = sh.best[r] > best ? sh.best[r] : best;
     row.scale.top = bits_value((uint32_t)(best >> 32));
-    const float T = p.temperature ? p.temperature[m] : 1.f;
-    const int k = p.top_k ? p.top_k[m] : 0;
     const bool none = !(row.scale.top > -INFINITY);
     if (none || !(T > 0.f) || k == 1) {
         if (rank == 0 && tid == 0) {
@@ -677,7 +713,6 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     }
     scale_of(T, row.scale);
 
-    const float top_p = p.top_p ? p.top_p[m] : 1.f;
     const bool by_p = top_p < 1.f;
     if (row.scale.top == INFINITY) {
         // infinities share the mass: equal logits before nothing
@@ -694,10 +729,10 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     // is within 2^-10 of -log2(min_p).
     uint32_t sure = sure_steps(row);
     u64 least = 0;
-    const float min_p = p.min_p ? fminf(p.min_p[m], 1.f) : 0.f;
     if (min_p > 0.f) {
-        least = __float2ull_ru(min_p * (float)(1ull << kMassBits));
-        const uint32_t t = (uint32_t)(fminf(-log2f(min_p), 41.f) * (float)(1 << (kStepBits - 6)));
+        const float ratio = fminf(min_p, 1.f);
+        least = __float2ull_ru(ratio * (float)(1ull << kMassBits));
+        const uint32_t t = (uint32_t)(fminf(-log2f(ratio), 41.f) * (float)(1 << (kStepBits - 6)));
         sure = min(sure, t > 128 ? t - 128 : 0);
         row.limit = min(row.limit, t + 129);
     }
@@ -708,7 +743,7 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     };
     u64 near = 0;
     const uint32_t from = summed <= sure ? summed : 0;
-    u64 own = sweep<false>(row, from, sure, sh, [&](int i, float x, uint32_t steps) { near += mass_at(i, x, steps); });
+    u64 own = sweep<false, true>(row, from, sure, sh, [&](int i, float x, uint32_t steps) { near += mass_at(i, x, steps); });
     own += near + (from ? below : 0);
     const int i0 = min(tid * row.len, row.n), i1 = min(i0 + row.len, row.n);
     u64 upto = own;  // of the warp's threads up to this one
@@ -733,7 +768,6 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
         all += sh.part[row.turn][r];
     }
     for (int i = 0; i < warp; ++i) before += sh.warp_sum[0][i];
-    const float u = p.u[m];
     const u64 goal = !(u > 0.f) ? 0ull : u < 1.f ? share(u, all, false) : all - 1;
     // the thread whose logits hold the first cumulated mass above the goal,
     // then its warp over those logits
