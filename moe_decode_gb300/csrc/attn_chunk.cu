@@ -111,7 +111,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                                                                   const __grid_constant__ CUtensorMap vmap) {
     using S = ChunkShape<D>;
     extern __shared__ uint8_t dyn[];
-    __shared__ int64_t scan[kThreads / 32], found[2];
+    __shared__ int64_t scan[kThreads / 32];
+    __shared__ Start found;
     __shared__ int abort_flag;
     __shared__ int join_info[2][3];  // first CTA, parts, whether this one is the last
     __shared__ uint32_t tmem_base;
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     // wait for what came before is over; none of its results are needed here,
     // so the two overlap. The wait at the end keeps the order for what follows.
     pdl_launch_dependents();
-    const Place at = attn_place<Many, kThreads>(p, blockIdx.x, scan, found);
+    const Place at = attn_place<Many, kThreads>(p, blockIdx.x, scan, &found);
     if (at.begin >= at.end) {
         pdl_wait();
         return;
@@ -266,7 +267,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         Walk<Many> walk(p, at);
-        const int slot = warp >> 2, row = (warp & 3) * 32 + lane;  // row of the slot
+        const int slot = warp >> 2, t = tid & (kSlotRows - 1);
+        const int row = t;  // of the slot: that of the warp's lanes of tensor memory
+        auto piece_at = [&](int slot, int row, int c) {  // 16 bytes of a slot's row
+            return slot * S::kTile + (c >> 3) * S::kPanel + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+        };
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t s_at = lanes + slot * 128, o_at = lanes + S::kColO + slot * D;
         uint32_t s_par = 0, o_par = 0;
@@ -277,23 +282,32 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             const uint32_t first_stage = pos;
             pos += 2 * n;
             if (slot * kSlotRows >= walk.rows) continue;
-            const int R = walk.row0 + slot * kSlotRows + row;
-            const bool real = slot * kSlotRows + row < walk.rows;
+            const int slot_row0 = walk.row0 + slot * kSlotRows;
+            const int slot_rows = min(kSlotRows, walk.rows - slot * kSlotRows);
+            const int R = slot_row0 + row;
+            const bool real = row < slot_rows;
             const int tok = token_of(p, R), head = walk.head * p.group + (R - tok * p.group);
-            // the row into shared memory, 16-byte pieces in the swizzle; rows
-            // past the end are zeros
+            // the slot's rows into shared memory, 16-byte pieces in the swizzle
+            // (a row's pieces by neighbouring threads); rows past the end are
+            // zeros
             {
-                const uint16_t* src = p.q + (walk.q.q0 + tok) * p.q_token + head * p.q_head;
-                uint8_t* dst = sm + slot * S::kTile + row * 128;
-                uint4 v[D / 8];
+                constexpr int kPer = D / 8;
+                uint4 v[kPer];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    v[c] = make_uint4(0, 0, 0, 0);
-                    if (real) v[c] = *reinterpret_cast<const uint4*>(src + c * 8);
+                for (int i = 0; i < kPer; ++i) {
+                    // (the last row again for those past the end: all the loads
+                    // are on their way before the first is waited for)
+                    const int g = i * kSlotRows + t, at_R = slot_row0 + min(g / kPer, slot_rows - 1);
+                    const int q_tok = token_of(p, at_R), q_head = walk.head * p.group + (at_R - q_tok * p.group);
+                    v[i] = *reinterpret_cast<const uint4*>(p.q + (walk.q.q0 + q_tok) * p.q_token + q_head * p.q_head +
+                                                           (g % kPer) * 8);
                 }
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kPanel + (((c & 7) ^ (row & 7)) << 4)) = v[c];
+                for (int i = 0; i < kPer; ++i) {
+                    const int g = i * kSlotRows + t;
+                    *reinterpret_cast<uint4*>(sm + piece_at(slot, g / kPer, g % kPer)) =
+                        g / kPer < slot_rows ? v[i] : make_uint4(0, 0, 0, 0);
+                }
                 fence_proxy_async_shared();
                 mbar_arrive(q_full + 8 * slot);
             }
@@ -301,8 +315,6 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             const int at_pos = walk.q.pos0 + tok;
             const int last = real ? min(at_pos, walk.hi - 1) : -1;
             const int from = p.window > 0 ? at_pos - p.window + 1 : 0;
-            const int slot_row0 = walk.row0 + slot * kSlotRows;
-            const int slot_rows = min(kSlotRows, walk.rows - slot * kSlotRows);
             const int all_to = min(walk.q.pos0 + token_of(p, slot_row0) + 1, walk.hi);
             const int all_from =
                 p.window > 0 ? walk.q.pos0 + token_of(p, slot_row0 + slot_rows - 1) - p.window + 1 : 0;
@@ -394,14 +406,13 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
             const int64_t at_row = (int64_t)(walk.q.q0 + tok) * p.heads + head;
             float* part = p.chunk_part + ((int64_t)blockIdx.x * 2 + walk.part()) * attn_part_floats(kAttnChunkRows, D);
-            const int part_row = slot * kSlotRows + row;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tc_ld32(o_at + 32 * c, o);
                 tc_wait_ld();
-                if (!real) continue;
                 if (whole) {
+                    // by way of the queries' place, which is free
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         uint4 v;
@@ -409,22 +420,35 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                         v.y = pack2<DT>(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
                         v.z = pack2<DT>(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
                         v.w = pack2<DT>(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-                        *reinterpret_cast<uint4*>(p.out + at_row * D + 32 * c + i) = v;
+                        *reinterpret_cast<uint4*>(sm + piece_at(slot, row, 4 * c + i / 8)) = v;
                     }
                 } else {
+                    float4* to = reinterpret_cast<float4*>(part) + (slot * (D / 4) + 8 * c) * kSlotRows + row;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4*>(part + part_row * D + 32 * c + i) =
-                            make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 8; ++i)
+                        to[i * kSlotRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
                 }
             }
-            if (real) {
-                if (!whole) reinterpret_cast<float2*>(part + kAttnChunkRows * D)[part_row] = make_float2(m, l);
-                else if (p.lse) p.lse[at_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-            }
-            if (!whole) {
+            if (whole) {
                 named_bar_sync(1 + slot, kSlotRows);
-                if ((tid & (kSlotRows - 1)) == 0) {
+                constexpr int kPer = D / 8;
+                // (each thread reads the pieces that it writes with the next
+                // item's queries, so no barrier follows)
+#pragma unroll 4
+                for (int i = 0; i < kPer; ++i) {
+                    const int g = i * kSlotRows + t, c = g % kPer, at_R = slot_row0 + g / kPer;
+                    const uint4 v = *reinterpret_cast<const uint4*>(sm + piece_at(slot, g / kPer, c));
+                    if (g / kPer < slot_rows) {
+                        const int o_tok = token_of(p, at_R), o_head = walk.head * p.group + (at_R - o_tok * p.group);
+                        *reinterpret_cast<uint4*>(p.out + ((int64_t)(walk.q.q0 + o_tok) * p.heads + o_head) * D + c * 8) = v;
+                    }
+                }
+                if (real && p.lse) p.lse[at_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                reinterpret_cast<float2*>(part + kAttnChunkRows * D)[slot * kSlotRows + row] = make_float2(m, l);
+                named_bar_sync(1 + slot, kSlotRows);
+                if (t == 0) {
                     const Span span = attn_span(walk, at);
                     join_info[slot][0] = span.cta;
                     join_info[slot][1] = span.parts;
@@ -432,9 +456,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 }
                 named_bar_sync(1 + slot, kSlotRows);
                 if (join_info[slot][2])
-                    attn_join<D, DT, kAttnChunkRows, kSlotRows, 8>(
-                        p, p.chunk_part, Span{join_info[slot][0], join_info[slot][1]}, slot * kSlotRows,
-                        min((slot + 1) * kSlotRows, walk.rows), walk.row0, walk.head, walk.q.q0, tid & (kSlotRows - 1));
+                    attn_join_slot<D, DT>(p, p.chunk_part, Span{join_info[slot][0], join_info[slot][1]}, slot, row, at_row, real);
                 named_bar_sync(1 + slot, kSlotRows);
             }
             // O is read: the next item's first product may write it

@@ -128,19 +128,23 @@ struct Many {
 };
 
 // A place in the order of units, and the CTA's range.
+struct Start {
+    int request, head, row0;
+    int skip;  // units of that item before the range
+    Request q;
+};
 struct Place {
     int64_t total;      // units of the call
     int ctas;           // CTAs with units
     int64_t begin, end; // this CTA's
-    int request;        // request of unit `begin`
-    int64_t rest;       // units of that request before `begin`
+    Start start;        // the item of unit `begin`
 };
 
-// Finds the CTA's range and the request that it begins in, all threads
-// together. `scan` is shared memory of THREADS / 32 values, `found` one of
-// two.
+// Finds the CTA's range and the item that it begins in, all threads together:
+// one of them walks to the item, for all. `scan` is shared memory of THREADS /
+// 32 values.
 template <class Class, int THREADS>
-__device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_t* scan, int64_t* found) {
+__device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_t* scan, Start* found) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + THREADS - 1) / THREADS;
     const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
@@ -159,10 +163,6 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_
         if (lane >= o) sum += v;
     }
     if (lane == 31) scan[warp] = sum;
-    if (tid == 0) {
-        found[0] = p.B;
-        found[1] = 0;
-    }
     __syncthreads();
     Place at;
     at.total = 0;
@@ -177,18 +177,25 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_
     if (own > 0 && before <= at.begin && at.begin < before + own) {
         for (int r = r0; r < r1; ++r) {
             const Request q = attn_request(p, r);
-            const int64_t u = Class::mine(p, q) ? attn_request_units<Class>(p, q) * p.kv_heads : 0;
-            if (at.begin < before + u) {
-                found[0] = r;
-                found[1] = at.begin - before;
+            const int64_t per_head = Class::mine(p, q) ? attn_request_units<Class>(p, q) : 0;
+            if (at.begin < before + per_head * p.kv_heads) {
+                int64_t rest = at.begin - before;
+                const int head = rest < (1 << 30) && per_head < (1 << 30) ? (int)((uint32_t)rest / (uint32_t)per_head)
+                                                                          : (int)(rest / per_head);
+                rest -= head * per_head;
+                RowTiles<Class::kRows> t(p, q);
+                for (int u = Class::kItem + t.tiles(); rest >= u; u = Class::kItem + t.tiles()) {
+                    rest -= u;
+                    t.next();
+                }
+                *found = Start{r, head, t.row0, (int)rest, q};
                 break;
             }
-            before += u;
+            before += per_head * p.kv_heads;
         }
     }
     __syncthreads();
-    at.request = (int)found[0];
-    at.rest = found[1];
+    at.start = *found;  // (anything, for a CTA without units)
     return at;
 }
 
@@ -208,21 +215,8 @@ struct Walk {
     bool over;
 
     __device__ __forceinline__ Walk(const AttnParams& params, const Place& at)
-        : p(params), unit(at.begin), end(at.end), r(at.request), head(0), row0(0), skip(0) {
-        if (unit >= end) return;
-        q = attn_request(p, r);
-        const int64_t per_head = attn_request_units<Class>(p, q);
-        head = at.rest < (1 << 30) && per_head < (1 << 30) ? (int)((uint32_t)at.rest / (uint32_t)per_head)
-                                                           : (int)(at.rest / per_head);
-        int64_t rest = at.rest - head * per_head;
-        RowTiles<ROWS> t(p, q);
-        for (int u = Class::kItem + t.tiles(); rest >= u; u = Class::kItem + t.tiles()) {
-            rest -= u;
-            t.next();
-        }
-        row0 = t.row0;
-        skip = (int)rest;
-    }
+        : p(params), unit(at.begin), end(at.end), r(at.start.request), head(at.start.head), row0(at.start.row0),
+          skip(at.start.skip), q(at.start.q) {}
     __device__ __forceinline__ void item() {
         rows = min(ROWS, q.n * p.group - row0);
         attn_keys(p, q, row0, rows, lo, hi, over);
@@ -353,6 +347,62 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const float* part
             if (d == 0 && p.lse) p.lse[at_row] = sum[u] > 0.f ? (mx[u] + log2f(sum[u])) * kLn2 : -INFINITY;
         }
     }
+}
+
+// A part of the chunk kernel: for each slot of 128 rows four dimensions of all
+// rows after another, so that a warp's 32 rows are stored and read together;
+// then the rows' largest scores and sums. The join, a thread a row.
+template <int D, int DT>
+__device__ __noinline__ void attn_join_slot(const AttnParams& p, const float* parts, const Span& span, int slot, int row,
+                                               int64_t at_row, bool real) {
+    constexpr int kFloats = attn_part_floats(kAttnChunkRows, D), kSlot = 128;
+    const float* first = parts + ((int64_t)span.cta * 2 + 1) * kFloats;
+    const float* rest = parts + (int64_t)span.cta * 2 * kFloats;  // part 0 of the k-th CTA at k * 2 * kFloats
+    auto part_of = [&](int k) { return k == 0 ? first : rest + (int64_t)k * 2 * kFloats; };
+    auto stat_of = [&](int k) {
+        return __ldcg(reinterpret_cast<const float2*>(part_of(k) + kAttnChunkRows * D) + slot * kSlot + row);
+    };
+    float mx = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < span.parts; ++k) mx = fmaxf(mx, stat_of(k).x);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    for (int k = 0; k < span.parts; ++k) {
+        const float2 ml = stat_of(k);
+        sum += exp2_approx(ml.x - ref) * ml.y;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    constexpr int kStep = 16;  // 16-byte loads in flight
+#pragma unroll
+    for (int c0 = 0; c0 < D / 4; c0 += kStep) {
+        float4 v[kStep];
+#pragma unroll
+        for (int c = 0; c < kStep; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < span.parts; ++k) {
+            const float4* f = reinterpret_cast<const float4*>(part_of(k)) + (slot * (D / 4) + c0) * kSlot + row;
+            float4 x[kStep];
+#pragma unroll
+            for (int c = 0; c < kStep; ++c) x[c] = __ldcg(f + c * kSlot);
+            const float w = exp2_approx(stat_of(k).x - ref) * inv;
+#pragma unroll
+            for (int c = 0; c < kStep; ++c) {
+                v[c].x += w * x[c].x;
+                v[c].y += w * x[c].y;
+                v[c].z += w * x[c].z;
+                v[c].w += w * x[c].w;
+            }
+        }
+        if (!real) continue;
+#pragma unroll
+        for (int c = 0; c < kStep; c += 2) {
+            uint4 o;
+            o.x = pack2<DT>(v[c].x, v[c].y);
+            o.y = pack2<DT>(v[c].z, v[c].w);
+            o.z = pack2<DT>(v[c + 1].x, v[c + 1].y);
+            o.w = pack2<DT>(v[c + 1].z, v[c + 1].w);
+            *reinterpret_cast<uint4*>(p.out + at_row * D + (c0 + c) * 4) = o;
+        }
+    }
+    if (real && p.lse) p.lse[at_row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Waits for the phase with parity `parity`, at most timeout_ns; false, with

@@ -24,7 +24,7 @@ struct DecodeShape {
     static constexpr int kOffStat = kOffMerge + kMerge;      // largest score and sum of each warp's rows
     static constexpr int kOffBar = kOffStat + kKeyWarps * kRows * 8;
     static constexpr int kOffMisc = kOffBar + 16 * (kStages + 2);
-    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + 16 + 16;
+    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + (int)sizeof(Start) + 16;
     static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -71,8 +71,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     const uint32_t full = base + S::kOffBar, empty = full + 8 * S::kStages;
     const uint32_t q_full = empty + 8 * S::kStages, q_empty = q_full + 16;
     int64_t* scan = reinterpret_cast<int64_t*>(sm + S::kOffMisc);
-    int64_t* found = scan + kThreads / 32;
-    int& abort_flag = *reinterpret_cast<int*>(found + 2);
+    Start* found = reinterpret_cast<Start*>(scan + kThreads / 32);
+    int& abort_flag = *reinterpret_cast<int*>(found + 1);
     volatile int* join_info = &abort_flag + 1;  // first CTA, parts, whether this one is the last
     if (tid == 0) {
         abort_flag = 0;
