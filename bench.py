@@ -160,11 +160,14 @@ def traffic_record(kernel: str, workload: str):
 
 
 def kernel_source_sha() -> str:
+    """Of the files that the layer kernel is compiled from (the library's other
+    kernels do not change its traffic)."""
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "moe_decode_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
-        h.update(open(os.path.join(csrc, f), "rb").read())
+        if f.startswith("layer_") or f in ("launch_common.cuh", "ptx.cuh"):
+            h.update(open(os.path.join(csrc, f), "rb").read())
     return h.hexdigest()[:16]
 
 

@@ -141,7 +141,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     }
     // The decode kernel runs before this one, and lets it start once its own
     // wait for what came before is over; none of its results are needed here,
-    // so the two overlap. The wait at the end keeps the order for what follows.
+    // so the two overlap (all reads go to the L2, where what came before is).
+    // The wait at the end keeps the order for what follows.
     pdl_launch_dependents();
     const Place at = attn_place<Many, kThreads>(p, blockIdx.x, scan, &found);
     if (at.begin >= at.end) {
@@ -299,8 +300,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                     // are on their way before the first is waited for)
                     const int g = i * kSlotRows + t, at_R = slot_row0 + min(g / kPer, slot_rows - 1);
                     const int q_tok = token_of(p, at_R), q_head = walk.head * p.group + (at_R - q_tok * p.group);
-                    v[i] = *reinterpret_cast<const uint4*>(p.q + (walk.q.q0 + q_tok) * p.q_token + q_head * p.q_head +
-                                                           (g % kPer) * 8);
+                    v[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + (walk.q.q0 + q_tok) * p.q_token +
+                                                                 q_head * p.q_head + (g % kPer) * 8));
                 }
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {

@@ -44,8 +44,9 @@ struct Request {
 
 __device__ __forceinline__ Request attn_request(const AttnParams& p, int r) {
     Request q;
-    const int a = p.q_start[r], b = p.q_start[r + 1];
-    int seq = p.seq[r];
+    // (past the L1: the chunk kernel begins without a wait of its own)
+    const int a = __ldcg(p.q_start + r), b = __ldcg(p.q_start + r + 1);
+    const int seq = __ldcg(p.seq + r);
     q.bad = a < 0 || b < a || b > p.T || seq < 0;
     q.q0 = a;
     q.n = q.bad ? 0 : b - a;
@@ -470,7 +471,7 @@ struct TileFeed {
         if (b.wanted) {
             const int page = key / p.block_size;
             b.token = key - page * p.block_size;
-            b.block = p.tables[(int64_t)walk.r * p.max_blocks + page];
+            b.block = __ldcg(p.tables + (int64_t)walk.r * p.max_blocks + page);
         }
         return b;
     }
