@@ -214,7 +214,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 auto scores = [&](int t, uint32_t i) {
                     const uint32_t a = operand(base + t * S::kTile, 16);
                     const uint32_t b = operand(base + S::kOffKv + (i % S::kStages) * S::kTile, 16);
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k >> 2) * S::kPanel + (k & 3) * 32) >> 4;
                         tc_mma_ss(tmem + t * 128, descriptor(a + off), descriptor(b + off), product<DT>(128, false), k > 0);
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                             p_par ^= 1u << t;
                             tc_fence_after();
                             const uint32_t b = operand(base + S::kOffKv + (pos % S::kStages) * S::kTile, S::kPanel);
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < kAttnTile / 16; ++k)
                                 tc_mma_ts(tmem + S::kColO + t * D, tmem + t * 128 + k * 8, descriptor(b + k * (2048 >> 4)),
                                           product<DT>(D, true), j > 0 || k > 0);
@@ -277,8 +277,14 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
         const uint32_t s_at = lanes + slot * 128, o_at = lanes + S::kColO + slot * D;
         uint32_t s_par = 0, o_par = 0;
         uint32_t pos = 0;  // stages of the items before
+        // A wait that ran out ends the work of the warp, but not its way past the
+        // barriers that others of its slot stand at.
         bool ok = true;
-        for (; ok && walk.next(); walk.done()) {
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && attn_wait(bar, parity, p, flag));
+            return ok;
+        };
+        for (; walk.next(); walk.done()) {
             const int n = walk.t1 - walk.t0;
             const uint32_t first_stage = pos;
             pos += 2 * n;
@@ -323,8 +329,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             float l = 0.f;
             for (int j = 0; j < n; ++j) {
                 const int key0 = (walk.tile0 + walk.t0 + j) * kAttnTile;
-                ok = attn_wait(s_full + 8 * slot, s_par, p, flag);
-                if (!ok) break;
+                if (!wait(s_full + 8 * slot, s_par)) break;
                 s_par ^= 1u;
                 tc_fence_after();
                 uint32_t s[128];
@@ -382,8 +387,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 // NaN is not 0, so they are cleared
                 if (slot == 0 && (key0 < walk.lo || key0 + kAttnTile > walk.hi)) {
                     const uint32_t i = first_stage + 2 * j + 1;
-                    ok = attn_wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1u, p, flag);
-                    if (!ok) break;
+                    if (!wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1u)) break;
                     if (key0 + row < walk.lo || key0 + row >= walk.hi) {
                         uint8_t* v = sm + S::kOffKv + (i % S::kStages) * S::kTile + row * 128;
 #pragma unroll
@@ -398,9 +402,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 tc_fence_before();
                 mbar_arrive(p_full + 8 * slot);
             }
-            if (!ok) break;
-            ok = attn_wait(o_full + 8 * slot, o_par, p, flag);
-            if (!ok) break;
+            wait(o_full + 8 * slot, o_par);
             o_par ^= 1u;
             tc_fence_after();
             const bool whole = walk.whole();

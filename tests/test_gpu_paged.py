@@ -354,3 +354,19 @@ def test_step_on_a_side_stream_and_in_a_graph(api):
             at += n
         ctx.copy_(seq)
         head += taken
+
+
+@pytest.mark.parametrize("heads,kv_heads,d", [(8, 1, 128), (64, 8, 64), (14, 2, 128)])
+@pytest.mark.parametrize("new", [9, 10, 12, 16, 18])
+@pytest.mark.parametrize("grid", [0, 3])
+def test_attention_around_one_slots_rows(api, heads, kv_heads, d, new, grid):
+    """Some 64 to 128 rows a kv head: items of one slot and of both of the chunk
+    kernel, of one tile, of two and of many, next to each other."""
+    lens = [(new, new), (1500, new), (128 + new, new), (127, new), (2000, 3 * new), (129, new), (700, new)]
+    s = make_step(lens, 16, heads, kv_heads, d, torch.bfloat16, new, window=0 if new % 4 else 300)
+    api.set_option(api.OPT_GRID_CTAS, grid)
+    try:
+        out, lse = run_attention(api, s)
+    finally:
+        api.set_option(api.OPT_GRID_CTAS, 0)
+    check_attention(out, lse, attention(s))
