@@ -173,13 +173,20 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     int stage = 0;
     uint32_t parity = 0;
     uint32_t items = 0;
+    // A wait that ran out ends the work of the warp, but not its way past the
+    // barriers that the others stand at.
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t par) {
+        ok = __all_sync(0xffffffffu, ok && attn_wait(bar, par, p, flag));
+        return ok;
+    };
     float2* stat = reinterpret_cast<float2*>(sm + S::kOffStat);  // [key warp][row]
     float* merge = reinterpret_cast<float*>(sm + S::kOffMerge);  // [row][D], groups of 8 columns swizzled by the row
     for (; walk.next(); walk.done()) {
         // (rows past the item's last hold anything; a row's results depend on
         // no other row)
         const uint32_t q_addr = base + S::kOffQ + (items & 1u) * S::kQ + (set * 16 + (lane & 15)) * S::kQRow + (lane >> 4) * 16;
-        bool ok = attn_wait(q_full + 8 * (items & 1u), (items >> 1) & 1u, p, flag);
+        wait(q_full + 8 * (items & 1u), (items >> 1) & 1u);
         const bool active = set * 16 < walk.rows;
         // the last key that each of this thread's two rows sees, and the first
         int last[2], from[2];
@@ -199,8 +206,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
         for (int t = walk.t0; t < walk.t1; ++t) {
-            ok = ok && attn_wait(full + 8 * stage, parity, p, flag);
-            if (!ok) break;
+            if (!wait(full + 8 * stage, parity)) break;
             const int key0 = (walk.tile0 + t) * kAttnTile + kw * kWarpKeys;
             const uint32_t ks = base + stage * S::kStage, vs = ks + S::kHalf;
             if (active && key0 < walk.hi && key0 + kWarpKeys > walk.lo) {
