@@ -394,7 +394,8 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * counts as -inf; +inf shares all the mass. Masses are summed in 64-bit
  * fixed point, so the result does not depend on any order. token int32 [M]
  * (-1 for a row without any logit above -inf), prob fp32 [M] or NULL: the
- * token's share of the kept mass (0 with token -1).
+ * token's share of the kept mass (0 with token -1). A token whose w_i is below
+ * 2^-41 has no part in any of it; temperatures below 1.4e-30 count as that.
  * V <= MOE_SAMPLE_MAX_VOCAB, any M >= 1; logits aligned to their type. */
 #define MOE_SAMPLE_MAX_VOCAB 720896
 int moe_sample(const void* logits, int dtype, int M, int V, int64_t row_stride, const float* u,

@@ -12,9 +12,7 @@
 // core works for the other slot: the order is PV(slot, j), QK(slot, j + 1) for
 // slot 0, then for slot 1, and each completion that lets a slot's warps read
 // S(j + 1) also says that PV(j) is done, so they may rescale O. They do so only
-// where the largest score of a row grew by more than 2^8 over m: weights up to
-// 2^8 lose nothing in fp32 sums or 16-bit weights, and most tiles then need no
-// pass over O.
+// where the largest score of a row has left the reference's range.
 //
 // Two chunks of 8,192 tokens over 16,383 keys (32/8 heads of 128) take 2.54 ms,
 // 1,300 TFLOP/s. A tile of both slots takes 3,500 cycles where its products
@@ -34,7 +32,6 @@ constexpr int kThreads = 384;  // two warpgroups of softmax, one for the two iss
 // registers from the third. Together exactly what the block is launched with.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kIssueRegs = 72;
 static_assert(2 * kSoftmaxRegs + kIssueRegs == 3 * kLaunchRegs, "registers of the block");
-constexpr float kGrow = 8.f;  // log2 of how far a weight may exceed 1
 
 template <int D>
 struct ChunkShape {
@@ -354,10 +351,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(s[i + k]));
                 const float big = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                const bool grows = big > m + kGrow;
+                const bool grows = big > m + WeightRange<DT>::kLimit;
+                const float to = big - WeightRange<DT>::kBias;
                 if (__any_sync(0xffffffffu, grows)) {
-                    const float f = grows ? exp2_approx(m - big) : 1.f;
-                    if (grows) m = big;
+                    const float f = grows ? exp2_approx(m - to) : 1.f;
+                    if (grows) m = to;
                     l *= f;
                     if (j > 0) {
 #pragma unroll

@@ -273,10 +273,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     mx *= p.scale_log2;
-                    const bool grows = mx > m[b];
+                    const bool grows = mx > m[b] + WeightRange<DT>::kLimit;
                     if (__any_sync(0xffffffffu, grows)) {
-                        const float f = grows ? exp2_approx(m[b] - mx) : 1.f;
-                        if (grows) m[b] = mx;
+                        const float to = mx - WeightRange<DT>::kBias;
+                        const float f = grows ? exp2_approx(m[b] - to) : 1.f;
+                        if (grows) m[b] = to;
                         l[b] *= f;
 #pragma unroll
                         for (int i = 0; i < D / 8; ++i) {

@@ -370,3 +370,23 @@ def test_attention_around_one_slots_rows(api, heads, kv_heads, d, new, grid):
     finally:
         api.set_option(api.OPT_GRID_CTAS, 0)
     check_attention(out, lse, attention(s))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("below", [10, 23, 25, 27, 33])
+def test_attention_to_many_keys_far_below_one(api, dtype, new, below):
+    """One key takes nearly all the weight, the others 2^-below of it each, but
+    there are many: what they add has to be there to the type's rounding, also
+    where a weight of 2^-25 is less than fp16 has next to 1."""
+    seq, d = 60000, 64
+    s = make_step([(seq, new)], 16, 4, 2, d, dtype, 31, poison=False)
+    s["q"].fill_(0.5)
+    s["k"].zero_()
+    s["v"].fill_(1.0)
+    first = int(s["table"][0, 0])
+    # q.k / sqrt(d) = 64 * 0.5 * x / 8 = 4 x, in nats
+    s["k"][first, 3] = below * math.log(2) / 4
+    s["v"][first, 3] = 0.0
+    out, lse = run_attention(api, s)
+    check_attention(out, lse, attention(s))
