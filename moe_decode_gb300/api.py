@@ -284,10 +284,14 @@ def _raw_stream(stream) -> int:
     return _current_raw_stream(torch.cuda.current_device())
 
 
-def _vector(t: Optional[torch.Tensor], n: Optional[int], dtype: torch.dtype, what: str):
-    """A contiguous device vector of n elements (None: any number), or None."""
-    if t is not None:
-        _want(t.dtype == dtype and t.is_contiguous() and t.is_cuda and (n is None or t.numel() == n), what)
+def _vectors(what: str, dtype: torch.dtype, *pairs):
+    """Each pair (tensor or None, elements or None for any number): contiguous
+    device tensors of one dtype."""
+    for t, n in pairs:
+        if t is not None and (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()
+                              or (n is not None and t.numel() != n)):
+            raise MoeError(EINVAL, f"{what}: {dtype}, contiguous, on the device, {n if n is not None else 'any number of'}"
+                                   f" elements; got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 class KvCache:
@@ -328,18 +332,9 @@ def paged_plan(ctx_lens, new_lens, free_list, block_tables, block_size: int, q_s
     (updated in place), outputs q_start [B + 1], seq_lens [B], slot_map [T],
     positions [T], taken [1]; free_head [1] is where the free list begins."""
     B, T = ctx_lens.numel(), slot_map.numel()
-    i32 = torch.int32
-    _vector(ctx_lens, B, i32, "paged_plan: ctx_lens int32 [B]")
-    _vector(new_lens, B, i32, "paged_plan: new_lens int32 [B]")
-    _vector(free_list, None, i32, "paged_plan: free_list int32 [F]")
-    _vector(free_head, 1, i32, "paged_plan: free_head int32 [1]")
     _want(block_tables.dim() == 2 and block_tables.shape[0] == B, "paged_plan: block_tables int32 [B, W]")
-    _vector(block_tables, None, i32, "paged_plan: block_tables int32 [B, W]")
-    _vector(q_start, B + 1, i32, "paged_plan: q_start int32 [B + 1]")
-    _vector(seq_lens, B, i32, "paged_plan: seq_lens int32 [B]")
-    _vector(slot_map, T, i32, "paged_plan: slot_map int32 [T]")
-    _vector(positions, T, i32, "paged_plan: positions int32 [T]")
-    _vector(taken, 1, i32, "paged_plan: taken int32 [1]")
+    _vectors("paged_plan", torch.int32, (ctx_lens, B), (new_lens, B), (free_list, None), (free_head, 1),
+             (block_tables, None), (q_start, B + 1), (seq_lens, B), (slot_map, T), (positions, T), (taken, 1))
     rc = lib.moe_paged_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, free_list.data_ptr(), free_list.numel(),
                             _raw(free_head), block_tables.data_ptr(), block_tables.shape[1], block_size,
                             q_start.data_ptr(), seq_lens.data_ptr(), slot_map.data_ptr(), _raw(positions), T,
@@ -357,7 +352,7 @@ def paged_append(k_new, v_new, slot_map, cache: KvCache, ws, stream=None):
           "paged_append: k_new, v_new [T, kv_heads, head_dim]", ESHAPE)
     _want(k_new.dtype == cache.dtype and v_new.dtype == cache.dtype and k_new.stride(2) == 1 and v_new.stride(2) == 1
           and k_new.is_cuda and v_new.is_cuda, "paged_append: k_new, v_new of the cache's dtype on the device")
-    _vector(slot_map, T, torch.int32, "paged_append: slot_map int32 [T]")
+    _vectors("paged_append: slot_map", torch.int32, (slot_map, T))
     kt, kh, _ = k_new.stride()
     vt, vh, _ = v_new.stride()
     rc = lib.moe_paged_append(k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T, slot_map.data_ptr(), cache._ref,
@@ -379,10 +374,9 @@ def paged_attention(q, cache: KvCache, block_tables, q_start, seq_lens, out, ws,
     _want(q.dtype == cache.dtype and out.dtype == cache.dtype and q.is_cuda and out.is_cuda
           and q.stride(2) == 1 and out.is_contiguous(), "paged_attention: q, out of the cache's dtype on the device")
     _want(block_tables.dim() == 2 and block_tables.shape[0] == B, "paged_attention: block_tables int32 [B, W]")
-    _vector(block_tables, None, torch.int32, "paged_attention: block_tables int32 [B, W]")
-    _vector(q_start, B + 1, torch.int32, "paged_attention: q_start int32 [B + 1]")
-    _vector(seq_lens, B, torch.int32, "paged_attention: seq_lens int32 [B]")
-    _vector(lse, T * heads, torch.float32, "paged_attention: lse fp32 [T, q_heads]")
+    _vectors("paged_attention: block_tables, q_start, seq_lens", torch.int32, (block_tables, None), (q_start, B + 1),
+             (seq_lens, B))
+    _vectors("paged_attention: lse", torch.float32, (lse, T * heads))
     qt, qh, _ = q.stride()
     rc = lib.moe_paged_attention(q.data_ptr(), qt, qh, T, heads, cache._ref, block_tables.data_ptr(),
                                  block_tables.shape[1], q_start.data_ptr(), seq_lens.data_ptr(), B, scale, window,
@@ -402,14 +396,9 @@ def sample(logits, u, tokens, probs=None, temperature=None, top_k=None, top_p=No
     M, V = logits.shape
     _want(logits.dtype in _LOGITS and logits.is_cuda and (V == 1 or logits.stride(1) == 1),
           "sample: logits fp32 or bf16 [M, V], rows contiguous, on the device")
-    f32 = torch.float32
-    _vector(u, M, f32, "sample: u fp32 [M]")
-    _vector(tokens, M, torch.int32, "sample: tokens int32 [M]")
-    _vector(probs, M, f32, "sample: probs fp32 [M]")
-    _vector(temperature, M, f32, "sample: temperature fp32 [M]")
-    _vector(top_k, M, torch.int32, "sample: top_k int32 [M]")
-    _vector(top_p, M, f32, "sample: top_p fp32 [M]")
-    _vector(min_p, M, f32, "sample: min_p fp32 [M]")
+    _vectors("sample: u, probs, temperature, top_p, min_p", torch.float32, (u, M), (probs, M), (temperature, M), (top_p, M),
+             (min_p, M))
+    _vectors("sample: tokens, top_k", torch.int32, (tokens, M), (top_k, M))
     rc = lib.moe_sample(logits.data_ptr(), _LOGITS[logits.dtype], M, V, logits.stride(0) if M > 1 else V, u.data_ptr(),
                         _raw(temperature), _raw(top_k), _raw(top_p), _raw(min_p), tokens.data_ptr(), _raw(probs),
                         _raw_stream(stream))
