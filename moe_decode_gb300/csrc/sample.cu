@@ -150,6 +150,34 @@ __device__ __forceinline__ u64 mass_of(float x, const Scale& s) {
     return mant >> (n + 127u - (b >> 23));
 }
 
+// Both for two logits, with the paired fp32 operations: the same roundings, so
+// the same bits.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 minus(float2 a, float2 b) { return ffma2(b, both(-1.f), a); }  // a - b
+__device__ __forceinline__ void steps_of(float2 x, const Scale& s, uint32_t (&steps)[2]) {
+    const float2 t = ffma2(minus(both(s.top), x), both(s.hi), both(64.f));
+    steps[0] = __float_as_uint(t.x) - 0x42800000u;
+    steps[1] = __float_as_uint(t.y) - 0x42800000u;
+}
+__device__ __forceinline__ void mass_of(float2 x, const Scale& s, u64 (&mass)[2]) {
+    const float2 top = both(s.top), hi = both(s.hi), lo = both(s.lo), round = both(12582912.f);
+    const float2 d = minus(top, x);
+    const float2 bb = minus(d, top), err = minus(minus(top, minus(d, bb)), __fadd2_rn(x, bb));
+    const float2 minus_t = __fmul2_rn(d, both(-s.hi));
+    const float2 rest = __fadd2_rn(ffma2(d, hi, minus_t), ffma2(d, lo, __fmul2_rn(err, hi)));
+    const float2 whole = minus(round, minus_t);
+    const float2 minus_f = minus(__fadd2_rn(minus(whole, round), minus_t), rest);
+    float e[2];
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e[0]) : "f"(minus_f.x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e[1]) : "f"(minus_f.y));
+    const uint32_t n[2] = {__float_as_uint(whole.x) & 0x3fu, __float_as_uint(whole.y) & 0x3fu};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t b = __float_as_uint(e[i]);
+        mass[i] = ((u64)((b & 0x7fffffu) | 0x800000u) << (kMassBits - 23)) >> (n[i] + 127u - (b >> 23));
+    }
+}
+
 // log2(e) / T as a sum of two fp32, without fp64 (two operations a clock and
 // SM here: a division by every thread cost 10 us a call).
 __device__ __forceinline__ void scale_of(float T, Scale& s) {
@@ -247,18 +275,23 @@ __device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to,
     for (int i = i0; i < i1; i += 4) {
         const float4 q = *reinterpret_cast<const float4*>(row.x + i);
         const float x[4] = {q.x, q.y, q.z, q.w};
-        uint32_t steps[4];
+        uint32_t steps[4], two[2];
+        steps_of(make_float2(q.x, q.y), row.scale, two);
+        steps[0] = two[0], steps[1] = two[1];
+        steps_of(make_float2(q.z, q.w), row.scale, two);
+        steps[2] = two[0], steps[3] = two[1];
         bool in = false, near = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            steps[j] = steps_of(x[j], row.scale);
             in |= steps[j] - from < span;
             near |= steps[j] - to < few;
         }
         if (in) {
-            u64 w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = mass_of(x[j], row.scale);
+            u64 w[4], pair[2];
+            mass_of(make_float2(q.x, q.y), row.scale, pair);
+            w[0] = pair[0], w[1] = pair[1];
+            mass_of(make_float2(q.z, q.w), row.scale, pair);
+            w[2] = pair[0], w[3] = pair[1];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sum += steps[j] - from < span ? w[j] : 0;
