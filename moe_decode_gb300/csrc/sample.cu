@@ -318,16 +318,6 @@ __device__ __forceinline__ u64 sweep(const Row& row, uint32_t from, uint32_t to,
     if (!OWN) flush();
     return sum;
 }
-// f(i, x, code) for each of the slice's members of the kept set with steps from
-// `from` on.
-template <class F>
-__device__ __forceinline__ void each_member(const Row& row, uint32_t from, Shared& sh, F f) {
-    sweep<false, false>(row, from, from, sh, [&](int i, float x, uint32_t steps) {
-        const u64 code = code_of(steps, x);
-        if (kept(row, code, row.base + i)) f(i, x, code);
-    });
-}
-
 // A run of 2^width codes from `from` on.
 struct Range {
     u64 from;
@@ -441,12 +431,17 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
 // Gathers the range's members in the first CTA, which ranks them and finds the
 // last one that is kept: the count-th (0: the last of all) and, with by_mass,
 // the first up to which the mass reaches `goal`, or where that is 0 `part` of
-// the mass up to the count-th. False when there are more than kList.
+// the mass up to the count-th. False when there are more than kList. WITH_BELOW:
+// the goal counts from the first of all; the thread's mass before the range
+// (which begins with a step) is left in `below`.
+template <bool WITH_BELOW>
 __device__ __forceinline__ bool settle(Row& row, const Range range, u64 count, bool by_mass, u64 goal, float part,
-                                       Shared& sh, uint32_t rank, int C) {
+                                       u64& below, Shared& sh, uint32_t rank, int C) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    each_member(row, (uint32_t)(range.from >> 32), sh, [&](int i, float x, u64 code) {
-        if (!range.has(code)) return;
+    const uint32_t first = (uint32_t)(range.from >> 32);
+    const u64 own = sweep<false, false>(row, WITH_BELOW ? 0 : first, first, sh, [&](int i, float x, uint32_t steps) {
+        const u64 code = code_of(steps, x);
+        if (!range.has(code) || !kept(row, code, row.base + i)) return;
         const uint32_t at = atom_add_remote32(remote(&sh.listed, 0), 1u);
         if (at < kList) {
             st_remote64(remote(&sh.list.code[at], 0), code);
@@ -454,7 +449,20 @@ __device__ __forceinline__ bool settle(Row& row, const Range range, u64 count, b
             st_remote32(remote(&sh.list.index[at], 0), row.base + i);
         }
     });
+    if (WITH_BELOW) {
+        below = own;
+        const u64 sum = warp_sum(own);
+        if (lane == 0) sh.warp_sum[0][warp] = sum;
+        __syncthreads();
+        if (tid == 0) {
+            u64 all = 0;
+            for (int w = 0; w < kWarps; ++w) all += sh.warp_sum[0][w];
+            st_remote64(remote(&sh.part[row.turn][rank], 0), all);
+        }
+    }
     cluster_sync();
+    if (WITH_BELOW)
+        for (int r = 0; r < C; ++r) goal -= sh.part[row.turn][r];  // (the first CTA's alone is used)
     const uint32_t members = ld_remote32(remote(&sh.listed, 0));
     const bool fits = members <= kList;
     if (rank == 0 && fits) {
@@ -538,7 +546,7 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
             locate<kByCount>(row, target, 0.f, 0, all, sh, rank, C);
             if (sh.bin_count) {
                 row.limit = min(row.limit, (sh.bin + 1) << (kStepBits - kBinBits));
-                if (k <= kList && settle(row, range, (u64)k, by_p, 0, part, sh, rank, C)) return;
+                if (k <= kList && settle<false>(row, range, (u64)k, by_p, 0, part, below, sh, rank, C)) return;
             }
             clear();
         } else {
@@ -556,7 +564,17 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
             row.limit = min(row.limit, (b2 + 1) << (kStepBits - kBinBits));
             summed = b1 << (kStepBits - kBinBits);
             all = 0;
+            // few members there (a row with some likely tokens): ranked at once
+            uint32_t members = kList + 1;
+            if (b2 - b1 < 16) {
+                members = 0;
+                for (uint32_t b = b1; b <= b2; ++b) members += sh.all.count[b];
+            }
             clear();
+            if (members <= kList) {
+                settle<true>(row, range, 0, true, target, 0.f, below, sh, rank, C);
+                return;
+            }
         }
         for (bool again = false;; again = true) {
             range.split();
@@ -589,7 +607,7 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
             }
             const u64 rest = by_mass ? target - sh.before : target;
             if (members <= kList) {
-                settle(row, range, by_mass ? 0 : rest, by_mass, rest, 0.f, sh, rank, C);
+                settle<false>(row, range, by_mass ? 0 : rest, by_mass, rest, 0.f, below, sh, rank, C);
                 break;
             }
             if (shift == 0) {
