@@ -345,6 +345,9 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
     if (tid == 0) {
         sh.bin_count = 0;
         sh.bin_to = kBins - 1;
+        // (here, before a barrier of the cluster: what follows may append to the
+        // first CTA's list at once)
+        sh.listed = 0;
     }
     __syncthreads();
     if (tid < C) {
@@ -532,7 +535,6 @@ __device__ __forceinline__ void narrow(Row& row, int k, bool by_p, float part, f
             sh.hist.count[i] = 0;
             sh.hist.mass[i] = 0;  // (and so the places)
         }
-        if (tid == 0) sh.listed = 0;
         __syncthreads();
     };
     for (int stage = k > 0 ? 0 : 1; stage < (by_p ? 2 : 1); ++stage) {

@@ -161,3 +161,29 @@ def test_same_token_on_any_split(api):
     for r in range(0, 40, 7):
         alone = run(api, x[r:r + 1], u[r:r + 1], top_p=0.93, temperature=1.1)
         assert alone[0][0] == together[0][r] and alone[1][0] == together[1][r]
+
+
+@pytest.mark.parametrize("settings", [dict(top_p=0.9), dict(top_k=50, top_p=0.9, min_p=0.01), dict(top_k=1000, top_p=0.5)], ids=str)
+def test_the_same_on_every_call(api, settings):
+    """Rows over 8 and 16 CTAs, 3,000 calls beside another stream's work, which
+    shifts the CTAs of a row against each other: the order in which they reach
+    each other's memory must not show."""
+    rows = [logits_of(M, V, 90 + M, dtype, spread) for M, V, dtype, spread in
+            ((14, 49633, torch.bfloat16, 0.01), (27, 38039, torch.float32, 3.0), (5, 157184, torch.float32, 2.0))]
+    side, noise = torch.cuda.Stream(), torch.randn((2048, 2048), device="cuda")
+    for x, u in rows:
+        M = x.shape[0]
+        f = {n: torch.full((M,), v, device="cuda").to(torch.int32 if n == "top_k" else torch.float32) for n, v in settings.items()}
+        u = u.cuda()
+        first, tokens = torch.empty(M, dtype=torch.int32, device="cuda"), torch.empty(M, dtype=torch.int32, device="cuda")
+        p0, probs = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        api.sample(x, u, first, probs=p0, **f)
+        differ = torch.zeros((), dtype=torch.int64, device="cuda")
+        for i in range(1000):
+            if i % 4 == 0:
+                with torch.cuda.stream(side):
+                    noise = noise @ noise * 1e-3
+            api.sample(x, u, tokens, probs=probs, **f)
+            differ += ((tokens != first) | (probs != p0)).sum()
+        torch.cuda.synchronize()
+        assert differ.item() == 0
