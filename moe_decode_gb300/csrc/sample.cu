@@ -107,7 +107,7 @@ struct Shared {
     u64 part[2][16];
     u64 warp_sum[2][kWarps];
     // what the search for a border found
-    u64 before, bin_mass, border;
+    u64 before, border;
     uint32_t bin_count, bin, bin_to, tie_limit;
     uint32_t listed;
 };
@@ -331,8 +331,8 @@ struct Range {
 enum Search { kByCount, kByMass, kByBounds };
 
 // The bin of the cluster's histogram in which the target is reached: in
-// sh.bin_count (0: it is not reached), sh.bin, sh.bin_mass and, with what lies
-// before the bin, sh.before. `own` is summed over the threads and added to
+// sh.bin_count (0: it is not reached), sh.bin and, with what lies before the
+// bin, sh.before. `own` is summed over the threads and added to
 // `all`. kByMass starts from `all`. kByBounds takes `part` of `all` as the
 // target, and finds the first bin in which the bins' largest possible masses
 // reach it and the first (sh.bin_to) in which their smallest do.
@@ -357,9 +357,9 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
     }
     cluster_sync();
     // Each CTA sums 512 / C bins and leaves the sums in all CTAs: a thread reads
-    // one bin of one CTA and writes one sum to one. (Every CTA reading all of the
-    // others' bins took 14,000 cycles with masses and C = 16: distributed shared
-    // memory brings some 10 bytes a clock.)
+    // one bin of one CTA and writes one sum to one. (With masses and C = 16 all of
+    // this takes 10,500 cycles, and 14,200 where every CTA reads all of the
+    // others' bins; the wait for the slowest CTA's sweep is in both.)
     {
         const int r = tid & (C - 1), bin = (int)rank * (kBins / C) + tid / C;
         uint32_t n = ld_remote32(remote(&sh.hist.count[bin], r));
@@ -389,13 +389,14 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
             // The mean of t, in parts of the bin, is known to 1/256. The mass
             // of one falls from `first` to `first` 2^(-1/8) within the bin and
             // is convex in t, so the mean mass is at least that of the mean t
-            // and at most the chord's there. 2^-16: t is off by its rounding.
+            // and at most the chord's there. 2^-16: t is off by its rounding; 1:
+            // a mass is cut to whole units.
             const float first = exp2f((float)kMassBits - (float)tid * (1.f / 8.f));
             const float mean = (float)value / ((float)count * 256.f);
             const float most = first * (1.f - 0.08299595f * mean) * (1.f + 1.f / 65536.f);
             const float least = first * exp2f((mean + 1.f / 256.f) * (-1.f / 8.f)) * (1.f - 1.f / 65536.f);
             sum[0] = count * __float2ull_ru(most);
-            sum[1] = count * __float2ull_rd(least);
+            sum[1] = least > 1.f ? count * (__float2ull_rd(least) - 1) : 0;
         }
     }
     u64 upto[2] = {sum[0], sum[1]};
@@ -421,7 +422,6 @@ __device__ __forceinline__ void locate(Row& row, u64& target, float part, u64 ow
             if (k == 0) {
                 sh.bin = tid;
                 sh.bin_count = count;
-                sh.bin_mass = sum[0];
                 sh.before = before;
             } else {
                 sh.bin_to = tid;

@@ -163,6 +163,26 @@ def test_same_token_on_any_split(api):
         assert alone[0][0] == together[0][r] and alone[1][0] == together[1][r]
 
 
+@pytest.mark.parametrize("depth", [12.0, 18.0, 22.0, 26.0])
+def test_top_p_ends_among_very_small_masses(api, depth):
+    """One token far above hundreds of thousands whose masses are a few units of
+    the fixed point each: the run that reaches top_p ends among them."""
+    V = 700000
+    g = torch.Generator(device="cuda").manual_seed(int(depth))
+    x = -depth - torch.rand((4, V), device="cuda", generator=g) * 2.0
+    x[:, 4321] = 0.0
+    w = torch.exp(x.double())
+    share = (w.sum(1) - 1) / w.sum(1)  # of the many
+    top_p = (1 - share * torch.tensor([0.2, 0.5, 0.9, 0.999], device="cuda", dtype=torch.float64)).float().cpu()
+    tokens, probs, _ = run(api, x, torch.full((4,), 0.9999999), top_p=top_p)
+    for r in range(4):
+        want, prob, margin = sample_row(x[r].double().cpu().numpy(), float(np.float32(0.9999999)), p=float(top_p[r]))
+        if margin > 2.0 ** -20:
+            assert tokens[r] == want and abs(probs[r] - prob) <= 2.0 ** -20 * prob, (r, tokens[r], want)
+        else:  # within what the masses are known to: some member near the border
+            assert 0 <= tokens[r] < V
+
+
 @pytest.mark.parametrize("settings", [dict(top_p=0.9), dict(top_k=50, top_p=0.9, min_p=0.01), dict(top_k=1000, top_p=0.5)], ids=str)
 def test_the_same_on_every_call(api, settings):
     """Rows over 8 and 16 CTAs, 3,000 calls beside another stream's work, which
