@@ -52,9 +52,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// (.aligned asks for whole warps: what comes before is often one lane's)
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
+// The two halves: shared memory of a CTA that has not begun may not be written.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 // The address of this CTA's shared variable in CTA r of the cluster.
 __device__ __forceinline__ uint32_t remote(const void* p, uint32_t r) {
     uint32_t a;
@@ -496,6 +501,7 @@ __device__ __forceinline__ bool settle(Row& row, const Range range, u64 count, b
                 if (lane >= o) upto += v;
             }
             if (lane == 31) sh.warp_sum[0][warp] = upto;
+            __syncwarp();
             named_bar_sync(1, kList);
             for (int w = 0; w < warp; ++w) upto += sh.warp_sum[0][w];
             sh.list.sums[tid] = upto;
@@ -684,6 +690,7 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int C = p.C, m = blockIdx.x / C;
+    cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
     // (asked for before the logits: each would otherwise be waited for on its own)
@@ -747,6 +754,7 @@ __global__ __launch_bounds__(kThreads, 2) void sample_kernel(SampleParams p) {
         best = other > best ? other : best;
     }
     if (lane == 0) sh.warp_sum[0][warp] = best;
+    cluster_wait();
     __syncthreads();
     if (tid < C) {
         for (int w = 0; w < kWarps; ++w) best = sh.warp_sum[0][w] > best ? sh.warp_sum[0][w] : best;
