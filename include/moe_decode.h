@@ -392,7 +392,9 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * temperature <= 0 (or NaN) takes the largest logit's lowest index;
  * temperature NULL is 1. u fp32 [M] in [0, 1) (clamped to it). A NaN logit
  * counts as -inf; +inf shares all the mass. Masses are summed in 64-bit
- * fixed point, so the result does not depend on any order. token int32 [M]
+ * fixed point, so the result does not depend on any order; each is off by some
+ * 2^-22 of itself and a unit of 2^-42, so where a mass meets min_p, or a sum
+ * top_p or u, more closely than that, either side may be taken. token int32 [M]
  * (-1 for a row without any logit above -inf), prob fp32 [M] or NULL: the
  * token's share of the kept mass (0 with token -1). A token whose w_i is below
  * 2^-41 has no part in any of it; temperatures below 1.4e-30 count as that.
