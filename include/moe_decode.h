@@ -368,7 +368,9 @@ int moe_paged_append(const void* k_new, int64_t k_token_stride, int64_t k_head_s
  * Products are summed in fp32, the softmax weights rounded once to the
  * cache's type for the second product. Pages that hold no visible key are
  * not read (their table entries may be anything), and what lies in a page
- * beyond the visible keys may be anything, NaN included. A visible key whose
+ * beyond the visible keys may be anything, NaN included. A row that sees a NaN
+ * score is NaN, in lse too; a value that is NaN or infinite may also reach the
+ * request's rows that do not see it yet (as 0 * NaN). A visible key whose
  * page is not in [0, n_blocks), or beyond max_blocks, is reported
  * (MOE_EDEVICE_BAD_INDEX) and that request's outputs are unspecified.
  * scale <= 0 takes 1 / sqrt(head_dim). block_tables int32 [B, max_blocks].

@@ -411,7 +411,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             o_par ^= 1u;
             tc_fence_after();
             const bool whole = walk.whole();
-            const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+            const float inv = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;
             const int64_t at_row = (int64_t)(walk.q.q0 + tok) * p.heads + head;
             float* part = p.chunk_part + ((int64_t)blockIdx.x * 2 + walk.part()) * attn_part_floats(kAttnChunkRows, D);
 #pragma unroll
@@ -452,7 +452,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                         *reinterpret_cast<uint4*>(p.out + ((int64_t)(walk.q.q0 + o_tok) * p.heads + o_head) * D + c * 8) = v;
                     }
                 }
-                if (real && p.lse) p.lse[at_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                if (real && p.lse) p.lse[at_row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             } else {
                 reinterpret_cast<float2*>(part + kAttnChunkRows * D)[slot * kSlotRows + row] = make_float2(m, l);
                 named_bar_sync(1 + slot, kSlotRows);

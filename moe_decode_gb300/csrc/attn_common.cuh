@@ -284,6 +284,7 @@ template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 __device__ __forceinline__ float exp2_approx(float x);
 
+// (A sum of weights is 0, NaN or above 0: NaN has to reach the output and lse.)
 // Joins the parts of an item, in the order of the keys (the part 1 of the CTA
 // that it begins in, then the part 0 of the CTAs after it): THREADS threads,
 // the rows [from, to). A thread takes U pieces of 8 dimensions at a time, all
@@ -335,7 +336,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const float* part
             const int i = i0 + u * THREADS;
             if (i >= end) break;
             const int row = i / kPer, d = (i % kPer) * 8;
-            const float inv = sum[u] > 0.f ? 1.f / sum[u] : 0.f;
+            const float inv = sum[u] != 0.f ? 1.f / sum[u] : 0.f;
             const int R = row0 + row, t = token_of(p, R), h = head * p.group + (R - t * p.group);
             const int64_t at_row = (int64_t)(token0 + t) * p.heads + h;
             uint4 o;
@@ -344,7 +345,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const float* part
             o.z = pack2<DT>(v[u][4] * inv, v[u][5] * inv);
             o.w = pack2<DT>(v[u][6] * inv, v[u][7] * inv);
             *reinterpret_cast<uint4*>(p.out + at_row * D + d) = o;
-            if (d == 0 && p.lse) p.lse[at_row] = sum[u] > 0.f ? (mx[u] + log2f(sum[u])) * kLn2 : -INFINITY;
+            if (d == 0 && p.lse) p.lse[at_row] = sum[u] != 0.f ? (mx[u] + log2f(sum[u])) * kLn2 : -INFINITY;
         }
     }
 }
@@ -372,7 +373,7 @@ __device__ __noinline__ void attn_join_slot(const AttnParams& p, const float* pa
         const float2 ml = stat_of(k);
         sum += exp2_approx(ml.x - ref) * ml.y;
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
     constexpr int kStep = 16;  // 16-byte loads in flight
 #pragma unroll
     for (int c0 = 0; c0 < D / 4; c0 += kStep) {
@@ -404,7 +405,7 @@ __device__ __noinline__ void attn_join_slot(const AttnParams& p, const float* pa
             *reinterpret_cast<uint4*>(p.out + at_row * D + (c0 + c) * 4) = o;
         }
     }
-    if (real && p.lse) p.lse[at_row] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    if (real && p.lse) p.lse[at_row] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Waits for the phase with parity `parity`, at most timeout_ns; false, with

@@ -386,7 +386,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             const float4 y = *reinterpret_cast<const float4*>(merge + row * D + (c ^ (row & 3)) * 8 + 4);
             if (whole) {
                 const float2 ml = stat[row];
-                const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+                const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
                 const int R = walk.row0 + row, t = token_of(p, R), h = walk.head * p.group + (R - t * p.group);
                 const int64_t at_row = (int64_t)(walk.q.q0 + t) * p.heads + h;
                 uint4 v;
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 v.z = pack2<DT>(y.x * inv, y.y * inv);
                 v.w = pack2<DT>(y.z * inv, y.w * inv);
                 *reinterpret_cast<uint4*>(p.out + at_row * D + c * 8) = v;
-                if (c == 0 && p.lse) p.lse[at_row] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
+                if (c == 0 && p.lse) p.lse[at_row] = ml.y != 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
             } else {
                 *reinterpret_cast<float4*>(part + row * D + c * 8) = x;
                 *reinterpret_cast<float4*>(part + row * D + c * 8 + 4) = y;

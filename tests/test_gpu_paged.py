@@ -390,3 +390,26 @@ def test_attention_to_many_keys_far_below_one(api, dtype, new, below):
     s["v"][first, 3] = 0.0
     out, lse = run_attention(api, s)
     check_attention(out, lse, attention(s))
+
+
+@pytest.mark.parametrize("grid", [0, 1, 61])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_to_a_nan_key(api, d, grid):
+    """Rows that see a NaN score are NaN, in lse too (-inf would say that they
+    see nothing); the rows before it and the other heads are as without it."""
+    s = make_step([(1000, 1), (2000, 6), (900, 300), (333, 20)], 16, 8, 2, d, torch.bfloat16, d)
+    api.set_option(api.OPT_GRID_CTAS, grid)
+    try:
+        out, lse = run_attention(api, s)
+        hit = torch.zeros_like(lse, dtype=torch.bool)
+        table, t0 = s["table"].cpu(), 0
+        for b, (seq, n) in enumerate(s["lens"]):
+            key = seq - (n + 1) // 2
+            s["k"][int(table[b, key // 16]), key % 16, 1] = math.nan
+            hit[t0 + n - (n + 1) // 2:t0 + n, 4:] = True
+            t0 += n
+        got, z = run_attention(api, s)
+    finally:
+        api.set_option(api.OPT_GRID_CTAS, 0)
+    assert got[hit].isnan().all() and z[hit].isnan().all()
+    assert torch.equal(got[~hit], out[~hit]) and torch.equal(z[~hit], lse[~hit])
