@@ -325,10 +325,9 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             // keys that the row sees, and that all or any rows of the slot see
             const int at_pos = walk.q.pos0 + tok;
             const int last = real ? min(at_pos, walk.hi - 1) : -1;
-            const int from = p.window > 0 ? at_pos - p.window + 1 : 0;
+            const int from = first_seen(p, at_pos);
             const int all_to = min(walk.q.pos0 + token_of(p, slot_row0) + 1, walk.hi);
-            const int all_from =
-                p.window > 0 ? walk.q.pos0 + token_of(p, slot_row0 + slot_rows - 1) - p.window + 1 : 0;
+            const int all_from = first_seen(p, walk.q.pos0 + token_of(p, slot_row0 + slot_rows - 1));
             float m = -INFINITY;  // reference of the weights, in log2
             float l = 0.f;
             for (int j = 0; j < n; ++j) {

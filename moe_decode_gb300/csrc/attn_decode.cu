@@ -204,10 +204,10 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             const int row = set * 16 + b * 8 + quad;
             const int pos = walk.q.pos0 + token_of(p, walk.row0 + row);
             last[b] = row < walk.rows ? min(pos, walk.hi - 1) : -1;
-            from[b] = p.window > 0 ? pos - p.window + 1 : 0;
+            from[b] = first_seen(p, pos);
         }
         const int all_to = min(walk.q.pos0 + token_of(p, walk.row0) + 1, walk.hi);
-        const int all_from = p.window > 0 ? walk.q.pos0 + token_of(p, walk.row0 + walk.rows - 1) - p.window + 1 : 0;
+        const int all_from = first_seen(p, walk.q.pos0 + token_of(p, walk.row0 + walk.rows - 1));
         float o[D / 8][4];
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll

@@ -50,6 +50,13 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int r) {
     return q;
 }
 
+// The first key that a row at position pos sees. (Without a step past 32 bits,
+// however wide the window and however far below zero the position: an overflow
+// is undefined, and the counts of units of the CTAs' roles then need not agree.)
+__device__ __forceinline__ int first_seen(const AttnParams& p, int pos) {
+    return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
 // Keys [lo, hi) that the rows [row0, row0 + rows) of a request see between
 // them, inside the block table; `over` where a row sees past it.
 __device__ __forceinline__ void attn_keys(const AttnParams& p, const Request& q, int row0, int rows, int& lo, int& hi,
@@ -58,7 +65,7 @@ __device__ __forceinline__ void attn_keys(const AttnParams& p, const Request& q,
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
     over = last + 1 > cap;
     hi = (int)min((int64_t)last + 1, cap);
-    lo = p.window > 0 ? max(first - p.window + 1, 0) : 0;
+    lo = first_seen(p, first);
     if (hi <= lo) lo = hi = 0;
 }
 
@@ -87,8 +94,7 @@ struct RowTiles {
         if (first_rem + step_rem == 0 || first_rem + step_rem == p.group) --last;  // which may begin there
         if (row0 + ROWS >= rows) last = token_of(p, rows - 1);
         const int hi = (int)min((int64_t)pos0 + last + 1, cap);
-        const int lo = p.window > 0 ? max(pos0 + first - p.window + 1, 0) : 0;
-        return attn_tiles(lo, hi);
+        return attn_tiles(first_seen(p, pos0 + first), hi);
     }
     __device__ __forceinline__ void next() {
         row0 += ROWS;

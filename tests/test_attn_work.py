@@ -48,3 +48,11 @@ def test_every_tile_once_at_random(divide):
         lens = [(int(2 ** rng.uniform(0, 13)), int(2 ** rng.uniform(0, 10)) - 1) for _ in range(rng.randint(1, 40))]
         divide(lens, page=rng.choice([8, 16, 24, 48, 64, 128, 136]), window=rng.choice([0, 0, rng.randint(1, 4000)]),
                kv_heads=rng.choice([1, 2, 8]), group=rng.choice([1, 3, 4, 7, 16, 32]), ctas=rng.choice([1, 7, 61, 152]))
+
+
+@pytest.mark.parametrize("lens", MIXED, ids=lambda v: "-".join("%d,%d" % p for p in v[:4]))
+@pytest.mark.parametrize("window", [1 << 28, 1 << 30, (1 << 31) - 3, (1 << 31) - 2, (1 << 31) - 1])
+def test_windows_wider_than_everything(divide, lens, window):
+    """Next to rows at negative positions too."""
+    for group, ctas in ((1, 152), (4, 3), (16, 152)):
+        divide(lens, window=window, group=group, ctas=ctas)

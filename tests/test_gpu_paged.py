@@ -413,3 +413,14 @@ def test_attention_to_a_nan_key(api, d, grid):
         api.set_option(api.OPT_GRID_CTAS, 0)
     assert got[hit].isnan().all() and z[hit].isnan().all()
     assert torch.equal(got[~hit], out[~hit]) and torch.equal(z[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("window", [1 << 28, 1 << 30, (1 << 31) - 2, (1 << 31) - 1])
+@pytest.mark.parametrize("lens", ["empty_rows", "decode", "chunk"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_windows_wider_than_everything(api, lens, window, d):
+    """Next to rows at negative positions too, a window of any size counts back
+    from each row's position."""
+    s = make_step(LENGTHS[lens], 16, 8, 2, d, torch.bfloat16, 41, window=window, pad=1)
+    out, lse = run_attention(api, s)
+    check_attention(out, lse, attention(s))
