@@ -323,11 +323,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 mbar_arrive(q_full + 8 * slot);
             }
             // keys that the row sees, and that all or any rows of the slot see
-            const int at_pos = walk.q.pos0 + tok;
-            const int last = real ? min(at_pos, walk.hi - 1) : -1;
-            const int from = first_seen(p, at_pos);
-            const int all_to = min(walk.q.pos0 + token_of(p, slot_row0) + 1, walk.hi);
-            const int all_from = first_seen(p, walk.q.pos0 + token_of(p, slot_row0 + slot_rows - 1));
+            const RowKeys sees = attn_row_keys(walk, slot * kSlotRows + row);
+            const AllKeys all = attn_all_keys(walk, slot * kSlotRows, slot * kSlotRows + slot_rows);
             float m = -INFINITY;  // reference of the weights, in log2
             float l = 0.f;
             for (int j = 0; j < n; ++j) {
@@ -339,10 +336,10 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld32(s_at + 32 * c, s + 32 * c);
                 tc_wait_ld();
-                if (key0 + kAttnTile > all_to || key0 < all_from) {
+                if (all.lacks(key0, kAttnTile)) {
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
-                        if (key0 + i > last || key0 + i < from) s[i] = 0xff800000u;  // -inf
+                        if (key0 + i > sees.last || key0 + i < sees.from) s[i] = 0xff800000u;  // -inf
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -389,7 +386,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 // values that no row sees may be anything: a weight of 0 times
                 // NaN is not 0, so they are cleared
-                if (slot == 0 && (key0 < walk.lo || key0 + kAttnTile > walk.hi)) {
+                if (slot == 0 && attn_ragged(walk, key0, kAttnTile)) {
                     const uint32_t i = first_stage + 2 * j + 1;
                     if (!wait(full + 8 * (i % S::kStages), (i / S::kStages) & 1u)) break;
                     if (key0 + row < walk.lo || key0 + row >= walk.hi) {

@@ -201,13 +201,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
         int last[2], from[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int row = set * 16 + b * 8 + quad;
-            const int pos = walk.q.pos0 + token_of(p, walk.row0 + row);
-            last[b] = row < walk.rows ? min(pos, walk.hi - 1) : -1;
-            from[b] = first_seen(p, pos);
+            const RowKeys k = attn_row_keys(walk, set * 16 + b * 8 + quad);
+            last[b] = k.last;
+            from[b] = k.from;
         }
-        const int all_to = min(walk.q.pos0 + token_of(p, walk.row0) + 1, walk.hi);
-        const int all_from = first_seen(p, walk.q.pos0 + token_of(p, walk.row0 + walk.rows - 1));
+        const AllKeys all = attn_all_keys(walk, 0, walk.rows);
         float o[D / 8][4];
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -218,8 +216,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             if (!wait(full + 8 * stage, parity)) break;
             const int key0 = (walk.tile0 + t) * kAttnTile + kw * kWarpKeys;
             const uint32_t ks = base + stage * S::kStage, vs = ks + S::kHalf;
-            if (active && key0 < walk.hi && key0 + kWarpKeys > walk.lo) {
-                const bool ragged = key0 < walk.lo || key0 + kWarpKeys > walk.hi;
+            if (active && attn_needs(walk, key0, kWarpKeys)) {
+                const bool ragged = attn_ragged(walk, key0, kWarpKeys);
                 if (ragged) {
                     // values that no row sees may be anything: a weight of 0 times
                     // NaN is not 0, so they are cleared (by both sets of rows,
@@ -255,7 +253,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                         mma_16816<DT>(s[2 * h + 1], qa, kb[h][2], kb[h][3]);
                     }
                 }
-                if (key0 + kWarpKeys > all_to || key0 < all_from) {
+                if (all.lacks(key0, kWarpKeys)) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -224,6 +224,34 @@ struct Walk {
     __device__ __forceinline__ int part() const { return t0 > 0 ? 0 : 1; }
 };
 
+// The keys that row `row` of the item at hand sees, [from, last] (from > last:
+// none). Rows past its end see none.
+struct RowKeys {
+    int last, from;
+};
+template <class W>
+__device__ __forceinline__ RowKeys attn_row_keys(const W& walk, int row) {
+    const int pos = walk.q.pos0 + token_of(walk.p, walk.row0 + min(row, walk.rows - 1));
+    return RowKeys{row < walk.rows ? min(pos, walk.hi - 1) : -1, first_seen(walk.p, pos)};
+}
+// Keys that all rows [from, to) of it see: [all_from, all_to).
+struct AllKeys {
+    int to, from;
+    // whether some row does not see one of the keys [key, key + n)
+    __device__ __forceinline__ bool lacks(int key, int n) const { return key > to - n || key < from; }
+};
+template <class W>
+__device__ __forceinline__ AllKeys attn_all_keys(const W& walk, int from, int to) {
+    return AllKeys{min(walk.q.pos0 + token_of(walk.p, walk.row0 + from) + 1, walk.hi),
+                   first_seen(walk.p, walk.q.pos0 + token_of(walk.p, walk.row0 + to - 1))};
+}
+// Of the keys [key, key + n) (key >= 0): whether the item needs any, and
+// whether there are some that it does not.
+template <class W>
+__device__ __forceinline__ bool attn_needs(const W& walk, int key, int n) { return key < walk.hi && key > walk.lo - n; }
+template <class W>
+__device__ __forceinline__ bool attn_ragged(const W& walk, int key, int n) { return key < walk.lo || key > walk.hi - n; }
+
 // The CTA in which an item's first tile lies, and how many CTAs hold its tiles
 // (the CTA of unit u is the largest k with kU/G <= u).
 struct Span {
@@ -268,8 +296,9 @@ struct TileFeed {
     __device__ __forceinline__ Box box() const {
         const AttnParams& p = walk.p;
         Box b;
-        const int key = (walk.tile0 + t) * kAttnTile + lane * p.box;
-        b.wanted = any && lane < kAttnTile / p.box && key < walk.hi && key + p.box > walk.lo;
+        // (a tile may end at key 2^31: no lane goes past it, and no sum reaches it)
+        const int key = (walk.tile0 + t) * kAttnTile + min(lane * p.box, kAttnTile - p.box);
+        b.wanted = any && lane < kAttnTile / p.box && key < walk.hi && key > walk.lo - p.box;
         b.head = walk.head;
         b.rows = any && t == walk.t0 ? walk.rows : 0;
         b.row0 = walk.row0;

@@ -66,6 +66,29 @@ static void check(AttnParams p, const std::vector<std::pair<int64_t, int64_t>>& 
             int& done = seen[{w.r, w.head, w.row0}];
             if (done != w.t0) fail("a tile left out or taken twice");
             done = w.t1;
+            // what the rows see of each tile, in quarters too
+            auto seen_from = [&](int64_t pos) { return p.window > 0 ? std::max<int64_t>(pos - p.window + 1, 0) : 0; };
+            for (int row = 0; row < ROWS; ++row) {
+                const int64_t pos = seq - n + (w.row0 + row) / p.group;
+                const RowKeys k = attn_row_keys(w, row);
+                if (row >= w.rows ? k.last >= 0 : k.last != std::min(pos, hi - 1) || k.from != seen_from(pos))
+                    fail("other keys than the row sees");
+            }
+            for (int from = 0; from < w.rows; from += 128) {
+                const int to = min(from + 128, w.rows);
+                const AllKeys all = attn_all_keys(w, from, to);
+                for (int t = w.t0; t < w.t1; ++t)
+                    for (int n_keys : {32, kAttnTile})
+                        for (int64_t key = (int64_t)(w.tile0 + t) * kAttnTile, end = key + kAttnTile; key < end; key += n_keys) {
+                            const int64_t first_pos = seq - n + (w.row0 + from) / p.group, last_pos = seq - n + (w.row0 + to - 1) / p.group;
+                            if (all.lacks((int)key, n_keys) !=
+                                (key + n_keys > std::min(first_pos + 1, hi) || key < seen_from(last_pos)))
+                                fail("a row's missing keys not noticed");
+                            if (attn_needs(w, (int)key, n_keys) != (key < hi && key + n_keys > lo) ||
+                                attn_ragged(w, (int)key, n_keys) != (key < lo || key + n_keys > hi))
+                                fail("an item's keys not noticed");
+                        }
+            }
             const Span s = attn_span(w, at);
             if (cta < s.cta || cta >= s.cta + s.parts) fail("a part outside its item's CTAs");
             if (w.whole() != (s.parts == 1)) fail("a count of parts that is not the item's");
@@ -127,11 +150,13 @@ int main(int argc, char** argv) {
     p.T = start.back();
     p.q_start = start.data();
     p.seq = seq.data();
-    std::vector<int32_t> tables((size_t)p.B * p.max_blocks, 0);
-    p.tables = tables.data();
+    // (zeros of which only the pages that are read take memory)
+    const size_t entries = (size_t)p.B * p.max_blocks;
+    p.tables = static_cast<int32_t*>(std::calloc(entries, sizeof(int32_t)));
+    if (!p.tables) fail("no memory");
     unsigned status[64] = {};
     p.ctrl = status;
-    readable = {{start.data(), start.size()}, {seq.data(), seq.size()}, {tables.data(), tables.size()}};
+    readable = {{start.data(), start.size()}, {seq.data(), seq.size()}, {p.tables, entries}};
     check<Few>(p, lens);
     check<Many>(p, lens);
     return 0;

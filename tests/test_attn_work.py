@@ -56,3 +56,14 @@ def test_windows_wider_than_everything(divide, lens, window):
     """Next to rows at negative positions too."""
     for group, ctas in ((1, 152), (4, 3), (16, 152)):
         divide(lens, window=window, group=group, ctas=ctas)
+
+
+@pytest.mark.parametrize("new", [1, 6, 20, 300])
+@pytest.mark.parametrize("page", [8, 136, 1024])
+@pytest.mark.parametrize("window", [1, 500, 5000])
+def test_up_to_the_last_position(divide, new, page, window):
+    """Keys up to 2^31 - 2: their numbers rounded up to whole tiles do not fit 32
+    bits."""
+    for short in (0, 1, 33, 127, 128, 1000):
+        seq = (1 << 31) - 1 - short
+        divide([(seq, new), (seq - 1, 1)], page=page, window=window, width=-(-seq // page), ctas=61)

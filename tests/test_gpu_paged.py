@@ -424,3 +424,21 @@ def test_attention_windows_wider_than_everything(api, lens, window, d):
     s = make_step(LENGTHS[lens], 16, 8, 2, d, torch.bfloat16, 41, window=window, pad=1)
     out, lse = run_attention(api, s)
     check_attention(out, lse, attention(s))
+
+
+@pytest.mark.parametrize("new", [1, 6, 20, 300])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("short", [0, 1, 33, 127, 128, 1000])
+def test_attention_up_to_the_last_position(api, new, d, short):
+    """Positions up to 2^31 - 2 under a window: the keys' numbers, rounded up to
+    whole tiles, do not fit 32 bits. The same as a short request's, moved by whole
+    pages."""
+    page, window, near = 1024, 500, 4 * 1024 - 1 - short
+    s = make_step([(near, new)], page, 8, 2, d, torch.bfloat16, 43, window=window, width=4)
+    want = attention(s)
+    moved = (1 << 31) - 4 * page
+    table = torch.full((1, 1 << 21), -1, dtype=torch.int32, device="cuda")
+    table[0, -4:] = s["table"][0]
+    s["table"], s["seq"] = table, i32([near + moved])
+    out, lse = run_attention(api, s)
+    check_attention(out, lse, want)
