@@ -129,8 +129,8 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanParams p) 
 
     const int step = gridDim.x * kPlanThreads, id = blockIdx.x * kPlanThreads + tid;
     // new blocks: the e-th goes to column have + e - first of its request
-    for (int e = id; e < given; e += step) {
-        const int b = last_at_most(first, p.B, e);
+    for (int64_t e = id; e < given; e += step) {
+        const int b = last_at_most(first, p.B, (int)e);
         const int have = (int)(((long long)max(p.ctx[b], 0) + bs - 1) / bs);
         p.tables[(int64_t)b * p.max_blocks + have + (e - first[b])] = p.free_list[head + e];
     }
@@ -139,16 +139,19 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanParams p) 
         if (t < total) {
             const int b = last_at_most(q0, p.B, (int)t);
             const int c = max(p.ctx[b], 0);
-            pos = c + (int)t - q0[b];
+            pos = c + ((int)t - q0[b]);  // (the sum of c and t may pass 32 bits)
             const int page = pos / bs, have = (int)(((long long)c + bs - 1) / bs);
             int block = -1;
             if (page < p.max_blocks) {
                 if (page < have) {
                     block = p.tables[(int64_t)b * p.max_blocks + page];
                     if (block < 0) bad = true;
-                } else if (first[b] + (page - have) < given) {
-                    block = p.free_list[head + first[b] + (page - have)];
-                    if (block < 0) bad = true;
+                } else {
+                    const int64_t e = (int64_t)first[b] + (page - have);
+                    if (e < given) {
+                        block = p.free_list[head + e];
+                        if (block < 0) bad = true;
+                    }
                 }
             }
             const long long s = (long long)block * bs + pos % bs;

@@ -115,6 +115,27 @@ def test_plan_bad_lengths(api):
     assert status == api.EDEVICE_BAD_INDEX and got["slots"].tolist() == [-1, -1]
 
 
+def test_plan_up_to_the_last_position(api):
+    """A request near 2^31 tokens beside others: its position plus a token's
+    place in the batch does not fit 32 bits."""
+    page, width = 1024, 1 << 21
+    ctx, new = [70, (1 << 31) - 1 - 1500, (1 << 31) - 1 - 900, 5], [1200, 1500, 700, 33]
+    table = np.full((4, width), -1)
+    table[0, 0], table[3, 0] = 3, 4
+    for b in (1, 2):
+        table[b, (ctx[b] - 1) // page] = 5 + b
+    free, T = list(range(20, 40)), sum(new) + 4
+    want = plan_reference(ctx, new, free, table, page, T)
+    out = dict(q_start=i32([7] * 5), seq=i32([7] * 4), slots=i32([7] * T), taken=i32([7]), positions=i32([7] * T),
+               table=torch.from_numpy(table.astype(np.int32)).cuda())
+    ws = api.paged_workspace()
+    api.paged_plan(i32(ctx), i32(new), i32(free), out["table"], page, out["q_start"], out["seq"], out["slots"], out["taken"], ws,
+                   positions=out["positions"])
+    assert api.read_status(ws) == 0
+    assert (out["table"].cpu().numpy() == want[0]).all() and out["taken"].tolist() == [want[4]]
+    assert out["slots"].tolist() == want[2].tolist() and out["positions"].tolist() == want[3].tolist()
+
+
 # ------------------------------------------------------------------ append
 @pytest.mark.parametrize("T,heads,d,page,dtype,layout", [(1, 1, 64, 8, torch.bfloat16, "bthd"), (37, 5, 128, 16, torch.float16, "bhtd"),
                                                          (515, 8, 128, 48, torch.bfloat16, "pair"), (2000, 2, 64, 24, torch.float16, "bthd")])
