@@ -272,38 +272,58 @@ def _raw(t: Optional[torch.Tensor]) -> Optional[int]:
 
 # The current stream's handle without a Stream object around it: 0.3 us a
 # call where torch.cuda.current_stream() takes 2.9 (measured on the host of a
-# GB300), of a call whose launch takes 4.
+# GB300), of a call whose launch takes 4. Alike the current device: where a
+# tensor is on one, torch.cuda is initialised.
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _raw_stream(stream) -> int:
+def _raw_stream(stream, dev: int) -> int:
     if stream is not None:
+        if stream.device_index != dev:
+            raise MoeError(EINVAL, f"a stream of device {stream.device_index}, the current device is {dev}")
         return stream.cuda_stream
     if _current_raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _current_raw_stream(torch.cuda.current_device())
+    return _current_raw_stream(dev)
 
 
-def _vectors(what: str, dtype: torch.dtype, *pairs):
+def _device(what: str, t: torch.Tensor) -> int:
+    """The current device, where a call launches: every tensor of the call has
+    to be there (get_device() is -1 for host memory)."""
+    if not t.is_cuda:
+        raise MoeError(EINVAL, f"{what}: tensors on the device, got {t.device}")
+    return _current_device()
+
+
+def _workspace(what: str, dev: int, ws: torch.Tensor):
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise MoeError(EINVAL, f"{what}: ws uint8, contiguous, on the current device (paged_workspace); got {ws.dtype} on {ws.device}")
+
+
+def _vectors(what: str, dev: int, dtype: torch.dtype, *pairs):
     """Each pair (tensor or None, elements or None for any number): contiguous
-    device tensors of one dtype."""
+    tensors of one dtype on the current device."""
     for t, n in pairs:
-        if t is not None and (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()
                               or (n is not None and t.numel() != n)):
-            raise MoeError(EINVAL, f"{what}: {dtype}, contiguous, on the device, {n if n is not None else 'any number of'}"
-                                   f" elements; got {t.dtype} {tuple(t.shape)} on {t.device}")
+            raise MoeError(EINVAL, f"{what}: {dtype}, contiguous, on the current device, "
+                                   f"{n if n is not None else 'any number of'} elements; got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 class KvCache:
     """A paged KV cache: K and V [n_blocks, block_size, kv_heads, head_dim]
     bf16 or fp16 views (any strides that are multiples of 8 elements, the last
     dimension contiguous: `.transpose(1, 2)` of a [block, head, token, d]
-    buffer is one). Keeps the tensors alive; build it once, next to them."""
+    buffer is one), on the device of the calls that use it. Keeps the tensors
+    alive; build it once, next to them."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         _want(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in DTYPES
               and k.stride(3) == 1 and v.stride(3) == 1, "KvCache: K and V [blocks, tokens, heads, d], one dtype", ESHAPE)
+        _want(k.get_device() == v.get_device(), "KvCache: K and V on one device")
         self.k, self.v = k, v
+        self.device_index = k.get_device()
         n_blocks, self.block_size, self.kv_heads, self.head_dim = k.shape
         # a dimension of one element has no stride of its own
         sk, sv = ([t.stride(i) if t.shape[i] > 1 else max(t.stride(i), (self.head_dim + 7) // 8 * 8) for i in range(3)]
@@ -333,12 +353,14 @@ def paged_plan(ctx_lens, new_lens, free_list, block_tables, block_size: int, q_s
     positions [T], taken [1]; free_head [1] is where the free list begins."""
     B, T = ctx_lens.numel(), slot_map.numel()
     _want(block_tables.dim() == 2 and block_tables.shape[0] == B, "paged_plan: block_tables int32 [B, W]")
-    _vectors("paged_plan", torch.int32, (ctx_lens, B), (new_lens, B), (free_list, None), (free_head, 1),
+    dev = _device("paged_plan", ctx_lens)
+    _vectors("paged_plan", dev, torch.int32, (ctx_lens, B), (new_lens, B), (free_list, None), (free_head, 1),
              (block_tables, None), (q_start, B + 1), (seq_lens, B), (slot_map, T), (positions, T), (taken, 1))
+    _workspace("paged_plan", dev, ws)
     rc = lib.moe_paged_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, free_list.data_ptr(), free_list.numel(),
                             _raw(free_head), block_tables.data_ptr(), block_tables.shape[1], block_size,
                             q_start.data_ptr(), seq_lens.data_ptr(), slot_map.data_ptr(), _raw(positions), T,
-                            taken.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+                            taken.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc:
         raise MoeError(rc, "moe_paged_plan")
 
@@ -350,13 +372,16 @@ def paged_append(k_new, v_new, slot_map, cache: KvCache, ws, stream=None):
     T = k_new.shape[0]
     _want(k_new.shape == (T, cache.kv_heads, cache.head_dim) and v_new.shape == k_new.shape,
           "paged_append: k_new, v_new [T, kv_heads, head_dim]", ESHAPE)
+    dev = _device("paged_append", k_new)
     _want(k_new.dtype == cache.dtype and v_new.dtype == cache.dtype and k_new.stride(2) == 1 and v_new.stride(2) == 1
-          and k_new.is_cuda and v_new.is_cuda, "paged_append: k_new, v_new of the cache's dtype on the device")
-    _vectors("paged_append: slot_map", torch.int32, (slot_map, T))
+          and k_new.get_device() == v_new.get_device() == cache.device_index == dev,
+          "paged_append: k_new, v_new of the cache's dtype, all on the current device")
+    _vectors("paged_append: slot_map", dev, torch.int32, (slot_map, T))
+    _workspace("paged_append", dev, ws)
     kt, kh, _ = k_new.stride()
     vt, vh, _ = v_new.stride()
     rc = lib.moe_paged_append(k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T, slot_map.data_ptr(), cache._ref,
-                              ws.data_ptr(), ws.numel(), _raw_stream(stream))
+                              ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc:
         raise MoeError(rc, "moe_paged_append")
 
@@ -371,16 +396,19 @@ def paged_attention(q, cache: KvCache, block_tables, q_start, seq_lens, out, ws,
     T, heads, d = q.shape
     B = seq_lens.numel()
     _want(d == cache.head_dim and out.shape == q.shape, "paged_attention: q, out [T, q_heads, head_dim]", ESHAPE)
-    _want(q.dtype == cache.dtype and out.dtype == cache.dtype and q.is_cuda and out.is_cuda
-          and q.stride(2) == 1 and out.is_contiguous(), "paged_attention: q, out of the cache's dtype on the device")
+    dev = _device("paged_attention", q)
+    _want(q.dtype == cache.dtype and out.dtype == cache.dtype and q.stride(2) == 1 and out.is_contiguous()
+          and q.get_device() == out.get_device() == cache.device_index == dev,
+          "paged_attention: q, out of the cache's dtype, all on the current device")
     _want(block_tables.dim() == 2 and block_tables.shape[0] == B, "paged_attention: block_tables int32 [B, W]")
-    _vectors("paged_attention: block_tables, q_start, seq_lens", torch.int32, (block_tables, None), (q_start, B + 1),
+    _vectors("paged_attention: block_tables, q_start, seq_lens", dev, torch.int32, (block_tables, None), (q_start, B + 1),
              (seq_lens, B))
-    _vectors("paged_attention: lse", torch.float32, (lse, T * heads))
+    _vectors("paged_attention: lse", dev, torch.float32, (lse, T * heads))
+    _workspace("paged_attention", dev, ws)
     qt, qh, _ = q.stride()
     rc = lib.moe_paged_attention(q.data_ptr(), qt, qh, T, heads, cache._ref, block_tables.data_ptr(),
                                  block_tables.shape[1], q_start.data_ptr(), seq_lens.data_ptr(), B, scale, window,
-                                 out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+                                 out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc:
         raise MoeError(rc, "moe_paged_attention")
 
@@ -394,13 +422,14 @@ def sample(logits, u, tokens, probs=None, temperature=None, top_k=None, top_p=No
     [M] or None; per-row settings temperature, top_p, min_p fp32 [M], top_k
     int32 [M], None for off."""
     M, V = logits.shape
-    _want(logits.dtype in _LOGITS and logits.is_cuda and (V == 1 or logits.stride(1) == 1),
-          "sample: logits fp32 or bf16 [M, V], rows contiguous, on the device")
-    _vectors("sample: u, probs, temperature, top_p, min_p", torch.float32, (u, M), (probs, M), (temperature, M), (top_p, M),
-             (min_p, M))
-    _vectors("sample: tokens, top_k", torch.int32, (tokens, M), (top_k, M))
+    dev = _device("sample", logits)
+    _want(logits.dtype in _LOGITS and logits.get_device() == dev and (V == 1 or logits.stride(1) == 1),
+          "sample: logits fp32 or bf16 [M, V], rows contiguous, on the current device")
+    _vectors("sample: u, probs, temperature, top_p, min_p", dev, torch.float32, (u, M), (probs, M), (temperature, M),
+             (top_p, M), (min_p, M))
+    _vectors("sample: tokens, top_k", dev, torch.int32, (tokens, M), (top_k, M))
     rc = lib.moe_sample(logits.data_ptr(), _LOGITS[logits.dtype], M, V, logits.stride(0) if M > 1 else V, u.data_ptr(),
                         _raw(temperature), _raw(top_k), _raw(top_p), _raw(min_p), tokens.data_ptr(), _raw(probs),
-                        _raw_stream(stream))
+                        _raw_stream(stream, dev))
     if rc:
         raise MoeError(rc, "moe_sample")

@@ -108,3 +108,90 @@ def test_binding_refuses_wrong_tensors(api):
     n = torch.zeros(2, dtype=torch.int64)
     with pytest.raises(api.MoeError):
         api.paged_plan(n, n, n, n.view(1, 2), 16, n, n, n, n, n)
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that passes for one on a GPU, where no call is made."""
+    index = 0
+    is_cuda = property(lambda self: self.index >= 0)
+
+    def get_device(self):
+        return self.index
+
+
+class OnOtherGpu(OnGpu):
+    index = 1
+
+
+class OnHost(OnGpu):
+    index = -1
+
+
+class Calls:
+    """Stands for the library: counts the calls that the binding lets through."""
+
+    def __init__(self, lib):
+        self.made, self.moe_status_str = [], lib.moe_status_str
+
+    def __getattr__(self, name):
+        return lambda *args: self.made.append(name) or 0
+
+
+def binding_call(api, name):
+    """(function, its tensors by argument) of an accepted call."""
+    def t(dtype, *shape):
+        return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+
+    i, f, b = torch.int32, torch.float32, torch.bfloat16
+    kv = dict(k=t(b, 8, 16, 2, 64), v=t(b, 8, 16, 2, 64))
+    ws = t(torch.uint8, 1024)
+    if name == "paged_plan":
+        a = dict(ctx_lens=t(i, 2), new_lens=t(i, 2), free_list=t(i, 9), block_tables=t(i, 2, 4), q_start=t(i, 3), seq_lens=t(i, 2),
+                 slot_map=t(i, 7), taken=t(i, 1), ws=ws, positions=t(i, 7), free_head=t(i, 1))
+        return (lambda **a: api.paged_plan(block_size=16, **a)), a
+    if name == "paged_append":
+        a = dict(k_new=t(b, 3, 2, 64), v_new=t(b, 3, 2, 64), slot_map=t(i, 3), ws=ws, **kv)
+        return (lambda k, v, **a: api.paged_append(cache=api.KvCache(k, v), **a)), a
+    if name == "paged_attention":
+        a = dict(q=t(b, 3, 4, 64), block_tables=t(i, 2, 4), q_start=t(i, 3), seq_lens=t(i, 2), out=t(b, 3, 4, 64), ws=ws,
+                 lse=t(f, 3, 4), **kv)
+        return (lambda k, v, **a: api.paged_attention(cache=api.KvCache(k, v), **a)), a
+    a = dict(logits=t(f, 2, 10), u=t(f, 2), tokens=t(i, 2), probs=t(f, 2), temperature=t(f, 2), top_k=t(i, 2), top_p=t(f, 2),
+             min_p=t(f, 2))
+    return api.sample, a
+
+
+@pytest.mark.parametrize("name", ["paged_plan", "paged_append", "paged_attention", "sample"])
+def test_binding_refuses_tensors_elsewhere(api, monkeypatch, name):
+    """Each tensor of a call in turn in host memory and on another device than
+    the current one: no address of it reaches the library."""
+    calls = Calls(api.lib)
+    monkeypatch.setattr(api, "lib", calls)
+    monkeypatch.setattr(api, "_current_raw_stream", lambda device: 0)
+    monkeypatch.setattr(api, "_current_device", lambda: 0)
+    call, tensors = binding_call(api, name)
+    call(**tensors)
+    assert calls.made == ["moe_" + name]
+    for arg, t in tensors.items():
+        for elsewhere in (OnHost, OnOtherGpu):
+            with pytest.raises(api.MoeError):
+                call(**{**tensors, arg: t.as_subclass(torch.Tensor).as_subclass(elsewhere)})
+        if arg == "ws":
+            for wrong in (torch.zeros(1024, dtype=torch.int32), torch.zeros(4096, dtype=torch.uint8)[::4]):
+                with pytest.raises(api.MoeError):
+                    call(**{**tensors, arg: wrong.as_subclass(OnGpu)})
+
+    if "k" in tensors:  # both of the cache's tensors
+        for elsewhere in (OnHost, OnOtherGpu):
+            with pytest.raises(api.MoeError):
+                call(**{**tensors, **{n: tensors[n].as_subclass(torch.Tensor).as_subclass(elsewhere) for n in "kv"}})
+
+    class Stream:
+        device_index, cuda_stream = 1, 5
+
+    with pytest.raises(api.MoeError):
+        call(**tensors, stream=Stream)
+    Stream.device_index = 0
+    assert len(calls.made) == 1
+    call(**tensors, stream=Stream)
+    assert len(calls.made) == 2
