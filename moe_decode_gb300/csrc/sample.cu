@@ -135,18 +135,22 @@ struct Scale {
 // roundings is. From kNoPart on (t = 41, -inf) it has no part in the mass.
 constexpr uint32_t kStepBits = 23, kNoPart = 41u << 17;
 __device__ __forceinline__ uint32_t steps_of(float x, const Scale& s) {
-    return __float_as_uint(fmaf(s.top - x, s.hi, 64.f)) - 0x42800000u;
+    return __float_as_uint(__fmaf_rn(__fsub_rn(s.top, x), s.hi, 64.f)) - 0x42800000u;
 }
-// Its mass w in units of 2^-42, given that it has a part.
+// Its mass w in units of 2^-42, given that it has a part. Each operation rounds
+// as it is written: were the product th fused into the sums that use it, its
+// error would count twice there, and a mass would not have the bits that the
+// paired form below gives it. (A row's total comes from the one and the search
+// in a thread's logits from the other: they have to end at the same number.)
 __device__ __forceinline__ u64 mass_of(float x, const Scale& s) {
-    const float d = s.top - x;
+    const float d = __fsub_rn(s.top, x);
     // the rounding error of the difference, then of the product
-    const float bb = d - s.top, err = (s.top - (d - bb)) - (x + bb);
-    const float th = d * s.hi;
-    const float tl = fmaf(d, s.hi, -th) + fmaf(d, s.lo, err * s.hi);
-    const float whole = th + 12582912.f;  // 1.5 * 2^23: rounds to a whole number n <= 41, in the low bits
+    const float bb = __fsub_rn(d, s.top), err = __fsub_rn(__fsub_rn(s.top, __fsub_rn(d, bb)), __fadd_rn(x, bb));
+    const float th = __fmul_rn(d, s.hi);
+    const float tl = __fadd_rn(__fmaf_rn(d, s.hi, -th), __fmaf_rn(d, s.lo, __fmul_rn(err, s.hi)));
+    const float whole = __fadd_rn(th, 12582912.f);  // 1.5 * 2^23: rounds to a whole number n <= 41, in the low bits
     const uint32_t n = __float_as_uint(whole) & 0x3fu;
-    const float f = (th - (whole - 12582912.f)) + tl;
+    const float f = __fadd_rn(__fsub_rn(th, __fsub_rn(whole, 12582912.f)), tl);
     float e;
     asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-f));
     // e = mant * 2^(exponent - 150), the exponent 126 or 127

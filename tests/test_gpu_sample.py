@@ -207,3 +207,38 @@ def test_the_same_on_every_call(api, settings):
             differ += ((tokens != first) | (probs != p0)).sum()
         torch.cuda.synchronize()
         assert differ.item() == 0
+
+
+def test_equal_logits_have_equal_shares(api):
+    """Hundreds of thousands of equal logits under one larger: the share of each
+    is 1 / (n + 1 / w). The numerator is one mass and the denominator the sum of
+    many, which must be the same number: what is left are three roundings to
+    fp32, and the mass's own error in what the larger one adds."""
+    n, M = 700000, 32
+    t = torch.linspace(4.0, 16.0, M, dtype=torch.float64)
+    T = torch.linspace(0.3, 3.1, M).roll(7)
+    x = torch.empty((M, n + 1), device="cuda")
+    low = (-t * math.log(2) * T.double()).float()
+    x[:] = low.cuda()[:, None]
+    x[:, 0] = 0.0
+    tokens, probs, _ = run(api, x, 0.9, temperature=T)
+    w = torch.exp(low.double() / T.double()).numpy()
+    want = 1 / (n + 1 / w)
+    assert (tokens > 0).all()
+    err = np.abs(probs / want - 1)
+    assert (err <= 3 * 2.0 ** -24 + 2.0 ** -21 / w * want).all(), err.max() * 2.0 ** 24
+
+
+def test_a_token_at_every_u_below_one(api):
+    """The mass of a row lies in its last few logits and u is the largest fp32
+    below 1: every row gets one of them."""
+    M, V, hot = 2000, 19976, 44
+    t = 4 + 4 * torch.rand(M, generator=torch.Generator().manual_seed(1))
+    T = 0.2 + 2 * torch.rand(M, generator=torch.Generator().manual_seed(2))
+    x = torch.full((M, V), -math.inf, device="cuda")
+    x[:, V - hot:] = (-t * math.log(2) * T).cuda()[:, None]
+    x[:, 0] = 0.0
+    u = float(np.nextafter(np.float32(1), np.float32(0)))
+    for settings in (dict(), dict(top_k=hot + 1), dict(top_p=0.999), dict(min_p=1e-4)):
+        tokens, probs, _ = run(api, x, u, temperature=T, **settings)
+        assert (tokens >= V - hot).all() and (tokens < V).all() and (probs > 0).all(), (settings, tokens.min())
