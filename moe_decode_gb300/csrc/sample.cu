@@ -53,13 +53,20 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 // (.aligned asks for whole warps: what comes before is often one lane's)
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
 }
-// The two halves: shared memory of a CTA that has not begun may not be written.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// (the two halves by themselves at the start: shared memory of a CTA that has
+// not begun may not be written)
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // The address of this CTA's shared variable in CTA r of the cluster.
 __device__ __forceinline__ uint32_t remote(const void* p, uint32_t r) {
     uint32_t a;
