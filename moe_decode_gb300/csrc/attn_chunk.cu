@@ -399,6 +399,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                     }
                     fence_proxy_async_shared();
                 }
+                __syncwarp();  // (some rows' threads cleared values)
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_full + 8 * slot);
@@ -435,7 +436,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 }
             }
             if (whole) {
-                named_bar_sync(1 + slot, kSlotRows);
+                warps_sync(1 + slot, kSlotRows);
                 constexpr int kPer = D / 8;
                 // (each thread reads the pieces that it writes with the next
                 // item's queries, so no barrier follows)
@@ -451,17 +452,17 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                 if (real && p.lse) p.lse[at_row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             } else {
                 reinterpret_cast<float2*>(part + kAttnChunkRows * D)[slot * kSlotRows + row] = make_float2(m, l);
-                named_bar_sync(1 + slot, kSlotRows);
+                warps_sync(1 + slot, kSlotRows);
                 if (t == 0) {
                     const Span span = attn_span(walk, at);
                     join_info[slot][0] = span.cta;
                     join_info[slot][1] = span.parts;
                     join_info[slot][2] = attn_last(p.arrived + (1 + slot) * kAttnMaxGrid + span.cta, span.parts);
                 }
-                named_bar_sync(1 + slot, kSlotRows);
+                warps_sync(1 + slot, kSlotRows);
                 if (join_info[slot][2])
                     attn_join_slot<D, DT>(p, p.chunk_part, Span{join_info[slot][0], join_info[slot][1]}, slot, row, at_row, real);
-                named_bar_sync(1 + slot, kSlotRows);
+                warps_sync(1 + slot, kSlotRows);
             }
             // O is read: the next item's first product may write it
             tc_fence_before();

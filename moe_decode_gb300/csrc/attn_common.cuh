@@ -49,6 +49,13 @@ __device__ __forceinline__ Place attn_place(const AttnParams& p, int cta, int64_
     return at;
 }
 
+// A barrier of some of the CTA's warps. (bar.sync is .aligned: it asks for whole
+// warps, and what comes before is often some lanes'.)
+__device__ __forceinline__ void warps_sync(uint32_t id, uint32_t threads) {
+    __syncwarp();
+    named_bar_sync(id, threads);
+}
+
 // One thread of a CTA whose part is in place (its threads' stores are behind a
 // barrier): whether all the others are. The last one to come leaves the count
 // at zero for the next call.

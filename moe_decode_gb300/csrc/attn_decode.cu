@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             l[b] += __shfl_xor_sync(0xffffffffu, l[b], 2);
             if (pair == 0) stat[kw * kRows + set * 16 + b * 8 + quad] = make_float2(m[b], l[b]);
         }
-        named_bar_sync(1, kConsumers * 32);
+        warps_sync(1, kConsumers * 32);
         float big[2], sum[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             if (w == kKeyWarps - 1 && kw == 0 && pair == 0)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) stat[set * 16 + b * 8 + quad] = make_float2(big[b], sum[b]);
-            named_bar_sync(1, kConsumers * 32);
+            warps_sync(1, kConsumers * 32);
         }
         // 16 bytes of output a thread
         const bool whole = walk.whole();
@@ -401,7 +401,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             }
         }
         // the next item writes the rows and the statistics after this barrier
-        named_bar_sync(1, kConsumers * 32);
+        warps_sync(1, kConsumers * 32);
         if (!whole) {
             if (tid == 0) {
                 const Span span = attn_span(walk, at);
@@ -409,11 +409,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 join_info[1] = span.parts;
                 join_info[2] = attn_last(p.arrived + span.cta, span.parts);
             }
-            named_bar_sync(1, kConsumers * 32);
+            warps_sync(1, kConsumers * 32);
             if (join_info[2])
                 attn_join<D, DT, kRows, kConsumers * 32, 2>(p, p.part, Span{join_info[0], join_info[1]}, 0, walk.rows,
                                                          walk.row0, walk.head, walk.q.q0, tid);
-            named_bar_sync(1, kConsumers * 32);
+            warps_sync(1, kConsumers * 32);
         }
     }
 }
