@@ -27,6 +27,7 @@ F_DEBUG_FORCE_TIMEOUT = 256
 OPT_GRID_CTAS = 1
 OPT_WAIT_TIMEOUT_NS = 2
 OPT_TRACE_BUFFER = 3
+OPT_DEBUG_HOLD_BACK = 4
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 LM_HEAD_WORKSPACE_BYTES = 1024
 STATIC_SCRATCH_BYTES = 524288

@@ -527,6 +527,10 @@ int moe_set_option(int option, int64_t value) {
             if (value < 0 || (value & 7)) return MOE_EINVAL;
             g_opt.trace = reinterpret_cast<unsigned long long*>(value);
             return MOE_OK;
+        case MOE_OPT_DEBUG_HOLD_BACK:
+            if (value < 0 || value > 1) return MOE_EINVAL;
+            g_opt.hold_back = value != 0;
+            return MOE_OK;
         default: return MOE_EINVAL;
     }
 }

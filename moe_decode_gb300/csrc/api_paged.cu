@@ -245,6 +245,7 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
     p.window = window;
     p.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)cache->head_dim)) * 1.44269504088896341f;
     p.timeout_ns = (unsigned long long)g_opt.timeout_ns;
+    p.hold_back = g_opt.hold_back ? 1 : 0;
     CUtensorMap maps[4];
     for (int i = 0; i < (moe::attn_may_chunk(p) ? 4 : 2); ++i) {
         const int panels = i < 2 ? cache->head_dim / 64 : 1;

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     uint8_t* sm = dyn + (base - smem_u32(dyn));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // barriers: key/value stages full and empty; per slot queries in place, S
-    // written, P written, O complete; the last work of an aborted CTA
+    // written, P written, O complete; the last products of the CTA
     const uint32_t full = base + S::kOffBar, empty = full + 8 * S::kStages;
     const uint32_t q_full = empty + 8 * S::kStages, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16,
                    drained = o_full + 16;
@@ -177,15 +177,16 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             for (bool more = feed.any; ok && more; cur = next) {
                 more = feed.advance();
                 if (more) next = feed.box();
-                const bool take = attn_take(p, cur.wanted, cur.block);
-                const int n = __popc(__ballot_sync(0xffffffffu, take));
+                const bool want = attn_take(p, cur.wanted, cur.block);
+                const int n = __popc(__ballot_sync(0xffffffffu, want));
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     ok = __all_sync(0xffffffffu, ok && attn_wait(empty + 8 * stage, parity, p, flag));
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 2));
+                    const bool held = p.hold_back && issued == 0;
+                    if (lane == 0 && !held) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 2));
                     __syncwarp();
-                    if (take) {
+                    if (want && !held) {
                         const uint32_t dst = base + S::kOffKv + stage * S::kTile + lane * p.box * 128;
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
@@ -199,15 +200,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                     }
                 }
             }
-            if (!ok && lane == 0) {
-                // copies may be in flight: see the last ones land (again bounded)
-                for (int i = max(0, issued - S::kStages); i < issued; ++i) {
-                    const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(full + 8 * (i % S::kStages), (uint32_t)((i / S::kStages) & 1)) &&
-                           global_timer_ns() - t0 < p.timeout_ns) {
-                    }
-                }
-            }
+            // the last copies of each stage, in flight where another role gave up
+            if (lane == 0)
+                for (int i = max(p.hold_back, issued - S::kStages); i < issued; ++i)
+                    attn_drain(full + 8 * (i % S::kStages), (uint32_t)((i / S::kStages) & 1));
+            __syncwarp();
         } else if (warp == kMmaWarp) {
             if (lane == 0) {
                 Walk<Many> walk(p, at);
@@ -259,13 +256,10 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
                         pos += more ? 2 : 1;
                     }
                 }
-                if (!ok) {
-                    // products may be in flight: tensor memory is freed after them
-                    tc_commit(drained);
-                    const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(drained, 0) && global_timer_ns() - t0 < p.timeout_ns) {
-                    }
-                }
+                // the last products, in flight where another role gave up: tensor
+                // memory is freed after them
+                tc_commit(drained);
+                attn_drain(drained, 0);
             }
             __syncwarp();
         }

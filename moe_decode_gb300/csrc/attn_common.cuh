@@ -211,6 +211,19 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const A
     return true;
 }
 
+// Waits for the phase with parity `parity` of work that the CTA itself has
+// issued: copies into its shared memory, products in its tensor memory. Both
+// belong to the next CTA once this one has ended, so whoever issued something
+// sees it done before it leaves, whether a wait of the CTA has run out or not,
+// and with a limit of its own: the option's may be short.
+constexpr uint64_t kDrainNs = 2000000000;
+__device__ __forceinline__ void attn_drain(uint32_t bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kDrainNs) {
+    }
+}
+
 // One box of a cache's tensor map (64 dimensions, token of the block, which 64,
 // head, block) into shared memory: `box` keys, 128 bytes a key in the 128-byte
 // swizzle, one panel of 64 dimensions after another. The innermost coordinate

@@ -112,7 +112,6 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
         // producer: lane i brings the tile's i-th box, if a row sees any of it
         int stage = 0, issued = 0;
         uint32_t parity = 1, items = 0;
-        bool ok = true;
         TileFeed<Few> feed(p, at, lane);
         auto cur = feed.box(), next = cur;
         for (bool more = feed.any; more; cur = next) {
@@ -121,8 +120,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             if (cur.rows > 0) {
                 // the item's queries, a row a lane
                 const uint32_t i = items & 1u;
-                ok = __all_sync(0xffffffffu, attn_wait(q_empty + 8 * i, ((items >> 1) & 1u) ^ 1u, p, flag));
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, attn_wait(q_empty + 8 * i, ((items >> 1) & 1u) ^ 1u, p, flag))) break;
                 if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * i, (uint32_t)(cur.rows * D * 2));
                 __syncwarp();
                 if (lane < cur.rows) {
@@ -132,11 +130,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 }
                 ++items;
             }
-            ok = __all_sync(0xffffffffu, attn_wait(empty + 8 * stage, parity, p, flag));
-            if (!ok) break;
-            const bool take = attn_take(p, cur.wanted, cur.block);
+            if (!__all_sync(0xffffffffu, attn_wait(empty + 8 * stage, parity, p, flag))) break;
+            const bool held = p.hold_back && issued == 0;
+            const bool take = attn_take(p, cur.wanted, cur.block) && !held;
             const int n = __popc(__ballot_sync(0xffffffffu, take));
-            if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 4));
+            if (lane == 0 && !held) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 4));
             __syncwarp();
             if (take) {
                 const uint32_t dst = base + stage * S::kStage + lane * p.box * D * 2;
@@ -149,19 +147,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                 parity ^= 1u;
             }
         }
-        if (!ok && lane == 0) {
-            // copies may be in flight: see the last ones land (again bounded)
-            for (int i = max(0, issued - S::kStages); i < issued; ++i) {
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(full + 8 * (i % S::kStages), (uint32_t)((i / S::kStages) & 1)) &&
-                       global_timer_ns() - t0 < p.timeout_ns) {
-                }
-            }
-            for (uint32_t i = items > 2 ? items - 2 : 0; i < items; ++i) {
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(q_full + 8 * (i & 1u), (i >> 1) & 1u) && global_timer_ns() - t0 < p.timeout_ns) {
-                }
-            }
+        // the last copies of each stage, in flight where a consumer gave up
+        if (lane == 0) {
+            for (int i = max(p.hold_back, issued - S::kStages); i < issued; ++i)
+                attn_drain(full + 8 * (i % S::kStages), (uint32_t)((i / S::kStages) & 1));
+            for (uint32_t i = items > 2 ? items - 2 : 0; i < items; ++i) attn_drain(q_full + 8 * (i & 1u), (i >> 1) & 1u);
         }
         return;
     }

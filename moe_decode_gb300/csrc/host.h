@@ -9,6 +9,7 @@ struct Options {
     int grid_ctas = 0;
     long long timeout_ns = 1000000000LL;
     unsigned long long* trace = nullptr;
+    bool hold_back = false;
 };
 extern Options g_opt;
 extern thread_local int g_last_launches;

@@ -195,3 +195,8 @@ def test_binding_refuses_tensors_elsewhere(api, monkeypatch, name):
     assert len(calls.made) == 1
     call(**tensors, stream=Stream)
     assert len(calls.made) == 2
+
+
+def test_hold_back_is_off_or_on(api):
+    for value, code in ((-1, api.EINVAL), (2, api.EINVAL), (0, api.OK)):
+        assert api.lib.moe_set_option(api.OPT_DEBUG_HOLD_BACK, value) == code

@@ -463,3 +463,37 @@ def test_attention_up_to_the_last_position(api, new, d, short):
     s["table"], s["seq"] = table, i32([near + moved])
     out, lse = run_attention(api, s)
     check_attention(out, lse, want)
+
+
+@pytest.mark.parametrize("lens", list(LENGTHS))
+@pytest.mark.parametrize("heads,kv_heads,d", [(8, 2, 128), (32, 1, 64)])
+def test_attention_waits_that_run_out(api, lens, heads, kv_heads, d):
+    """Keys that never come: the call ends, reports it, and leaves nothing behind
+    that still writes where the next call works. The next ones follow at once on
+    the same SMs, on a workspace of their own; the call's own serves again once it
+    is initialised."""
+    s = make_step(LENGTHS[lens], 16, heads, kv_heads, d, torch.bfloat16, 47)
+    cache = api.KvCache(s["k"], s["v"])
+    ws, other = api.paged_workspace(heads, cache), api.paged_workspace(heads, cache)
+    outs = [torch.full_like(s["q"], math.nan) for _ in range(5)]
+
+    def call(out, ws):
+        api.paged_attention(s["q"], cache, s["table"], s["q_start"], s["seq"], out, ws)
+
+    torch.cuda.synchronize()
+    api.set_option(api.OPT_WAIT_TIMEOUT_NS, 2_000_000)
+    api.set_option(api.OPT_DEBUG_HOLD_BACK, 1)
+    try:
+        call(outs[0], ws)
+    finally:
+        api.set_option(api.OPT_DEBUG_HOLD_BACK, 0)
+        api.set_option(api.OPT_WAIT_TIMEOUT_NS, 1_000_000_000)
+    for out in outs[1:4]:
+        call(out, other)
+    assert api.read_status(ws) == api.ETIMEOUT
+    api.workspace_init(ws)
+    call(outs[4], ws)
+    assert api.read_status(ws) == 0 and api.read_status(other) == 0
+    want = attention(s)
+    for out in outs[1:]:
+        check_attention(out, None, want)
