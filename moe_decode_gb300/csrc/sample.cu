@@ -32,6 +32,7 @@
 // order.
 #include <atomic>
 
+#include "host.h"
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -895,19 +896,23 @@ cudaError_t launch_sample(SampleParams p, int M, int dtype, cudaStream_t stream)
         cfg.gridDim = dim3((unsigned)((int64_t)M * C));
         return p.slice <= kSampleMaxSlice;
     };
-    // clusters of 2^i CTAs, j + 1 CTAs an SM, that are on the GPU at once
-    // (asked once; 0: not yet)
-    static std::atomic<int> active[5][2];
+    // 1 + the clusters of 2^i CTAs, j + 1 CTAs an SM (the kernel's registers
+    // allow no more), that are on this GPU at once (asked once; 0: not yet)
+    static std::atomic<int> active[kMaxDevices][2][5][2];
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     int best = 0;
     for (int i = 4; i >= 0 && best == 0; --i) {
         if (!shape(1 << i) || (i > 0 && p.V / (1 << i) < 2048)) continue;
-        std::atomic<int>& known = active[i][cfg.dynamicSmemBytes <= kSampleSmemOfTwo ? 1 : 0];
-        int n = known.load(std::memory_order_relaxed);
-        if (n == 0) {
+        std::atomic<int>& known = active[dev][dtype == 0 ? 0 : 1][i][cfg.dynamicSmemBytes <= kSampleSmemOfTwo ? 1 : 0];
+        int n = known.load(std::memory_order_relaxed) - 1;
+        if (n < 0) {
             cfg.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
             if (e != cudaSuccess) return e;
-            known.store(n, std::memory_order_relaxed);
+            known.store(n + 1, std::memory_order_relaxed);
         }
         if (M <= n) best = 1 << i;
     }
