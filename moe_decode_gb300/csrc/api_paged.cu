@@ -265,7 +265,7 @@ int moe_sample(const void* logits, int dtype, int M, int V, int64_t row_stride, 
                int32_t* token, float* prob, void* stream) {
     g_last_launches = 0;
     if (dtype != 0 && dtype != 1) return MOE_ESHAPE;
-    if (M < 1 || M > (1 << 20) || V < 1 || V > MOE_SAMPLE_MAX_VOCAB || row_stride < V) return MOE_ESHAPE;
+    if (M < 1 || V < 1 || V > MOE_SAMPLE_MAX_VOCAB || row_stride < V) return MOE_ESHAPE;
     if (!logits || !u || !token) return MOE_EINVAL;
     if ((reinterpret_cast<uintptr_t>(logits) & (dtype == 0 ? 3u : 1u)) != 0) return MOE_EALIGN;
     for (const void* a : {(const void*)u, (const void*)temperature, (const void*)top_k, (const void*)top_p,

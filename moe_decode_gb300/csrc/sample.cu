@@ -919,6 +919,8 @@ cudaError_t launch_sample(SampleParams p, int M, int dtype, cudaStream_t stream)
     for (int C = 1; C <= 16 && best == 0; C *= 2)
         if (shape(C) && (cfg.dynamicSmemBytes <= kSampleSmemOfTwo || C == 16)) best = C;
     shape(best);
+    // (a grid's limit, which no logits in memory reach)
+    if ((int64_t)M * best > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }

@@ -242,3 +242,12 @@ def test_a_token_at_every_u_below_one(api):
     for settings in (dict(), dict(top_k=hot + 1), dict(top_p=0.999), dict(min_p=1e-4)):
         tokens, probs, _ = run(api, x, u, temperature=T, **settings)
         assert (tokens >= V - hot).all() and (tokens < V).all() and (probs > 0).all(), (settings, tokens.min())
+
+
+def test_more_rows_than_20_bits(api):
+    M = (1 << 20) + 37
+    x = torch.full((M, 8), -1.0, device="cuda")
+    want = torch.arange(M, device="cuda") % 8
+    x.scatter_(1, want[:, None], 60.0)
+    tokens, probs, _ = run(api, x, 0.5, temperature=1.0)
+    assert (tokens == want.cpu().numpy()).all() and (probs == 1.0).all()
