@@ -396,8 +396,9 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  *   token = the lowest index at which the kept tokens' cumulated mass, in
  *           index order, exceeds u * (their total mass)
  * temperature <= 0 (or NaN) takes the largest logit's lowest index;
- * temperature NULL is 1. u fp32 [M] in [0, 1) (clamped to it). A NaN logit
- * counts as -inf; +inf shares all the mass. Masses are summed in 64-bit
+ * temperature NULL is 1; a NaN top_p or min_p is off. u fp32 [M] in [0, 1)
+ * (clamped to it, NaN: 0). A NaN logit counts as -inf; +inf shares all the
+ * mass. Masses are summed in 64-bit
  * fixed point, so the result does not depend on any order; each is off by some
  * 2^-22 of itself and a unit of 2^-42, so where a mass meets min_p, or a sum
  * top_p or u, more closely than that, either side may be taken. token int32 [M]

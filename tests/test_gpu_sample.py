@@ -251,3 +251,13 @@ def test_more_rows_than_20_bits(api):
     x.scatter_(1, want[:, None], 60.0)
     tokens, probs, _ = run(api, x, 0.5, temperature=1.0)
     assert (tokens == want.cpu().numpy()).all() and (probs == 1.0).all()
+
+
+def test_settings_that_are_nan(api):
+    """A NaN top_p or min_p is off, a NaN temperature takes the largest."""
+    x, u = logits_of(9, 5000, 15)
+    plain = run(api, x, u, temperature=0.9)
+    for settings in (dict(top_p=math.nan), dict(min_p=math.nan), dict(top_p=math.nan, min_p=math.nan)):
+        got = run(api, x, u, temperature=0.9, **settings)
+        assert (got[0] == plain[0]).all() and (got[1] == plain[1]).all(), settings
+    assert (run(api, x, u, temperature=math.nan, top_p=math.nan)[0] == x.argmax(1).cpu().numpy()).all()
