@@ -261,3 +261,53 @@ def test_settings_that_are_nan(api):
         got = run(api, x, u, temperature=0.9, **settings)
         assert (got[0] == plain[0]).all() and (got[1] == plain[1]).all(), settings
     assert (run(api, x, u, temperature=math.nan, top_p=math.nan)[0] == x.argmax(1).cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("V", [31, 1000, 50257])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("settings", SETTINGS[:-1], ids=lambda d: "-".join("%s%g" % p for p in d.items()) or "plain")
+def test_settings_on_clear_rows(api, V, dtype, settings):
+    """test_settings with a count of the rows that were compared. The worst is
+    top_p among some 50,000 masses of 10^-5: a border comes within 2^-20 in one
+    row of five."""
+    x, u = logits_of(64, V, 3 * V + len(settings), dtype)
+    check(api, x, u, least=0.5, **settings)
+
+
+# (at a depth of 26 the small masses together are known to a tenth, and hold
+# some twenty fp32 u: one share of them alone can be told)
+@pytest.mark.parametrize("depth,dropped", [(d, f) for d in (12.0, 18.0, 22.0) for f in (0.2, 0.5, 0.9)] + [(26.0, 0.5)])
+def test_top_p_keeps_what_reaches_it_of_very_small_masses(api, depth, dropped):
+    """The rows of test_top_p_ends_among_very_small_masses at 256 u that fall
+    among the small masses. The sums are known to `known` (2^-22 of a mass and a
+    unit of 2^-42 each), so no token may lie further behind the border of the
+    kept run than twice that (the run's mass and its goal), nor away from where u
+    points by more than what the border's place and the sums together move."""
+    V, M = 700000, 256
+    g = torch.Generator(device="cuda").manual_seed(int(depth))
+    x = -depth - torch.rand(V, device="cuda", generator=g) * 2.0
+    x[4321] = 0.0
+    w = torch.exp(x.double()).cpu().numpy()
+    total, small = w.sum(), w.sum() - 1
+    top_p = float(np.float32(1 - dropped * small / total))
+    order = np.argsort(-x.cpu().numpy(), kind="stable")
+    before = np.cumsum(w[order]) - w[order]  # in the order of the run
+    keep = int(np.searchsorted(before, top_p * total, side="left"))
+    place = np.empty(V)
+    place[order] = before
+    kept = np.zeros(V, bool)
+    kept[order[:keep]] = True
+    cdf = np.cumsum(np.where(kept, w, 0.0))
+    known, one = small * 2.0 ** -22 + V * 2.0 ** -42, w[order[1]]
+    assert total - top_p * total > 3 * known  # there is something that must not be taken
+    # u over the small masses behind the large one
+    u = (1 - (1 - cdf[4321] / cdf[-1]) * (torch.arange(M, dtype=torch.float64) + 0.5) / M).float().clamp_max(1 - 2.0 ** -24)
+    tokens, probs, _ = run(api, x.expand(M, V).contiguous(), u, top_p=top_p)
+    assert (tokens != 4321).sum() >= 0.7 * M and len(np.unique(tokens)) >= 8
+    assert (place[tokens] <= top_p * total + 2 * known).all()
+    goal = u.double().numpy() * cdf[-1]
+    slack = 6 * known + 2 * one
+    assert (cdf[tokens] - np.where(kept[tokens], w[tokens], 0.0) <= goal + slack).all()
+    assert (cdf[tokens] >= goal - slack).all()
+    share = w[tokens] / cdf[-1]
+    assert (np.abs(probs - share) <= share * 2.0 ** -20 + share * slack + 2.0 ** -42).all()
