@@ -376,7 +376,10 @@ int moe_paged_append(const void* k_new, int64_t k_token_stride, int64_t k_head_s
  * score is NaN, in lse too; a value that is NaN or infinite may also reach the
  * request's rows that do not see it yet (as 0 * NaN). A visible key whose
  * page is not in [0, n_blocks), or beyond max_blocks, is reported
- * (MOE_EDEVICE_BAD_INDEX) and that request's outputs are unspecified.
+ * (MOE_EDEVICE_BAD_INDEX) and that request's outputs are unspecified. A
+ * request with a negative length, or whose rows q_start does not place within
+ * [0, T] in ascending order (moe_paged_plan with more new tokens than T), is
+ * reported alike and its rows are not written.
  * scale <= 0 takes 1 / sqrt(head_dim). block_tables int32 [B, max_blocks].
  * ws: moe_paged_attention_workspace_bytes(q_heads, cache). The result is
  * deterministic. */

@@ -497,3 +497,25 @@ def test_attention_waits_that_run_out(api, lens, heads, kv_heads, d):
     want = attention(s)
     for out in outs[1:]:
         check_attention(out, None, want)
+
+
+@pytest.mark.parametrize("what", ["seq", "past_T"])
+def test_attention_requests_that_do_not_fit_are_left_out(api, what):
+    """Their rows keep what was there; the others' are right."""
+    s = make_step([(200, 2), (300, 90), (77, 3)], 16, 4, 2, 64, torch.bfloat16, 53)
+    want = attention(s)
+    q_start, seq = s["q_start"].clone(), s["seq"].clone()
+    good = torch.ones(95, dtype=torch.bool, device="cuda")
+    if what == "seq":
+        seq[1] = -5
+        good[2:92] = False
+    else:
+        q_start[3] = 96
+        good[92:] = False
+    cache = api.KvCache(s["k"], s["v"])
+    ws = api.paged_workspace(4, cache)
+    out, lse = torch.full_like(s["q"], 7.0), torch.full(s["q"].shape[:2], 7.0, device="cuda")
+    api.paged_attention(s["q"], cache, s["table"], q_start, seq, out, ws, lse=lse)
+    assert api.read_status(ws) == api.EDEVICE_BAD_INDEX
+    assert (out[~good] == 7).all() and (lse[~good] == 7).all()
+    check_attention(out[good], lse[good], [t[good] for t in want])
