@@ -326,9 +326,9 @@ class KvCache:
         self.k, self.v = k, v
         self.device_index = k.get_device()
         n_blocks, self.block_size, self.kv_heads, self.head_dim = k.shape
-        # a dimension of one element has no stride of its own
-        sk, sv = ([t.stride(i) if t.shape[i] > 1 else max(t.stride(i), (self.head_dim + 7) // 8 * 8) for i in range(3)]
-                  for t in (k, v))
+        # (a dimension of one element has no stride of its own: what a view says
+        # there may be anything)
+        sk, sv = ([t.stride(i) if t.shape[i] > 1 else (self.head_dim + 7) // 8 * 8 for i in range(3)] for t in (k, v))
         self.dtype = k.dtype
         self._c = _KvCache(k.data_ptr(), v.data_ptr(), DTYPES[k.dtype], n_blocks, self.block_size, self.kv_heads,
                            self.head_dim, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2])
@@ -381,6 +381,10 @@ def paged_append(k_new, v_new, slot_map, cache: KvCache, ws, stream=None):
     _workspace("paged_append", dev, ws)
     kt, kh, _ = k_new.stride()
     vt, vh, _ = v_new.stride()
+    if T == 1:
+        kt = vt = 0
+    if cache.kv_heads == 1:
+        kh = vh = 0
     rc = lib.moe_paged_append(k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T, slot_map.data_ptr(), cache._ref,
                               ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc:
@@ -407,6 +411,10 @@ def paged_attention(q, cache: KvCache, block_tables, q_start, seq_lens, out, ws,
     _vectors("paged_attention: lse", dev, torch.float32, (lse, T * heads))
     _workspace("paged_attention", dev, ws)
     qt, qh, _ = q.stride()
+    if T == 1:
+        qt = 0
+    if heads == 1:
+        qh = 0
     rc = lib.moe_paged_attention(q.data_ptr(), qt, qh, T, heads, cache._ref, block_tables.data_ptr(),
                                  block_tables.shape[1], q_start.data_ptr(), seq_lens.data_ptr(), B, scale, window,
                                  out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))

@@ -131,10 +131,10 @@ class Calls:
     """Stands for the library: counts the calls that the binding lets through."""
 
     def __init__(self, lib):
-        self.made, self.moe_status_str = [], lib.moe_status_str
+        self.made, self.args, self.moe_status_str = [], [], lib.moe_status_str
 
     def __getattr__(self, name):
-        return lambda *args: self.made.append(name) or 0
+        return lambda *args: self.made.append(name) or self.args.append(args) or 0
 
 
 def binding_call(api, name):
@@ -200,3 +200,28 @@ def test_binding_refuses_tensors_elsewhere(api, monkeypatch, name):
 def test_hold_back_is_off_or_on(api):
     for value, code in ((-1, api.EINVAL), (2, api.EINVAL), (0, api.OK)):
         assert api.lib.moe_set_option(api.OPT_DEBUG_HOLD_BACK, value) == code
+
+
+def test_binding_takes_any_stride_of_a_dimension_of_one(api, monkeypatch):
+    """One token, one head, one block: what a view says of the step along them
+    (here not a multiple of 8) is not one that anything takes."""
+    calls = Calls(api.lib)
+    monkeypatch.setattr(api, "lib", calls)
+    monkeypatch.setattr(api, "_current_raw_stream", lambda device: 0)
+    monkeypatch.setattr(api, "_current_device", lambda: 0)
+    base = torch.zeros(8192, dtype=torch.bfloat16)
+
+    def view(shape, strides):
+        return base.as_strided(shape, strides).as_subclass(OnGpu)
+
+    for shape, strides in (((1, 16, 2, 64), (5, 128, 64, 1)), ((2, 16, 1, 64), (1024, 64, 3, 1)), ((1, 8, 1, 64), (0, 64, 7, 1))):
+        cache = api.KvCache(view(shape, strides), view(shape, strides))
+        assert all(getattr(cache._c, f"{n}_{w}_stride") % 8 == 0 and getattr(cache._c, f"{n}_{w}_stride") >= 64
+                   for n in "kv" for w in ("block", "token", "head"))
+    _, a = binding_call(api, "paged_append")
+    api.paged_append(view((1, 1, 64), (389, 7, 1)), view((1, 1, 64), (3, 9, 1)), a["slot_map"][:1], cache, a["ws"])
+    assert calls.args[-1][1:3] == calls.args[-1][4:6] == (0, 0)
+    _, a = binding_call(api, "paged_attention")
+    api.paged_attention(view((1, 1, 64), (389, 7, 1)), cache, a["block_tables"], a["q_start"], a["seq_lens"], view((1, 1, 64), (64, 64, 1)),
+                        a["ws"])
+    assert calls.args[-1][1:3] == (0, 0)

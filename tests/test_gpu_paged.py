@@ -519,3 +519,21 @@ def test_attention_requests_that_do_not_fit_are_left_out(api, what):
     assert api.read_status(ws) == api.EDEVICE_BAD_INDEX
     assert (out[~good] == 7).all() and (lse[~good] == 7).all()
     check_attention(out[good], lse[good], [t[good] for t in want])
+
+
+def test_one_token_of_an_odd_width(api):
+    """One request's one token, sliced out of a projection whose width is not a
+    multiple of 8."""
+    page, heads, d = 16, 8, 64
+    s = make_step([(100, 1)], page, heads, 1, d, torch.bfloat16, 59, poison=False)
+    width = (heads + 2) * d + 3
+    rows = torch.randn((1, width), device="cuda").bfloat16().as_strided((1, heads + 2, d), (width, d, 1))
+    cache, ws = api.KvCache(s["k"], s["v"]), api.paged_workspace(heads, api.KvCache(s["k"], s["v"]))
+    out = torch.empty((1, heads, d), dtype=torch.bfloat16, device="cuda")
+    slot = s["table"][:, 99 // page] * page + 99 % page
+    api.paged_append(rows[:, heads:heads + 1], rows[:, heads + 1:], slot.int(), cache, ws)
+    api.paged_attention(rows[:, :heads], cache, s["table"], s["q_start"], s["seq"], out, ws)
+    assert api.read_status(ws) == 0
+    assert torch.equal(s["k"][int(s["table"][0, 6]), 3], rows[0, heads:heads + 1])
+    s["q"] = rows[:, :heads].contiguous()
+    check_attention(out, None, attention(s))
