@@ -122,10 +122,11 @@ extern "C" {
                                      entries; each CTA writes the global timer
                                      (ns) at its phase boundaries into its 16
                                      entries. 0 (default) disables it. */
-#define MOE_OPT_DEBUG_HOLD_BACK 4 /* test hook: 1 keeps the first keys of each
-                                     CTA of moe_paged_attention from coming, so
-                                     that its waits run out and report
-                                     MOE_ETIMEOUT. 0 (default) disables it. */
+#define MOE_OPT_DEBUG_HOLD_BACK 4 /* test hook: 1 keeps the first keys (or
+                                     their scores) of each CTA of
+                                     moe_paged_attention from coming, so that
+                                     its waits run out and report MOE_ETIMEOUT.
+                                     0 (default) disables it. */
 
 typedef struct moe_shape {
     int32_t hidden;       /* H: multiple of 256 (bf16) or 512 (MXFP4, FP8), <= 8192 */

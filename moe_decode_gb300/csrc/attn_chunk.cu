@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_full + 8 * t, kSlotRows);
-            mbar_init(s_full + 8 * t, 1);
+            mbar_init(s_full + 8 * t, 1 + p.hold_back);  // (held back: a second arrival that never comes)
             mbar_init(p_full + 8 * t, kSlotRows);
             mbar_init(o_full + 8 * t, 1);
         }
@@ -177,16 +177,15 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             for (bool more = feed.any; ok && more; cur = next) {
                 more = feed.advance();
                 if (more) next = feed.box();
-                const bool want = attn_take(p, cur.wanted, cur.block);
-                const int n = __popc(__ballot_sync(0xffffffffu, want));
+                const bool take = attn_take(p, cur.wanted, cur.block);
+                const int n = __popc(__ballot_sync(0xffffffffu, take));
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     ok = __all_sync(0xffffffffu, ok && attn_wait(empty + 8 * stage, parity, p, flag));
                     if (!ok) break;
-                    const bool held = p.hold_back && issued == 0;
-                    if (lane == 0 && !held) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 2));
+                    if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * D * 2));
                     __syncwarp();
-                    if (want && !held) {
+                    if (take) {
                         const uint32_t dst = base + S::kOffKv + stage * S::kTile + lane * p.box * 128;
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
@@ -202,7 +201,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             }
             // the last copies of each stage, in flight where another role gave up
             if (lane == 0)
-                for (int i = max(p.hold_back, issued - S::kStages); i < issued; ++i)
+                for (int i = max(0, issued - S::kStages); i < issued; ++i)
                     attn_drain(full + 8 * (i % S::kStages), (uint32_t)((i / S::kStages) & 1));
             __syncwarp();
         } else if (warp == kMmaWarp) {

@@ -83,7 +83,7 @@ struct AttnParams {
     int G;       // CTAs
     float scale_log2;  // scale * log2(e)
     unsigned long long timeout_ns;
-    int hold_back;  // test hook: 1, a CTA's first copies are never issued
+    int hold_back;  // test hook: 1, a CTA's first keys (scores, in the chunk kernel) never come
 };
 
 // Whether any request of the call may have many rows.
