@@ -14,8 +14,8 @@
 // S(j + 1) also says that PV(j) is done, so they may rescale O. They do so only
 // where the largest score of a row has left the reference's range.
 //
-// Two chunks of 8,192 tokens over 16,383 keys (32/8 heads of 128) take 2.54 ms,
-// 1,300 TFLOP/s. A tile of both slots takes 3,500 cycles where its products
+// Two chunks of 8,192 tokens over 16,383 keys (32/8 heads of 128) take 2.58 ms
+// replayed from a graph, 1,280 TFLOP/s (2.09 ms with heads of 64). A tile of both slots takes 3,500 cycles where its products
 // alone are 2,048: 1,580 of a slot's softmax, 1,024 of its products and 500 to
 // 900 of hand-overs and of waiting for shared memory, which brings the 128
 // bytes a clock that Q K^T with both operands from it wants (without any
@@ -30,6 +30,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kThreads = 384;  // two warpgroups of softmax, one for the two issuing warps
 // A thread of the softmax holds a row of 128 scores: its warpgroups take
 // registers from the third. Together exactly what the block is launched with.
+// (At 128 dimensions 360 bytes of stores and 504 of loads are spilled.)
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kIssueRegs = 72;
 static_assert(2 * kSoftmaxRegs + kIssueRegs == 3 * kLaunchRegs, "registers of the block");
 

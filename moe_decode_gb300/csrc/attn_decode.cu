@@ -60,12 +60,12 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
 // three tiles of 128 keys (192 KB at 128 dimensions) on their way, across
 // items, and the queries of the item after the one at hand.
 //
-// Bound by HBM where the histories are long: 4 streams of 120,000 to 131,000
-// keys (64/8 heads of 128) take 296 us, 6.7 TB/s; 32 streams of 6 new tokens
-// over 300 to 16,000 keys (24 rows an item, pages of 16) 173 us, 5.9 TB/s in
-// the kernel. Four warps with 32 rows each took 206 us there: the second set of
+// Bound by HBM where the histories are long (times are of calls replayed from a
+// graph): 4 streams of 120,000 to 131,000 keys (64/8 heads of 128) take 309 us,
+// 6.7 TB/s; 32 streams of 6 new tokens over 300 to 16,000 keys (24 rows an item,
+// pages of 16) 174 us, 5.9 TB/s in the kernel. Four warps with 32 rows each took 206 us there: the second set of
 // warps hides the first's chains. Short histories are bound by latency: one
-// token over 1,001 keys takes 10.9 us.
+// token over 1,001 keys takes 11.2 us.
 template <int D, int DT>
 __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_constant__ AttnParams p,
                                                                    const __grid_constant__ CUtensorMap kmap,

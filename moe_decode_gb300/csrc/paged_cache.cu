@@ -66,7 +66,7 @@ __device__ __forceinline__ int last_at_most(const int* v, int n, int x) {
 // the prefix sums by bisection in shared memory. A token in a new block takes
 // its block from the free list directly, not from the table that another CTA
 // may be writing. Bound by the launch: 16 requests of 6 tokens (one CTA) take
-// 4.0 us a graph-replayed call, 512 requests of 40,895 tokens (80 CTAs) 5.0.
+// 4.1 us a graph-replayed call, 512 requests of 40,895 tokens (80 CTAs) 4.9.
 __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanParams p) {
     __shared__ int q0[kMaxRequests + 1];     // first token of each request
     __shared__ int first[kMaxRequests + 1];  // first new block of each request
