@@ -390,6 +390,126 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
                         const int32_t* q_start, const int32_t* seq_lens, int B, float scale, int window, void* out,
                         float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------- rotary positions
+ * The first rotary_dim of a head's dimensions turn with the token's position
+ * p, two at a time: pair i (i < rotary_dim / 2) is (x_i, x_(i + rotary_dim/2)),
+ * or, interleaved, (x_2i, x_(2i+1)), and with the angle a = p f_i
+ *   y_first = scale (x_first cos a - x_second sin a)
+ *   y_second = scale (x_first sin a + x_second cos a)
+ * in fp32, rounded once. The other dimensions are copied. Frequencies are held
+ * as turns: f_i / (2 pi), its whole part dropped, in units of 2^-64 turns. p
+ * times that is exact modulo one turn in 64-bit integers, so the angle is as
+ * good at position 2^31 - 1 as at 1. */
+typedef struct moe_rope_angles {
+    const uint64_t* turns; /* device, [rotary_dim / 2] */
+    int32_t rotary_dim;    /* a multiple of 16, at most the head's dimensions */
+    int32_t interleaved;   /* 0 or 1 */
+    float scale;           /* of the rotated values (1: none) */
+} moe_rope_angles;
+
+/* How frequencies base^(-2i / rotary_dim) are changed for contexts `factor`
+ * times the `context` that a model was made for:
+ *  LINEAR  f / factor
+ *  NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *  YARN    pairs that turn more than `high` times in `context` keep f, those
+ *          of less than `low` turns get f / factor, between them by a ramp
+ *          over the pair's number; scale = 0.1 ln(factor) + 1 (factor > 1)
+ *  BANDS   the same borders, the ramp over the number of turns; scale 1 */
+#define MOE_ROPE_NONE 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_NTK 2
+#define MOE_ROPE_YARN 3
+#define MOE_ROPE_BANDS 4
+/* Fills turns (host, [rotary_dim / 2]) and *scale (host) for these settings;
+ * computed on the host in 64 bits, once when a model is loaded. base > 1,
+ * factor > 0; context >= 1 for YARN and BANDS, with low < high (low <= 0: 1,
+ * high <= 0: 32 for YARN, 4 for BANDS). */
+int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int context, double low, double high,
+                   uint64_t* turns, float* scale);
+/* turns [n] (host) of any frequencies [n] in radians a position (host). */
+int moe_rope_turns(const double* radians, int n, uint64_t* turns);
+
+/* Rotates T tokens' queries q [T, q_heads, head_dim] and keys k [T, kv_heads,
+ * head_dim] (k NULL: queries alone), each by its strides (elements, multiples
+ * of 8), into q_out and k_out by theirs (at least head_dim). An output may be
+ * its input (with its strides); otherwise outputs overlap nothing. dtype 0
+ * bf16, 1 fp16; head_dim a multiple of 16, at most 512; heads <= 1024.
+ * positions int32 [T] as moe_paged_plan or moe_tree_plan gives them: rows at a
+ * negative one are padding and stay as they are in the outputs. */
+int moe_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
+             int64_t q_out_head_stride, int q_heads, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+             void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride, int kv_heads, int T, int head_dim,
+             int dtype, const int32_t* positions, const moe_rope_angles* angles, void* stream);
+
+/* moe_rope and moe_paged_append in one launch, with their results bit for bit:
+ * rotates q into q_out, and writes the rotated keys and the values as they are
+ * to the cache's slots. q NULL (q_heads 0): keys and values alone. A row at a
+ * negative position is padding: nothing of it is written. A row with slot -1
+ * writes no keys and values; a slot outside the cache is skipped and reported
+ * (MOE_EDEVICE_BAD_INDEX). All of the cache's dtype. ws as for
+ * moe_paged_append. */
+int moe_paged_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                          int64_t q_out_token_stride, int64_t q_out_head_stride, int q_heads, const void* k_new,
+                          int64_t k_token_stride, int64_t k_head_stride, const void* v_new, int64_t v_token_stride,
+                          int64_t v_head_stride, int T, const int32_t* positions, const int32_t* slot_map,
+                          const moe_rope_angles* angles, const moe_kv_cache* cache, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* ------------------------------------------------- cache of 8-bit values
+ * A paged cache whose keys and values are e4m3 codes with one power of two for
+ * each token and head, an e8m0 byte: value = e4m3(code) * 2^(byte - 127). As
+ * written by the append calls: for the head_dim values x of a token's head the
+ * byte is that of the least exponent e >= -127 with max |x| <= 448 * 2^e, and a
+ * code is the e4m3 number nearest to x * 2^-e (ties to even; no value is cut
+ * off, and a power of two adds no rounding of its own). A head in which some
+ * value is not finite gets the byte 255: all its values are NaN. Writing again
+ * what was read back gives the same values.
+ * Codes by strides as in moe_kv_cache, in bytes, multiples of 16. Scales
+ * [n_blocks, kv_heads, block_size], contiguous, 16-byte aligned. block_size a
+ * multiple of 16, at most 1024; the other limits as in moe_kv_cache. */
+typedef struct moe_kv_cache8 {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int32_t n_blocks;
+    int32_t block_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int64_t k_block_stride, k_token_stride, k_head_stride;
+    int64_t v_block_stride, v_token_stride, v_head_stride;
+} moe_kv_cache8;
+
+/* moe_paged_append into such a cache, from bf16 (dtype 0) or fp16 (1). */
+int moe_paged_append8(const void* k_new, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
+                      int64_t v_token_stride, int64_t v_head_stride, int T, int dtype, const int32_t* slot_map,
+                      const moe_kv_cache8* cache, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_paged_rope_append into such a cache: a rotated key is rounded to dtype
+ * and then quantised, as by moe_rope and moe_paged_append8. */
+int moe_paged_rope_append8(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                           int64_t q_out_token_stride, int64_t q_out_head_stride, int q_heads, const void* k_new,
+                           int64_t k_token_stride, int64_t k_head_stride, const void* v_new, int64_t v_token_stride,
+                           int64_t v_head_stride, int T, int dtype, const int32_t* positions, const int32_t* slot_map,
+                           const moe_rope_angles* angles, const moe_kv_cache8* cache, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* Reads T slots back: k_out, v_out [T, kv_heads, head_dim] by their strides
+ * (elements, multiples of 8, at least head_dim) get the keys and values of
+ * slot_map [T]. Slot -1 leaves its row as it is; a slot outside the cache too,
+ * and is reported (MOE_EDEVICE_BAD_INDEX). A slot may be read more than once.
+ * moe_paged_read copies the cache's own dtype; moe_paged_read8 gives bf16
+ * (dtype 0, exact but below 2^-126) or fp16 (1: rounded once, infinite above
+ * 65504). Uses: the context of a prompt chunk into a 16-bit cache that
+ * moe_paged_attention's many-row kernel reads; an accepted path of a tree,
+ * read from its slots and appended to the consecutive ones. */
+int moe_paged_read(const moe_kv_cache* cache, const int32_t* slot_map, int T, void* k_out, int64_t k_token_stride,
+                   int64_t k_head_stride, void* v_out, int64_t v_token_stride, int64_t v_head_stride, void* ws,
+                   size_t ws_bytes, void* stream);
+int moe_paged_read8(const moe_kv_cache8* cache, const int32_t* slot_map, int T, int dtype, void* k_out,
+                    int64_t k_token_stride, int64_t k_head_stride, void* v_out, int64_t v_token_stride,
+                    int64_t v_head_stride, void* ws, size_t ws_bytes, void* stream);
+
 /* One token from each of M rows of logits [M, V] (row_stride elements from
  * row to row; dtype 0: fp32, as moe_lm_head writes, 1: bf16), each with its
  * own settings (device arrays [M], NULL: off for every row):

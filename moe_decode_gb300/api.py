@@ -34,6 +34,7 @@ STATIC_SCRATCH_BYTES = 524288
 PAGED_WORKSPACE_BYTES = 1024
 PAGED_MAX_REQUESTS = 4096
 SAMPLE_MAX_VOCAB = 720896
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
@@ -60,6 +61,18 @@ class _KvCache(ctypes.Structure):
         (n, ctypes.c_int32) for n in ("dtype", "n_blocks", "block_size", "kv_heads", "head_dim")] + [
         (n, ctypes.c_int64) for n in ("k_block_stride", "k_token_stride", "k_head_stride", "v_block_stride",
                                       "v_token_stride", "v_head_stride")]
+
+
+class _KvCache8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int32) for n in ("n_blocks", "block_size", "kv_heads", "head_dim")] + [
+        (n, ctypes.c_int64) for n in ("k_block_stride", "k_token_stride", "k_head_stride", "v_block_stride",
+                                      "v_token_stride", "v_head_stride")]
+
+
+class _RopeAngles(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 def _load():
@@ -94,11 +107,23 @@ def _load():
     lib.moe_paged_attention_workspace_bytes.restype = SZ
     lib.moe_paged_attention.argtypes = [P, I64, I64, I32, I32, cp, P, I32, P, P, I32, F32, I32, P, P, P, SZ, P]
     lib.moe_sample.argtypes = [P, I32, I32, I32, I64, P, P, P, P, P, P, P, P]
+    F64, rp, c8 = ctypes.c_double, ctypes.POINTER(_RopeAngles), ctypes.POINTER(_KvCache8)
+    lib.moe_rope_table.argtypes = [I32, F64, I32, F64, I32, F64, F64, P, ctypes.POINTER(F32)]
+    lib.moe_rope_turns.argtypes = [P, I32, P]
+    rows = [P, I64, I64]
+    lib.moe_rope.argtypes = [*rows, *rows, I32, *rows, *rows, I32, I32, I32, I32, P, rp, P]
+    lib.moe_paged_rope_append.argtypes = [*rows, *rows, I32, *rows, *rows, I32, P, P, rp, cp, P, SZ, P]
+    lib.moe_paged_rope_append8.argtypes = [*rows, *rows, I32, *rows, *rows, I32, I32, P, P, rp, c8, P, SZ, P]
+    lib.moe_paged_append8.argtypes = [*rows, *rows, I32, I32, P, c8, P, SZ, P]
+    lib.moe_paged_read.argtypes = [cp, P, I32, *rows, *rows, P, SZ, P]
+    lib.moe_paged_read8.argtypes = [c8, P, I32, I32, *rows, *rows, P, SZ, P]
     lib.moe_last_launch_count.argtypes = []
     for f in ("moe_workspace_init", "moe_route", "moe_ffn", "moe_decode_layer", "moe_decode_layer_static_scratch",
               "moe_read_status", "moe_static_scratch_status", "moe_mxfp4_dequant", "moe_set_option", "moe_last_launch_count",
               "moe_lm_head", "moe_fp8_quantize", "moe_fp8_dequant", "moe_transpose_down",
-              "moe_paged_plan", "moe_paged_append", "moe_paged_attention", "moe_sample"):
+              "moe_paged_plan", "moe_paged_append", "moe_paged_attention", "moe_sample", "moe_rope_table", "moe_rope_turns",
+              "moe_rope", "moe_paged_rope_append", "moe_paged_rope_append8", "moe_paged_append8", "moe_paged_read",
+              "moe_paged_read8"):
         getattr(lib, f).restype = I32
     return lib
 
@@ -335,6 +360,38 @@ class KvCache:
         self._ref = ctypes.pointer(self._c)
 
 
+class KvCache8:
+    """A paged KV cache of e4m3 codes with one power of two for each token and
+    head (moe_kv_cache8): K and V [n_blocks, block_size, kv_heads, head_dim]
+    uint8 or float8_e4m3fn views (strides multiples of 16, the last dimension
+    contiguous), k_scale and v_scale uint8 [n_blocks, kv_heads, block_size]
+    contiguous (e8m0: 2^(byte - 127), 255 for NaN). KvCache8.empty makes one.
+    Takes the place of a KvCache in paged_append, paged_rope_append,
+    paged_attention and paged_read; their other tensors are bf16 or fp16."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        _want(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in (torch.uint8, torch.float8_e4m3fn)
+              and k.stride(3) == 1 and v.stride(3) == 1, "KvCache8: K and V [blocks, tokens, heads, d], uint8 or float8_e4m3fn", ESHAPE)
+        n_blocks, self.block_size, self.kv_heads, self.head_dim = k.shape
+        for s in (k_scale, v_scale):
+            _want(s.dtype is torch.uint8 and s.shape == (n_blocks, self.kv_heads, self.block_size) and s.is_contiguous(),
+                  "KvCache8: k_scale and v_scale uint8 [blocks, heads, tokens], contiguous", ESHAPE)
+        _want(k.get_device() == v.get_device() == k_scale.get_device() == v_scale.get_device(), "KvCache8: all tensors on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device_index = k.get_device()
+        # (a dimension of one element has no stride of its own)
+        sk, sv = ([t.stride(i) if t.shape[i] > 1 else (self.head_dim + 15) // 16 * 16 for i in range(3)] for t in (k, v))
+        self._c = _KvCache8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_blocks, self.block_size,
+                            self.kv_heads, self.head_dim, *sk, *sv)
+        self._ref = ctypes.pointer(self._c)
+
+    @classmethod
+    def empty(cls, n_blocks: int, block_size: int, kv_heads: int, head_dim: int, device="cuda") -> "KvCache8":
+        k, v = (torch.zeros((n_blocks, block_size, kv_heads, head_dim), dtype=torch.uint8, device=device) for _ in range(2))
+        ks, vs = (torch.zeros((n_blocks, kv_heads, block_size), dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
 def paged_workspace(q_heads: int = 0, cache: Optional[KvCache] = None, device="cuda", stream=None) -> torch.Tensor:
     """A zeroed workspace for the paged-step calls: for paged_attention with
     q_heads over `cache`, or, without them, for paged_plan and paged_append."""
@@ -366,17 +423,36 @@ def paged_plan(ctx_lens, new_lens, free_list, block_tables, block_size: int, q_s
         raise MoeError(rc, "moe_paged_plan")
 
 
-def paged_append(k_new, v_new, slot_map, cache: KvCache, ws, stream=None):
+def _strides(t: torch.Tensor, least: int = 0):
+    """Token and head strides of [T, heads, d]; a dimension of one element has
+    no stride of its own."""
+    T, heads, d = t.shape
+    a, b, _ = t.stride()
+    own = (d + 7) // 8 * 8
+    return (a if T > 1 else max(least, own) * heads if least else 0), (b if heads > 1 else own if least else 0)
+
+
+def _rows(what: str, dev: int, dtype: torch.dtype, shape, *tensors):
+    for t in tensors:
+        if t.shape != shape:
+            raise MoeError(ESHAPE, f"{what}: {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype != dtype or t.get_device() != dev or t.stride(2) != 1:
+            raise MoeError(EINVAL, f"{what}: {dtype}, the last dimension contiguous, on the current device; got {t.dtype} on {t.device}")
+
+
+def paged_append(k_new, v_new, slot_map, cache, ws, stream=None):
     """Writes k_new, v_new [T, kv_heads, head_dim] (last dimension contiguous,
     e.g. slices of a fused projection's output) to the cache's slots
-    slot_map [T] (moe_paged_append)."""
+    slot_map [T] (moe_paged_append, or moe_paged_append8 into a KvCache8)."""
     T = k_new.shape[0]
     _want(k_new.shape == (T, cache.kv_heads, cache.head_dim) and v_new.shape == k_new.shape,
           "paged_append: k_new, v_new [T, kv_heads, head_dim]", ESHAPE)
     dev = _device("paged_append", k_new)
-    _want(k_new.dtype == cache.dtype and v_new.dtype == cache.dtype and k_new.stride(2) == 1 and v_new.stride(2) == 1
+    codes = isinstance(cache, KvCache8)
+    dtype = k_new.dtype if codes and k_new.dtype in DTYPES else torch.bfloat16 if codes else cache.dtype
+    _want(k_new.dtype == dtype and v_new.dtype == dtype and k_new.stride(2) == 1 and v_new.stride(2) == 1
           and k_new.get_device() == v_new.get_device() == cache.device_index == dev,
-          "paged_append: k_new, v_new of the cache's dtype, all on the current device")
+          "paged_append: k_new, v_new of the cache's dtype (KvCache8: bf16 or fp16), all on the current device")
     _vectors("paged_append: slot_map", dev, torch.int32, (slot_map, T))
     _workspace("paged_append", dev, ws)
     kt, kh, _ = k_new.stride()
@@ -385,10 +461,145 @@ def paged_append(k_new, v_new, slot_map, cache: KvCache, ws, stream=None):
         kt = vt = 0
     if cache.kv_heads == 1:
         kh = vh = 0
-    rc = lib.moe_paged_append(k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T, slot_map.data_ptr(), cache._ref,
-                              ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    if codes:
+        rc = lib.moe_paged_append8(k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T, DTYPES[dtype], slot_map.data_ptr(),
+                                   cache._ref, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    else:
+        rc = lib.moe_paged_append(k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T, slot_map.data_ptr(), cache._ref,
+                                  ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc:
-        raise MoeError(rc, "moe_paged_append")
+        raise MoeError(rc, "moe_paged_append8" if codes else "moe_paged_append")
+
+
+class Rope:
+    """Angles of rotary positions (moe_rope_angles): how fast each pair of the
+    first rotary_dim dimensions turns, as integers on the device. scaling:
+    "none", "linear", "ntk", "yarn" or "bands" for contexts `factor` times the
+    `context` a model was made for (moe_rope_table; low and high are the
+    borders in turns, 0 for the usual ones); scale: of the rotated values, None
+    for the scaling's own. Rope.of(frequencies) takes any frequencies."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, context: int = 0, low: float = 0.0, high: float = 0.0, scale: Optional[float] = None,
+                 device="cuda"):
+        _want(scaling in ROPE_SCALINGS, f"Rope: scaling one of {', '.join(ROPE_SCALINGS)}")
+        turns = (ctypes.c_uint64 * max(1, rotary_dim // 2))()
+        own = ctypes.c_float(1.0)
+        _check(lib.moe_rope_table(rotary_dim, base, ROPE_SCALINGS[scaling], factor, context, low, high, turns,
+                                  ctypes.byref(own)), "moe_rope_table")
+        self._set(turns, rotary_dim, interleaved, own.value if scale is None else scale, device)
+
+    @classmethod
+    def of(cls, frequencies, interleaved: bool = False, scale: float = 1.0, device="cuda") -> "Rope":
+        """frequencies: radians a position of each pair (numbers of 64 bits)."""
+        f = [float(x) for x in frequencies]
+        turns = (ctypes.c_uint64 * max(1, len(f)))()
+        _check(lib.moe_rope_turns((ctypes.c_double * max(1, len(f)))(*f), len(f), turns), "moe_rope_turns")
+        self = cls.__new__(cls)
+        self._set(turns, 2 * len(f), interleaved, scale, device)
+        return self
+
+    def _set(self, turns, rotary_dim, interleaved, scale, device):
+        # (the same 64 bits in torch's signed integers)
+        signed = [t - (1 << 64) if t >= 1 << 63 else t for t in turns]
+        self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+        self.rotary_dim, self.interleaved, self.scale = rotary_dim, bool(interleaved), scale
+        self.device_index = self.turns.get_device()
+        self._c = _RopeAngles(self.turns.data_ptr(), rotary_dim, int(interleaved), scale)
+        self._ref = ctypes.pointer(self._c)
+
+
+def rope(q, k, positions, angles: Rope, q_out=None, k_out=None, stream=None):
+    """Rotates q [T, q_heads, head_dim] and k [T, kv_heads, head_dim] (or
+    None) to the positions int32 [T] (moe_rope): into q_out and k_out, or in
+    place. bf16 or fp16, the last dimension contiguous; rows at a negative
+    position stay as they are."""
+    T, heads, d = q.shape
+    dev = _device("rope", q)
+    _want(q.dtype in DTYPES, "rope: q bf16 or fp16")
+    q_out = q if q_out is None else q_out
+    _rows("rope: q, q_out", dev, q.dtype, q.shape, q, q_out)
+    qt, qh = _strides(q)
+    ot, oh = _strides(q_out, d)
+    if q_out.data_ptr() == q.data_ptr():
+        qt, qh = (ot if T == 1 else qt), (oh if heads == 1 else qh)
+    kv, kp, ko, kt, kh, pt, ph = 0, None, None, 0, 0, 0, 0
+    if k is not None:
+        kv = k.shape[1]
+        k_out = k if k_out is None else k_out
+        _rows("rope: k, k_out", dev, q.dtype, (T, kv, d), k, k_out)
+        kt, kh = _strides(k)
+        pt, ph = _strides(k_out, d)
+        if k_out.data_ptr() == k.data_ptr():
+            kt, kh = (pt if T == 1 else kt), (ph if kv == 1 else kh)
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+    else:
+        _want(k_out is None, "rope: k_out without k")
+    _vectors("rope: positions", dev, torch.int32, (positions, T))
+    _want(angles.device_index == dev, "rope: angles on the current device")
+    rc = lib.moe_rope(q.data_ptr(), qt, qh, q_out.data_ptr(), ot, oh, heads, kp, kt, kh, ko, pt, ph, kv, T, d,
+                      DTYPES[q.dtype], positions.data_ptr(), angles._ref, _raw_stream(stream, dev))
+    if rc:
+        raise MoeError(rc, "moe_rope")
+
+
+def paged_rope_append(q, k_new, v_new, positions, slot_map, angles: Rope, cache, ws, q_out=None, stream=None):
+    """rope and paged_append in one launch (moe_paged_rope_append, or
+    moe_paged_rope_append8 into a KvCache8): q [T, q_heads, head_dim] (or None)
+    rotated into q_out or in place, k_new [T, kv_heads, head_dim] rotated and
+    v_new as it is into the cache's slots slot_map [T]; k_new keeps its values."""
+    T = k_new.shape[0]
+    d = cache.head_dim
+    dev = _device("paged_rope_append", k_new)
+    codes = isinstance(cache, KvCache8)
+    dtype = k_new.dtype if codes else cache.dtype
+    _want(dtype in DTYPES and cache.device_index == dev and angles.device_index == dev,
+          "paged_rope_append: bf16 or fp16, cache and angles on the current device")
+    _rows("paged_rope_append: k_new, v_new", dev, dtype, (T, cache.kv_heads, d), k_new, v_new)
+    kt, kh = _strides(k_new)
+    vt, vh = _strides(v_new)
+    heads, qp, op, qt, qh, ot, oh = 0, None, None, 0, 0, 0, 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        heads = q.shape[1]
+        _rows("paged_rope_append: q, q_out", dev, dtype, (T, heads, d), q, q_out)
+        qt, qh = _strides(q)
+        ot, oh = _strides(q_out, d)
+        if q_out.data_ptr() == q.data_ptr():
+            qt, qh = (ot if T == 1 else qt), (oh if heads == 1 else qh)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    else:
+        _want(q_out is None, "paged_rope_append: q_out without q")
+    _vectors("paged_rope_append: positions, slot_map", dev, torch.int32, (positions, T), (slot_map, T))
+    _workspace("paged_rope_append", dev, ws)
+    args = (qp, qt, qh, op, ot, oh, heads, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T)
+    rest = (positions.data_ptr(), slot_map.data_ptr(), angles._ref, cache._ref, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    rc = lib.moe_paged_rope_append8(*args, DTYPES[dtype], *rest) if codes else lib.moe_paged_rope_append(*args, *rest)
+    if rc:
+        raise MoeError(rc, "moe_paged_rope_append8" if codes else "moe_paged_rope_append")
+
+
+def paged_read(cache, slot_map, k_out, v_out, ws, stream=None):
+    """Reads the slots slot_map [T] back into k_out, v_out [T, kv_heads,
+    head_dim] (moe_paged_read, of the cache's dtype, or moe_paged_read8 of a
+    KvCache8, bf16 or fp16); rows of slot -1 stay as they are."""
+    T = slot_map.numel()
+    dev = _device("paged_read", slot_map)
+    codes = isinstance(cache, KvCache8)
+    dtype = k_out.dtype if codes else cache.dtype
+    _want(dtype in DTYPES and cache.device_index == dev, "paged_read: bf16 or fp16, cache on the current device")
+    _rows("paged_read: k_out, v_out", dev, dtype, (T, cache.kv_heads, cache.head_dim), k_out, v_out)
+    _vectors("paged_read: slot_map", dev, torch.int32, (slot_map, T))
+    _workspace("paged_read", dev, ws)
+    kt, kh = _strides(k_out, cache.head_dim)
+    vt, vh = _strides(v_out, cache.head_dim)
+    out = (k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    if codes:
+        rc = lib.moe_paged_read8(cache._ref, slot_map.data_ptr(), T, DTYPES[dtype], *out)
+    else:
+        rc = lib.moe_paged_read(cache._ref, slot_map.data_ptr(), T, *out)
+    if rc:
+        raise MoeError(rc, "moe_paged_read8" if codes else "moe_paged_read")
 
 
 def paged_attention(q, cache: KvCache, block_tables, q_start, seq_lens, out, ws, lse=None, scale: float = 0.0,

@@ -12,69 +12,27 @@
 #include "host.h"
 #include "layer_params.h"
 #include "paged.h"
+#include "paged_host.h"
 
 namespace {
 
 using moe::DeviceInfo;
+using moe::EncodeTiled;
 using moe::aligned16;
+using moe::aligned4;
+using moe::check_cache;
+using moe::check_ws;
 using moe::device_info;
+using moe::encode_tiled;
 using moe::g_last_launches;
 using moe::g_opt;
+using moe::launched;
+using moe::stride_ok;
 
 static_assert(moe::kMaxRequests == MOE_PAGED_MAX_REQUESTS, "request limit");
 static_assert(moe::kSampleMaxSlice * 16 == MOE_SAMPLE_MAX_VOCAB, "vocabulary limit");
 static_assert(moe::kAttnMaxGrid == MOE_MAX_GRID, "grid limit");
 static_assert(moe::kCtlBytes <= MOE_PAGED_WORKSPACE_BYTES, "control block");
-
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-int check_ws(const void* ws, size_t ws_bytes, size_t need) {
-    if (!ws) return MOE_EWORKSPACE;
-    if (!aligned16(ws)) return MOE_EALIGN;
-    return ws_bytes < need ? MOE_EWORKSPACE : MOE_OK;
-}
-
-bool stride_ok(int64_t s, int least) { return s >= least && s % 8 == 0 && s < (1LL << 36); }
-
-int check_cache(const moe_kv_cache* c) {
-    if (!c || !c->k || !c->v) return MOE_EINVAL;
-    if (c->dtype != 0 && c->dtype != 1) return MOE_ESHAPE;
-    if (c->head_dim != 64 && c->head_dim != 128) return MOE_ESHAPE;
-    if (c->kv_heads < 1 || c->kv_heads > 256) return MOE_ESHAPE;
-    if (c->block_size < 8 || c->block_size > 1024 || c->block_size % 8 != 0) return MOE_ESHAPE;
-    if (c->n_blocks < 1 || (int64_t)c->n_blocks * c->block_size > 0x7fffffffLL) return MOE_ESHAPE;
-    for (int64_t s : {c->k_block_stride, c->k_token_stride, c->k_head_stride, c->v_block_stride, c->v_token_stride,
-                      c->v_head_stride})
-        if (!stride_ok(s, c->head_dim)) return MOE_ESHAPE;
-    if (!aligned16(c->k) || !aligned16(c->v)) return MOE_EALIGN;
-    return MOE_OK;
-}
-
-int launched(cudaError_t e, int n) {
-    g_last_launches = n;
-    if (e == cudaSuccess) return MOE_OK;
-    cudaGetLastError();
-    return MOE_ECUDA;
-}
-
-using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
-
-// The driver's tensor-map encoder, looked up once (the library links the
-// runtime alone).
-EncodeTiled encode_tiled() {
-    static EncodeTiled f = [] {
-        void* sym = nullptr;
-        cudaDriverEntryPointQueryResult res;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &res) !=
-                cudaSuccess ||
-            res != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            sym = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(sym);
-    }();
-    return f;
-}
 
 // Tensor map of a cache: (64 dimensions, token of the block, which 64, head,
 // block), boxes of `panels` times 64 dimensions by `box` tokens in the 128-byte

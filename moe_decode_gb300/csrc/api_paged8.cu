@@ -1,0 +1,326 @@
+// C ABI of rotary positions, of the paged cache of 8-bit values and of reading
+// slots back: argument checking and launch configuration. Declarations and the
+// contract of every entry point are in include/moe_decode.h.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "moe_decode.h"
+#include "host.h"
+#include "layer_params.h"
+#include "paged.h"
+#include "paged_host.h"
+
+namespace {
+
+using moe::DeviceInfo;
+using moe::aligned16;
+using moe::aligned4;
+using moe::check_cache;
+using moe::check_cache8;
+using moe::check_ws;
+using moe::device_info;
+using moe::g_last_launches;
+using moe::launched;
+using moe::stride_ok;
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+// The part of a turn that a position adds, in 2^-64 of one.
+uint64_t turns_of(double radians) {
+    double t = radians / kTwoPi;
+    t -= std::floor(t);
+    const double units = std::nearbyint(std::ldexp(t, 64));
+    return units >= 18446744073709551616.0 ? 0u : static_cast<uint64_t>(units);
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+int check_angles(const moe_rope_angles* a, int head_dim) {
+    if (!a || !a->turns) return MOE_EINVAL;
+    if (a->rotary_dim < 16 || a->rotary_dim % 16 != 0 || a->rotary_dim > head_dim) return MOE_ESHAPE;
+    if (a->interleaved != 0 && a->interleaved != 1) return MOE_EINVAL;
+    if (!std::isfinite(a->scale)) return MOE_EINVAL;
+    return aligned8(a->turns) ? MOE_OK : MOE_EALIGN;
+}
+
+struct Rows {
+    const void* p;
+    int64_t token, head;
+};
+int check_rows(const Rows& in) {
+    if (!in.p) return MOE_EINVAL;
+    if (!stride_ok(in.token, 0) || !stride_ok(in.head, 0)) return MOE_ESHAPE;
+    return aligned16(in.p) ? MOE_OK : MOE_EALIGN;
+}
+int check_out(const Rows& out, int head_dim) {
+    if (!out.p) return MOE_EINVAL;
+    if (!stride_ok(out.token, head_dim) || !stride_ok(out.head, head_dim)) return MOE_ESHAPE;
+    return aligned16(out.p) ? MOE_OK : MOE_EALIGN;
+}
+// An output in its input's place has its strides.
+int check_pair(const Rows& in, const Rows& out, int head_dim) {
+    int rc = check_rows(in);
+    if (rc == MOE_OK) rc = check_out(out, head_dim);
+    if (rc == MOE_OK && in.p == out.p && (in.token != out.token || in.head != out.head)) rc = MOE_EINVAL;
+    return rc;
+}
+
+void set_rows(moe::RotateParams& p, int i, const Rows& in, int heads) {
+    p.src[i] = static_cast<const uint16_t*>(in.p);
+    p.src_token[i] = in.token;
+    p.src_head[i] = in.head;
+    p.heads[i] = heads;
+}
+void set_out(moe::RotateParams& p, int i, const Rows& out) {
+    p.dst[i] = static_cast<uint16_t*>(const_cast<void*>(out.p));
+    p.dst_token[i] = out.token;
+    p.dst_head[i] = out.head;
+}
+void set_angles(moe::RotateParams& p, const moe_rope_angles* a, const int32_t* positions) {
+    p.positions = positions;
+    p.turns = reinterpret_cast<const unsigned long long*>(a->turns);
+    p.scale = a->scale;
+    p.rotary_dim = a->rotary_dim;
+    p.interleaved = a->interleaved;
+}
+template <class P>
+void set_cache(P& p, const moe_kv_cache* c) {
+    p.cache[0] = static_cast<uint8_t*>(c->k);
+    p.cache[1] = static_cast<uint8_t*>(c->v);
+    const int64_t s[2][3] = {{c->k_block_stride, c->k_token_stride, c->k_head_stride},
+                             {c->v_block_stride, c->v_token_stride, c->v_head_stride}};
+    for (int i = 0; i < 2; ++i) {
+        p.cache_block[i] = 2 * s[i][0];
+        p.cache_token[i] = 2 * s[i][1];
+        p.cache_head[i] = 2 * s[i][2];
+    }
+    p.block_size = c->block_size;
+    p.n_slots = (int64_t)c->n_blocks * c->block_size;
+}
+template <class P>
+void set_cache(P& p, const moe_kv_cache8* c) {
+    p.cache[0] = static_cast<uint8_t*>(c->k);
+    p.cache[1] = static_cast<uint8_t*>(c->v);
+    p.cache_scale[0] = c->k_scale;
+    p.cache_scale[1] = c->v_scale;
+    const int64_t s[2][3] = {{c->k_block_stride, c->k_token_stride, c->k_head_stride},
+                             {c->v_block_stride, c->v_token_stride, c->v_head_stride}};
+    for (int i = 0; i < 2; ++i) {
+        p.cache_block[i] = s[i][0];
+        p.cache_token[i] = s[i][1];
+        p.cache_head[i] = s[i][2];
+    }
+    p.block_size = c->block_size;
+    p.n_slots = (int64_t)c->n_blocks * c->block_size;
+}
+
+// Keys and values into a cache, rotated where there are angles, and queries
+// rotated beside them.
+template <class Cache>
+int append(const Rows& q, const Rows& q_out, int q_heads, const Rows& k, const Rows& v, int T, int dtype,
+           const int32_t* positions, const int32_t* slot_map, const moe_rope_angles* angles, bool rotate,
+           const Cache* cache, int to, void* ws, size_t ws_bytes, void* stream) {
+    if (T < 0 || (dtype != 0 && dtype != 1)) return MOE_ESHAPE;
+    if (q_heads < 0 || q_heads > 1024 || ((q.p != nullptr) != (q_heads > 0))) return MOE_ESHAPE;
+    if (rotate) {
+        const int rc = check_angles(angles, cache->head_dim);
+        if (rc) return rc;
+    }
+    if (T == 0) return MOE_OK;
+    if (!slot_map || (rotate && !positions)) return MOE_EINVAL;
+    int rc = check_rows(k);
+    if (rc == MOE_OK) rc = check_rows(v);
+    if (rc == MOE_OK && q_heads > 0) rc = check_pair(q, q_out, cache->head_dim);
+    if (rc) return rc;
+    if (!aligned4(slot_map) || !aligned4(positions)) return MOE_EALIGN;
+    rc = check_ws(ws, ws_bytes, MOE_PAGED_WORKSPACE_BYTES);
+    if (rc) return rc;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc) return rc;
+    moe::RotateParams p = {};
+    set_rows(p, 0, q, q_heads);
+    set_rows(p, 1, k, cache->kv_heads);
+    set_rows(p, 2, v, cache->kv_heads);
+    set_out(p, 0, q_out);
+    if (rotate) set_angles(p, angles, positions);
+    set_cache(p, cache);
+    p.slots = slot_map;
+    p.ctrl = static_cast<unsigned*>(ws);
+    p.T = T;
+    p.head_dim = cache->head_dim;
+    return launched(moe::launch_rotate(p, to, dtype, dev.sms, static_cast<cudaStream_t>(stream)), 1);
+}
+
+template <class Cache>
+int read(const Cache* cache, const int32_t* slot_map, int T, int dtype, int from, const Rows& k, const Rows& v, void* ws,
+         size_t ws_bytes, void* stream) {
+    if (T < 0 || (dtype != 0 && dtype != 1)) return MOE_ESHAPE;
+    if (T == 0) return MOE_OK;
+    if (!slot_map) return MOE_EINVAL;
+    int rc = check_out(k, cache->head_dim);
+    if (rc == MOE_OK) rc = check_out(v, cache->head_dim);
+    if (rc) return rc;
+    if (!aligned4(slot_map)) return MOE_EALIGN;
+    rc = check_ws(ws, ws_bytes, MOE_PAGED_WORKSPACE_BYTES);
+    if (rc) return rc;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc) return rc;
+    moe::ReadParams p = {};
+    set_cache(p, cache);
+    const Rows* out[2] = {&k, &v};
+    for (int i = 0; i < 2; ++i) {
+        p.dst[i] = static_cast<uint16_t*>(const_cast<void*>(out[i]->p));
+        p.dst_token[i] = out[i]->token;
+        p.dst_head[i] = out[i]->head;
+    }
+    p.slots = slot_map;
+    p.ctrl = static_cast<unsigned*>(ws);
+    p.T = T;
+    p.heads = cache->kv_heads;
+    p.lane_shift = cache->head_dim == 64 ? 2 : 3;
+    return launched(moe::launch_read(p, from, dtype, dev.sms, static_cast<cudaStream_t>(stream)), 1);
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_rope_turns(const double* radians, int n, uint64_t* turns) {
+    if (n < 0) return MOE_ESHAPE;
+    if (n > 0 && (!radians || !turns)) return MOE_EINVAL;
+    for (int i = 0; i < n; ++i)
+        if (!std::isfinite(radians[i])) return MOE_EINVAL;
+    for (int i = 0; i < n; ++i) turns[i] = turns_of(radians[i]);
+    return MOE_OK;
+}
+
+int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int context, double low, double high,
+                   uint64_t* turns, float* scale) {
+    if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > 512) return MOE_ESHAPE;
+    if (!turns || !scale || scaling < MOE_ROPE_NONE || scaling > MOE_ROPE_BANDS) return MOE_EINVAL;
+    if (!std::isfinite(base) || !(base > 1)) return MOE_EINVAL;
+    const bool borders = scaling == MOE_ROPE_YARN || scaling == MOE_ROPE_BANDS;
+    if (scaling != MOE_ROPE_NONE && (!std::isfinite(factor) || !(factor > 0))) return MOE_EINVAL;
+    if (!std::isfinite(low) || !std::isfinite(high)) return MOE_EINVAL;
+    if (low <= 0) low = 1;
+    if (high <= 0) high = scaling == MOE_ROPE_YARN ? 32 : 4;
+    if (borders && (context < 1 || !(low < high))) return MOE_EINVAL;
+    const int pairs = rotary_dim / 2;
+    if (scaling == MOE_ROPE_NTK) base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+    // the pair's number at which a frequency makes n turns in the context
+    auto pair_of = [&](double n) { return rotary_dim * std::log(context / (n * kTwoPi)) / (2 * std::log(base)); };
+    double first = 0, last = 0;
+    if (scaling == MOE_ROPE_YARN) {
+        first = std::fmax(std::floor(pair_of(high)), 0);
+        last = std::fmin(std::ceil(pair_of(low)), rotary_dim - 1);
+    }
+    *scale = scaling == MOE_ROPE_YARN && factor > 1 ? (float)(0.1 * std::log(factor) + 1) : 1.f;
+    for (int i = 0; i < pairs; ++i) {
+        const double f = std::pow(base, -2.0 * i / rotary_dim);
+        double kept = 1;  // share of the frequency that stays
+        if (scaling == MOE_ROPE_LINEAR) kept = 0;
+        if (scaling == MOE_ROPE_YARN) kept = 1 - std::fmin(std::fmax((i - first) / std::fmax(last - first, 0.001), 0), 1);
+        if (scaling == MOE_ROPE_BANDS) kept = std::fmin(std::fmax((context * f / kTwoPi - low) / (high - low), 0), 1);
+        turns[i] = turns_of(kept == 1 ? f : f / factor * (1 - kept) + f * kept);
+    }
+    return MOE_OK;
+}
+
+int moe_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
+             int64_t q_out_head_stride, int q_heads, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+             void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride, int kv_heads, int T, int head_dim,
+             int dtype, const int32_t* positions, const moe_rope_angles* angles, void* stream) {
+    g_last_launches = 0;
+    if (head_dim < 16 || head_dim % 16 != 0 || head_dim > 512 || (dtype != 0 && dtype != 1)) return MOE_ESHAPE;
+    int rc = check_angles(angles, head_dim);
+    if (rc) return rc;
+    if (T < 0 || q_heads < 1 || q_heads > 1024 || kv_heads < 0 || kv_heads > 1024 || ((k != nullptr) != (kv_heads > 0)))
+        return MOE_ESHAPE;
+    if (T == 0) return MOE_OK;
+    const Rows qs{q, q_token_stride, q_head_stride}, qo{q_out, q_out_token_stride, q_out_head_stride};
+    const Rows ks{k, k_token_stride, k_head_stride}, ko{k_out, k_out_token_stride, k_out_head_stride};
+    rc = check_pair(qs, qo, head_dim);
+    if (rc == MOE_OK && k) rc = check_pair(ks, ko, head_dim);
+    if (rc) return rc;
+    if (!positions) return MOE_EINVAL;
+    if (!aligned4(positions)) return MOE_EALIGN;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc) return rc;
+    moe::RotateParams p = {};
+    set_rows(p, 0, qs, q_heads);
+    set_out(p, 0, qo);
+    if (k) {
+        set_rows(p, 1, ks, kv_heads);
+        set_out(p, 1, ko);
+    }
+    set_angles(p, angles, positions);
+    p.T = T;
+    p.head_dim = head_dim;
+    return launched(moe::launch_rotate(p, moe::kRotateRows, dtype, dev.sms, static_cast<cudaStream_t>(stream)), 1);
+}
+
+int moe_paged_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                          int64_t q_out_token_stride, int64_t q_out_head_stride, int q_heads, const void* k_new,
+                          int64_t k_token_stride, int64_t k_head_stride, const void* v_new, int64_t v_token_stride,
+                          int64_t v_head_stride, int T, const int32_t* positions, const int32_t* slot_map,
+                          const moe_rope_angles* angles, const moe_kv_cache* cache, void* ws, size_t ws_bytes,
+                          void* stream) {
+    g_last_launches = 0;
+    const int rc = check_cache(cache);
+    if (rc) return rc;
+    return append({q, q_token_stride, q_head_stride}, {q_out, q_out_token_stride, q_out_head_stride}, q_heads,
+                  {k_new, k_token_stride, k_head_stride}, {v_new, v_token_stride, v_head_stride}, T, cache->dtype, positions,
+                  slot_map, angles, true, cache, moe::kRotateCache16, ws, ws_bytes, stream);
+}
+
+int moe_paged_rope_append8(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                           int64_t q_out_token_stride, int64_t q_out_head_stride, int q_heads, const void* k_new,
+                           int64_t k_token_stride, int64_t k_head_stride, const void* v_new, int64_t v_token_stride,
+                           int64_t v_head_stride, int T, int dtype, const int32_t* positions, const int32_t* slot_map,
+                           const moe_rope_angles* angles, const moe_kv_cache8* cache, void* ws, size_t ws_bytes,
+                           void* stream) {
+    g_last_launches = 0;
+    const int rc = check_cache8(cache);
+    if (rc) return rc;
+    return append({q, q_token_stride, q_head_stride}, {q_out, q_out_token_stride, q_out_head_stride}, q_heads,
+                  {k_new, k_token_stride, k_head_stride}, {v_new, v_token_stride, v_head_stride}, T, dtype, positions,
+                  slot_map, angles, true, cache, moe::kRotateCache8, ws, ws_bytes, stream);
+}
+
+int moe_paged_append8(const void* k_new, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
+                      int64_t v_token_stride, int64_t v_head_stride, int T, int dtype, const int32_t* slot_map,
+                      const moe_kv_cache8* cache, void* ws, size_t ws_bytes, void* stream) {
+    g_last_launches = 0;
+    const int rc = check_cache8(cache);
+    if (rc) return rc;
+    return append({nullptr, 0, 0}, {nullptr, 0, 0}, 0, {k_new, k_token_stride, k_head_stride},
+                  {v_new, v_token_stride, v_head_stride}, T, dtype, nullptr, slot_map, nullptr, false, cache,
+                  moe::kRotateCache8, ws, ws_bytes, stream);
+}
+
+int moe_paged_read(const moe_kv_cache* cache, const int32_t* slot_map, int T, void* k_out, int64_t k_token_stride,
+                   int64_t k_head_stride, void* v_out, int64_t v_token_stride, int64_t v_head_stride, void* ws,
+                   size_t ws_bytes, void* stream) {
+    g_last_launches = 0;
+    const int rc = check_cache(cache);
+    if (rc) return rc;
+    return read(cache, slot_map, T, cache->dtype, 0, {k_out, k_token_stride, k_head_stride},
+                {v_out, v_token_stride, v_head_stride}, ws, ws_bytes, stream);
+}
+
+int moe_paged_read8(const moe_kv_cache8* cache, const int32_t* slot_map, int T, int dtype, void* k_out,
+                    int64_t k_token_stride, int64_t k_head_stride, void* v_out, int64_t v_token_stride,
+                    int64_t v_head_stride, void* ws, size_t ws_bytes, void* stream) {
+    g_last_launches = 0;
+    const int rc = check_cache8(cache);
+    if (rc) return rc;
+    return read(cache, slot_map, T, dtype, 1, {k_out, k_token_stride, k_head_stride},
+                {v_out, v_token_stride, v_head_stride}, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -37,6 +37,50 @@ struct AppendParams {
     int64_t n_slots;
 };
 
+// Rotation of queries and keys, and the write of keys and values, by token
+// (rope.cu). Sources and destinations: 0 queries, 1 keys, 2 values.
+struct RotateParams {
+    const uint16_t* src[3];
+    int64_t src_token[3], src_head[3];
+    uint16_t* dst[2];  // rotated queries and (without a cache) keys
+    int64_t dst_token[2], dst_head[2];
+    int heads[3];
+    const int32_t* positions;         // null: no rotation
+    const unsigned long long* turns;  // of a pair's frequency, in 2^-64
+    float scale;
+    int rotary_dim, interleaved;
+    int T, head_dim;
+    int lanes, per;  // lanes of a head (16 elements each), heads that a warp takes at a time
+    int split;       // warps that share a token
+    // the cache that keys and values go to
+    const int32_t* slots;
+    uint8_t* cache[2];
+    uint8_t* cache_scale[2];  // e4m3 codes alone
+    int64_t cache_block[2], cache_token[2], cache_head[2];  // bytes
+    int block_size;
+    int64_t n_slots;
+    unsigned* ctrl;
+};
+// Where keys go.
+enum { kRotateRows = 0, kRotateCache16 = 1, kRotateCache8 = 2 };
+cudaError_t launch_rotate(RotateParams p, int to, int dtype, int sms, cudaStream_t stream);
+
+// Slots of a cache back into rows.
+struct ReadParams {
+    const uint8_t* cache[2];
+    const uint8_t* cache_scale[2];
+    int64_t cache_block[2], cache_token[2], cache_head[2];  // bytes
+    uint16_t* dst[2];
+    int64_t dst_token[2], dst_head[2];
+    const int32_t* slots;
+    unsigned* ctrl;
+    int T, heads, lane_shift;  // head_dim = 16 << lane_shift
+    int block_size, split;
+    int64_t n_slots;
+};
+// from: 0 a cache of 16 bits, 1 of e4m3 codes
+cudaError_t launch_read(ReadParams p, int from, int dtype, int sms, cudaStream_t stream);
+
 constexpr int kSampleThreads = 512;
 constexpr int kSampleMaxSlice = 45056;  // logits of a row that one CTA holds
 
