@@ -390,6 +390,37 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
                         const int32_t* q_start, const int32_t* seq_lens, int B, float scale, int window, void* out,
                         float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------- trees of drafted tokens
+ * A step may verify a tree of drafted tokens of each request instead of a
+ * chain: its new tokens lie packed and in the cache as ever (token i of request
+ * b in the slot of position ctx + i), and parents [T] names for each the one
+ * that it continues, by its place among the request's new tokens, -1 for the
+ * token before all of them. A token comes after its parent. A request of more
+ * than MOE_TREE_MAX_TOKENS new tokens (a prompt's chunk in the same step) is no
+ * tree: its parents are not read.
+ * moe_tree_plan gives for each token row the mask of the new tokens that it
+ * sees (bit i: token i; its own path up to the root) and its position, ctx
+ * plus its depth (positions may be NULL). Rows that are no tree's get all
+ * bits and consecutive positions, padding rows (from q_start[B] on) 0 and -1.
+ * q_start and seq_lens as moe_paged_plan gives them. A parent outside
+ * [-1, i) counts as -1 and is reported (MOE_EDEVICE_BAD_INDEX); so is a
+ * request that q_start or seq_lens place wrongly, whose rows are not written. */
+#define MOE_TREE_MAX_TOKENS 64
+int moe_tree_plan(const int32_t* parents, const int32_t* q_start, const int32_t* seq_lens, int B, int T, uint64_t* masks,
+                  int32_t* positions, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_paged_attention without a window, in which a row sees of its request's
+ * new tokens those whose bits are set in masks [T] (as from moe_tree_plan, or
+ * any others; bits of tokens after its own count as 0, those of requests of
+ * more than MOE_TREE_MAX_TOKENS new tokens are not read), and all tokens before
+ * them. A row that sees nothing gets out = 0, lse = -inf. To go on with an
+ * accepted path, read its slots (moe_paged_read) and append them to the
+ * consecutive ones. */
+int moe_paged_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int T, int q_heads,
+                             const moe_kv_cache* cache, const int32_t* block_tables, int max_blocks,
+                             const int32_t* q_start, const int32_t* seq_lens, const uint64_t* masks, int B, float scale,
+                             void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------- rotary positions
  * The first rotary_dim of a head's dimensions turn with the token's position
  * p, two at a time: pair i (i < rotary_dim / 2) is (x_i, x_(i + rotary_dim/2)),
@@ -493,6 +524,25 @@ int moe_paged_rope_append8(const void* q, int64_t q_token_stride, int64_t q_head
                            int64_t v_head_stride, int T, int dtype, const int32_t* positions, const int32_t* slot_map,
                            const moe_rope_angles* angles, const moe_kv_cache8* cache, void* ws, size_t ws_bytes,
                            void* stream);
+
+/* moe_paged_attention over such a cache, of bf16 (dtype 0) or fp16 (1) queries
+ * and outputs, in one launch; masks [T] of trees as for
+ * moe_paged_tree_attention, or NULL (with masks window is 0). What it says of
+ * scale, window, out, lse, padding, pages and bad tables holds here. Codes and
+ * powers of two are exact, queries are held in fp16 times a power of two of
+ * their row's own (exact down to 2^-28 of the row's largest), products are
+ * summed in fp32, and the softmax weights times the values' powers of two are
+ * rounded once to fp16, relative to the row's largest such weight. A key whose
+ * byte is 255 gives the rows that see it NaN, and may give NaN to the request's
+ * rows that do not see it yet. A request of any length is taken 32 rows (tokens
+ * times the heads that share a kv head) at a time: beyond some 256 rows it is
+ * faster to read its context back (moe_paged_read8) into a 16-bit cache for
+ * moe_paged_attention. ws: moe_paged_attention8_workspace_bytes. */
+size_t moe_paged_attention8_workspace_bytes(int q_heads, const moe_kv_cache8* cache);
+int moe_paged_attention8(const void* q, int64_t q_token_stride, int64_t q_head_stride, int T, int q_heads, int dtype,
+                         const moe_kv_cache8* cache, const int32_t* block_tables, int max_blocks, const int32_t* q_start,
+                         const int32_t* seq_lens, const uint64_t* masks, int B, float scale, int window, void* out,
+                         float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* Reads T slots back: k_out, v_out [T, kv_heads, head_dim] by their strides
  * (elements, multiples of 8, at least head_dim) get the keys and values of

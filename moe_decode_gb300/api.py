@@ -33,6 +33,7 @@ LM_HEAD_WORKSPACE_BYTES = 1024
 STATIC_SCRATCH_BYTES = 524288
 PAGED_WORKSPACE_BYTES = 1024
 PAGED_MAX_REQUESTS = 4096
+TREE_MAX_TOKENS = 64
 SAMPLE_MAX_VOCAB = 720896
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 DTYPES = {torch.bfloat16: 0, torch.float16: 1}
@@ -115,6 +116,11 @@ def _load():
     lib.moe_paged_rope_append.argtypes = [*rows, *rows, I32, *rows, *rows, I32, P, P, rp, cp, P, SZ, P]
     lib.moe_paged_rope_append8.argtypes = [*rows, *rows, I32, *rows, *rows, I32, I32, P, P, rp, c8, P, SZ, P]
     lib.moe_paged_append8.argtypes = [*rows, *rows, I32, I32, P, c8, P, SZ, P]
+    lib.moe_tree_plan.argtypes = [P, P, P, I32, I32, P, P, P, SZ, P]
+    lib.moe_paged_tree_attention.argtypes = [P, I64, I64, I32, I32, cp, P, I32, P, P, P, I32, F32, P, P, P, SZ, P]
+    lib.moe_paged_attention8_workspace_bytes.argtypes = [I32, c8]
+    lib.moe_paged_attention8_workspace_bytes.restype = SZ
+    lib.moe_paged_attention8.argtypes = [P, I64, I64, I32, I32, I32, c8, P, I32, P, P, P, I32, F32, I32, P, P, P, SZ, P]
     lib.moe_paged_read.argtypes = [cp, P, I32, *rows, *rows, P, SZ, P]
     lib.moe_paged_read8.argtypes = [c8, P, I32, I32, *rows, *rows, P, SZ, P]
     lib.moe_last_launch_count.argtypes = []
@@ -123,7 +129,7 @@ def _load():
               "moe_lm_head", "moe_fp8_quantize", "moe_fp8_dequant", "moe_transpose_down",
               "moe_paged_plan", "moe_paged_append", "moe_paged_attention", "moe_sample", "moe_rope_table", "moe_rope_turns",
               "moe_rope", "moe_paged_rope_append", "moe_paged_rope_append8", "moe_paged_append8", "moe_paged_read",
-              "moe_paged_read8"):
+              "moe_paged_read8", "moe_tree_plan", "moe_paged_tree_attention", "moe_paged_attention8"):
         getattr(lib, f).restype = I32
     return lib
 
@@ -392,11 +398,11 @@ class KvCache8:
         return cls(k, v, ks, vs)
 
 
-def paged_workspace(q_heads: int = 0, cache: Optional[KvCache] = None, device="cuda", stream=None) -> torch.Tensor:
+def paged_workspace(q_heads: int = 0, cache: "Optional[KvCache | KvCache8]" = None, device="cuda", stream=None) -> torch.Tensor:
     """A zeroed workspace for the paged-step calls: for paged_attention with
-    q_heads over `cache`, or, without them, for paged_plan and paged_append."""
-    n = PAGED_WORKSPACE_BYTES if cache is None else int(
-        lib.moe_paged_attention_workspace_bytes(q_heads, cache._ref))
+    q_heads over `cache`, or, without them, for the other calls."""
+    need = lib.moe_paged_attention8_workspace_bytes if isinstance(cache, KvCache8) else lib.moe_paged_attention_workspace_bytes
+    n = PAGED_WORKSPACE_BYTES if cache is None else int(need(q_heads, cache._ref))
     _want(n > 0, "moe_paged_attention_workspace_bytes", ESHAPE)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     workspace_init(ws, stream)
@@ -421,6 +427,22 @@ def paged_plan(ctx_lens, new_lens, free_list, block_tables, block_size: int, q_s
                             taken.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc:
         raise MoeError(rc, "moe_paged_plan")
+
+
+def tree_plan(parents, q_start, seq_lens, masks, positions, ws, stream=None):
+    """Masks int64 [T] and positions int32 [T] (or None) of trees of drafted
+    tokens from parents int32 [T] (moe_tree_plan): each token's parent among its
+    request's new tokens, -1 for the token before them; q_start int32 [B + 1],
+    seq_lens int32 [B] as paged_plan gives them."""
+    T, B = parents.numel(), seq_lens.numel()
+    dev = _device("tree_plan", parents)
+    _vectors("tree_plan: parents, q_start, seq_lens, positions", dev, torch.int32, (parents, T), (q_start, B + 1), (seq_lens, B), (positions, T))
+    _vectors("tree_plan: masks", dev, torch.int64, (masks, T))
+    _workspace("tree_plan", dev, ws)
+    rc = lib.moe_tree_plan(parents.data_ptr(), q_start.data_ptr(), seq_lens.data_ptr(), B, T, masks.data_ptr(), _raw(positions),
+                           ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise MoeError(rc, "moe_tree_plan")
 
 
 def _strides(t: torch.Tensor, least: int = 0):
@@ -602,35 +624,51 @@ def paged_read(cache, slot_map, k_out, v_out, ws, stream=None):
         raise MoeError(rc, "moe_paged_read8" if codes else "moe_paged_read")
 
 
-def paged_attention(q, cache: KvCache, block_tables, q_start, seq_lens, out, ws, lse=None, scale: float = 0.0,
-                    window: int = 0, stream=None):
+def paged_attention(q, cache, block_tables, q_start, seq_lens, out, ws, lse=None, scale: float = 0.0,
+                    window: int = 0, stream=None, tree_masks=None):
     """Attention of the step's tokens q [T, q_heads, head_dim] over the paged
-    cache (moe_paged_attention): out [T, q_heads, head_dim] contiguous, lse
-    fp32 [T, q_heads] or None; block_tables int32 [B, W], q_start int32
-    [B + 1], seq_lens int32 [B] as paged_plan gives them; window > 0: only the
-    last `window` keys; scale <= 0: 1 / sqrt(head_dim)."""
+    cache (moe_paged_attention; moe_paged_attention8 over a KvCache8, of bf16 or
+    fp16 queries): out [T, q_heads, head_dim] contiguous, lse fp32 [T, q_heads]
+    or None; block_tables int32 [B, W], q_start int32 [B + 1], seq_lens int32
+    [B] as paged_plan gives them; window > 0: only the last `window` keys;
+    scale <= 0: 1 / sqrt(head_dim). tree_masks int64 [T] from tree_plan: of its
+    request's new tokens a row sees those that its mask names
+    (moe_paged_tree_attention; without a window)."""
     T, heads, d = q.shape
     B = seq_lens.numel()
+    codes = isinstance(cache, KvCache8)
+    dtype = q.dtype if codes else cache.dtype
     _want(d == cache.head_dim and out.shape == q.shape, "paged_attention: q, out [T, q_heads, head_dim]", ESHAPE)
     dev = _device("paged_attention", q)
-    _want(q.dtype == cache.dtype and out.dtype == cache.dtype and q.stride(2) == 1 and out.is_contiguous()
+    _want(q.dtype == dtype and dtype in DTYPES and out.dtype == dtype and q.stride(2) == 1 and out.is_contiguous()
           and q.get_device() == out.get_device() == cache.device_index == dev,
-          "paged_attention: q, out of the cache's dtype, all on the current device")
+          "paged_attention: q, out of the cache's dtype (KvCache8: bf16 or fp16), all on the current device")
     _want(block_tables.dim() == 2 and block_tables.shape[0] == B, "paged_attention: block_tables int32 [B, W]")
     _vectors("paged_attention: block_tables, q_start, seq_lens", dev, torch.int32, (block_tables, None), (q_start, B + 1),
              (seq_lens, B))
     _vectors("paged_attention: lse", dev, torch.float32, (lse, T * heads))
+    _vectors("paged_attention: tree_masks", dev, torch.int64, (tree_masks, T))
+    _want(tree_masks is None or window == 0, "paged_attention: tree_masks and a window", ESHAPE)
     _workspace("paged_attention", dev, ws)
     qt, qh, _ = q.stride()
     if T == 1:
         qt = 0
     if heads == 1:
         qh = 0
-    rc = lib.moe_paged_attention(q.data_ptr(), qt, qh, T, heads, cache._ref, block_tables.data_ptr(),
-                                 block_tables.shape[1], q_start.data_ptr(), seq_lens.data_ptr(), B, scale, window,
-                                 out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    queries = (q.data_ptr(), qt, qh, T, heads)
+    step = (cache._ref, block_tables.data_ptr(), block_tables.shape[1], q_start.data_ptr(), seq_lens.data_ptr())
+    rest = (out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    if codes:
+        name = "moe_paged_attention8"
+        rc = lib.moe_paged_attention8(*queries, DTYPES[dtype], *step, _raw(tree_masks), B, scale, window, *rest)
+    elif tree_masks is not None:
+        name = "moe_paged_tree_attention"
+        rc = lib.moe_paged_tree_attention(*queries, *step, tree_masks.data_ptr(), B, scale, *rest)
+    else:
+        name = "moe_paged_attention"
+        rc = lib.moe_paged_attention(*queries, *step, B, scale, window, *rest)
     if rc:
-        raise MoeError(rc, "moe_paged_attention")
+        raise MoeError(rc, name)
 
 
 _LOGITS = {torch.float32: 0, torch.bfloat16: 1}

@@ -18,7 +18,7 @@ OUT = os.path.join(HERE, "libmoe_decode.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "layer_bf16.cu", "layer_mxfp4.cu", "layer_fp8.cu", "layer_splitk.cu", "lm_head.cu",
            "api_paged.cu", "api_paged8.cu", "paged_cache.cu", "rope.cu", "sample.cu", "attn_decode.cu",
-           "attn_chunk.cu"]
+           "attn_chunk.cu", "attn_codes.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

@@ -1,8 +1,10 @@
-// C ABI of rotary positions, of the paged cache of 8-bit values and of reading
-// slots back: argument checking and launch configuration. Declarations and the
+// C ABI of rotary positions, of the paged cache of 8-bit values (write, reading
+// back, attention) and of reading slots back: argument checking and launch configuration. Declarations and the
 // contract of every entry point are in include/moe_decode.h.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -17,11 +19,14 @@ namespace {
 using moe::DeviceInfo;
 using moe::aligned16;
 using moe::aligned4;
+using moe::aligned8;
 using moe::check_cache;
 using moe::check_cache8;
 using moe::check_ws;
 using moe::device_info;
+using moe::encode_tiled;
 using moe::g_last_launches;
+using moe::g_opt;
 using moe::launched;
 using moe::stride_ok;
 
@@ -34,8 +39,6 @@ uint64_t turns_of(double radians) {
     const double units = std::nearbyint(std::ldexp(t, 64));
     return units >= 18446744073709551616.0 ? 0u : static_cast<uint64_t>(units);
 }
-
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 int check_angles(const moe_rope_angles* a, int head_dim) {
     if (!a || !a->turns) return MOE_EINVAL;
@@ -185,6 +188,19 @@ int read(const Cache* cache, const int32_t* slot_map, int T, int dtype, int from
     return launched(moe::launch_read(p, from, dtype, dev.sms, static_cast<cudaStream_t>(stream)), 1);
 }
 
+// Tensor map of a cache of codes: (dimensions, token of the block, head, block),
+// boxes of all dimensions of `box` tokens, swizzled by the dimensions' width.
+bool codes_map(CUtensorMap* m, const moe_kv_cache8* c, void* base, int64_t bs, int64_t ts, int64_t hs, int box) {
+    const moe::EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->block_size, (cuuint64_t)c->kv_heads, (cuuint64_t)c->n_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)ts, (cuuint64_t)hs, (cuuint64_t)bs};
+    const cuuint32_t boxes[4] = {(cuuint32_t)c->head_dim, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -321,6 +337,80 @@ int moe_paged_read8(const moe_kv_cache8* cache, const int32_t* slot_map, int T, 
     if (rc) return rc;
     return read(cache, slot_map, T, dtype, 1, {k_out, k_token_stride, k_head_stride},
                 {v_out, v_token_stride, v_head_stride}, ws, ws_bytes, stream);
+}
+
+size_t moe_paged_attention8_workspace_bytes(int q_heads, const moe_kv_cache8* cache) {
+    if (check_cache8(cache) != MOE_OK) return 0;
+    if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 32) return 0;
+    return MOE_PAGED_WORKSPACE_BYTES + MOE_MAX_GRID * sizeof(unsigned) +
+           (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows, cache->head_dim) * sizeof(float);
+}
+
+int moe_paged_attention8(const void* q, int64_t q_token_stride, int64_t q_head_stride, int T, int q_heads, int dtype,
+                         const moe_kv_cache8* cache, const int32_t* block_tables, int max_blocks, const int32_t* q_start,
+                         const int32_t* seq_lens, const uint64_t* masks, int B, float scale, int window, void* out,
+                         float* lse, void* ws, size_t ws_bytes, void* stream) {
+    g_last_launches = 0;
+    int rc = check_cache8(cache);
+    if (rc) return rc;
+    if (dtype != 0 && dtype != 1) return MOE_ESHAPE;
+    if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 32) return MOE_ESHAPE;
+    const int group = q_heads / cache->kv_heads;
+    if (T < 0 || (int64_t)T * group >= (1 << 28)) return MOE_ESHAPE;
+    if (B < 1 || B > MOE_PAGED_MAX_REQUESTS || max_blocks < 1 || window < 0 || (masks && window > 0)) return MOE_ESHAPE;
+    if (!(scale == scale) || std::isinf(scale)) return MOE_EINVAL;
+    if (!block_tables || !q_start || !seq_lens) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!out) return MOE_EINVAL;
+    rc = check_rows({q, q_token_stride, q_head_stride});
+    if (rc) return rc;
+    if (!aligned16(out) || !aligned4(lse) || !aligned4(block_tables) || !aligned4(q_start) || !aligned4(seq_lens) ||
+        !aligned8(masks))
+        return MOE_EALIGN;
+    rc = check_ws(ws, ws_bytes, moe_paged_attention8_workspace_bytes(q_heads, cache));
+    if (rc) return rc;
+    DeviceInfo dev;
+    rc = device_info(&dev);
+    if (rc) return rc;
+    moe::AttnParams p = {};
+    p.G = g_opt.grid_ctas > 0 ? g_opt.grid_ctas : std::min(dev.sms, MOE_MAX_GRID);
+    if (p.G > dev.sms || p.G > MOE_MAX_GRID) return MOE_EINVAL;
+    p.q = static_cast<const uint16_t*>(q);
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.tables = block_tables;
+    p.q_start = q_start;
+    p.seq = seq_lens;
+    p.ctrl = static_cast<unsigned*>(ws);
+    p.arrived = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + MOE_PAGED_WORKSPACE_BYTES);
+    p.part = reinterpret_cast<float*>(p.arrived + MOE_MAX_GRID);
+    p.q_token = q_token_stride;
+    p.q_head = q_head_stride;
+    p.T = T;
+    p.B = B;
+    p.heads = q_heads;
+    p.kv_heads = cache->kv_heads;
+    p.group = group;
+    p.group_magic = ((1ull << 36) + group - 1) / group;
+    p.max_blocks = max_blocks;
+    p.block_size = cache->block_size;
+    p.n_blocks = cache->n_blocks;
+    // copies of the largest power of two that divides the block: none ends
+    // beyond a block, and a tile is a whole number of them
+    p.box_shift = std::min(__builtin_ctz((unsigned)cache->block_size), 7);
+    p.box = 1 << p.box_shift;
+    p.window = window;
+    p.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)cache->head_dim)) * 1.44269504088896341f;
+    p.timeout_ns = (unsigned long long)g_opt.timeout_ns;
+    p.hold_back = g_opt.hold_back ? 1 : 0;
+    p.tree = reinterpret_cast<const unsigned long long*>(masks);
+    p.scales[0] = cache->k_scale;
+    p.scales[1] = cache->v_scale;
+    CUtensorMap k_map, v_map;
+    if (!codes_map(&k_map, cache, cache->k, cache->k_block_stride, cache->k_token_stride, cache->k_head_stride, p.box) ||
+        !codes_map(&v_map, cache, cache->v, cache->v_block_stride, cache->v_token_stride, cache->v_head_stride, p.box))
+        return MOE_ECUDA;
+    return launched(moe::launch_attn_codes(p, &k_map, &v_map, cache->head_dim, dtype, static_cast<cudaStream_t>(stream)), 1);
 }
 
 }  // extern "C"

@@ -110,7 +110,9 @@ __device__ constexpr uint32_t product(uint32_t n, bool across) {
            ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-template <int D, int DT>
+// TREE: as in the kernel of few rows; a row's mask is laid over the tile's keys as
+// four words.
+template <int D, int DT, bool TREE>
 __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_constant__ AttnParams p,
                                                                   const __grid_constant__ CUtensorMap kmap,
                                                                   const __grid_constant__ CUtensorMap vmap) {
@@ -319,6 +321,8 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             // keys that the row sees, and that all or any rows of the slot see
             const RowKeys sees = attn_row_keys(walk, slot * kSlotRows + row);
             const AllKeys all = attn_all_keys(walk, slot * kSlotRows, slot * kSlotRows + slot_rows);
+            const Tree tree = attn_tree<TREE>(walk);
+            const unsigned long long mask = TREE ? attn_tree_mask(walk, tree, slot * kSlotRows + row) : ~0ull;
             float m = -INFINITY;  // reference of the weights, in log2
             float l = 0.f;
             for (int j = 0; j < n; ++j) {
@@ -334,6 +338,15 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         if (key0 + i > sees.last || key0 + i < sees.from) s[i] = 0xff800000u;  // -inf
+                }
+                if (TREE && tree.reaches(key0, kAttnTile)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t bits = attn_tree_bits(tree, mask, key0 + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((bits >> i) & 1u)) s[32 * c + i] = 0xff800000u;
+                    }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -471,9 +484,9 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     }
 }
 
-template <int D, int DT>
+template <int D, int DT, bool TREE>
 cudaError_t launch_typed(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
-    auto* kern = attn_chunk_kernel<D, DT>;
+    auto* kern = attn_chunk_kernel<D, DT, TREE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkShape<D>::kBytes);
     if (e != cudaSuccess) return e;
     // the warpgroups' shares wait for ever where the launch brings fewer
@@ -500,8 +513,12 @@ cudaError_t launch_attn_chunk(const AttnParams& p, const void* k_map, const void
                               cudaStream_t stream) {
     const CUtensorMap& k = *static_cast<const CUtensorMap*>(k_map);
     const CUtensorMap& v = *static_cast<const CUtensorMap*>(v_map);
-    if (head_dim == 128) return dtype == 0 ? launch_typed<128, 0>(p, k, v, stream) : launch_typed<128, 1>(p, k, v, stream);
-    return dtype == 0 ? launch_typed<64, 0>(p, k, v, stream) : launch_typed<64, 1>(p, k, v, stream);
+    if (p.tree) {
+        if (head_dim == 128) return dtype == 0 ? launch_typed<128, 0, true>(p, k, v, stream) : launch_typed<128, 1, true>(p, k, v, stream);
+        return dtype == 0 ? launch_typed<64, 0, true>(p, k, v, stream) : launch_typed<64, 1, true>(p, k, v, stream);
+    }
+    if (head_dim == 128) return dtype == 0 ? launch_typed<128, 0, false>(p, k, v, stream) : launch_typed<128, 1, false>(p, k, v, stream);
+    return dtype == 0 ? launch_typed<64, 0, false>(p, k, v, stream) : launch_typed<64, 1, false>(p, k, v, stream);
 }
 
 }  // namespace moe

@@ -66,7 +66,11 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
 // pages of 16) 174 us, 5.9 TB/s in the kernel. Four warps with 32 rows each took 206 us there: the second set of
 // warps hides the first's chains. Short histories are bound by latency: one
 // token over 1,001 keys takes 11.2 us.
-template <int D, int DT>
+//
+// TREE: rows see of their request's new tokens those that their masks name. Only
+// the last tiles of an item look at the masks; a kernel without is compiled as
+// before.
+template <int D, int DT, bool TREE>
 __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_constant__ AttnParams p,
                                                                    const __grid_constant__ CUtensorMap kmap,
                                                                    const __grid_constant__ CUtensorMap vmap) {
@@ -196,6 +200,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
             from[b] = k.from;
         }
         const AllKeys all = attn_all_keys(walk, 0, walk.rows);
+        const Tree tree = attn_tree<TREE>(walk);
+        unsigned long long mask[2] = {~0ull, ~0ull};
+        if (TREE)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) mask[b] = attn_tree_mask(walk, tree, set * 16 + b * 8 + quad);
         float o[D / 8][4];
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -251,6 +260,13 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
                             const int key = key0 + i * 8 + 2 * pair + (j & 1);
                             if (key > last[j >> 1] || key < from[j >> 1]) s[i][j] = -INFINITY;
                         }
+                }
+                if (TREE && tree.reaches(key0, kWarpKeys)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (attn_tree_hides(tree, mask[j >> 1], key0 + i * 8 + 2 * pair + (j & 1))) s[i][j] = -INFINITY;
                 }
                 uint32_t pa[2][4];
 #pragma unroll
@@ -427,9 +443,9 @@ cudaError_t launch(void (*kern)(Args...), dim3 grid, int threads, int smem, cuda
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, int DT>
+template <int D, int DT, bool TREE>
 cudaError_t launch_typed(const AttnParams& p, const CUtensorMap* maps, cudaStream_t stream, int* launches) {
-    cudaError_t e = launch(attn_decode_kernel<D, DT>, dim3((unsigned)p.G), kThreads, DecodeShape<D>::kBytes, stream, p,
+    cudaError_t e = launch(attn_decode_kernel<D, DT, TREE>, dim3((unsigned)p.G), kThreads, DecodeShape<D>::kBytes, stream, p,
                            maps[0], maps[1]);
     if (e != cudaSuccess) return e;
     ++*launches;
@@ -446,8 +462,14 @@ cudaError_t launch_attn(const AttnParams& p, const void* maps, int head_dim, int
                         int* launches) {
     const CUtensorMap* m = static_cast<const CUtensorMap*>(maps);
     *launches = 0;
-    if (head_dim == 128) return dtype == 0 ? launch_typed<128, 0>(p, m, stream, launches) : launch_typed<128, 1>(p, m, stream, launches);
-    return dtype == 0 ? launch_typed<64, 0>(p, m, stream, launches) : launch_typed<64, 1>(p, m, stream, launches);
+    if (p.tree) {
+        if (head_dim == 128)
+            return dtype == 0 ? launch_typed<128, 0, true>(p, m, stream, launches) : launch_typed<128, 1, true>(p, m, stream, launches);
+        return dtype == 0 ? launch_typed<64, 0, true>(p, m, stream, launches) : launch_typed<64, 1, true>(p, m, stream, launches);
+    }
+    if (head_dim == 128)
+        return dtype == 0 ? launch_typed<128, 0, false>(p, m, stream, launches) : launch_typed<128, 1, false>(p, m, stream, launches);
+    return dtype == 0 ? launch_typed<64, 0, false>(p, m, stream, launches) : launch_typed<64, 1, false>(p, m, stream, launches);
 }
 
 }  // namespace moe

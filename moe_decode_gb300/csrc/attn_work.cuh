@@ -125,6 +125,11 @@ struct Few {
         return q.n > 0 && q.n * p.group <= kAttnFewRows;
     }
 };
+// (over a cache of 8-bit values one kernel takes every request)
+struct All {
+    static constexpr int kRows = kAttnRows, kItem = 2;
+    static __device__ __forceinline__ bool mine(const AttnParams& p, const Request& q) { return q.n > 0; }
+};
 struct Many {
     static constexpr int kRows = kAttnChunkRows, kItem = 2;
     static __device__ __forceinline__ bool mine(const AttnParams& p, const Request& q) {
@@ -246,6 +251,35 @@ template <class W>
 __device__ __forceinline__ AllKeys attn_all_keys(const W& walk, int from, int to) {
     return AllKeys{min(walk.q.pos0 + token_of(walk.p, walk.row0 + from) + 1, walk.hi),
                    first_seen(walk.p, walk.q.pos0 + token_of(walk.p, walk.row0 + to - 1))};
+}
+// The new tokens of a tree (a request of up to kTreeTokens new tokens, in a
+// call with masks): keys from `from` on are seen where the row's mask says so,
+// and no later one than the row's own, so that the division of the work, made
+// for rows that see all before them, holds.
+struct Tree {
+    int from;  // no key is as far where there is no tree
+    __device__ __forceinline__ bool reaches(int key, int n) const { return key > from - n; }
+};
+template <bool TREE, class W>
+__device__ __forceinline__ Tree attn_tree(const W& walk) {
+    return Tree{TREE && walk.q.n <= kTreeTokens ? walk.q.pos0 : 0x7fffffff};
+}
+template <class W>
+__device__ __forceinline__ unsigned long long attn_tree_mask(const W& walk, const Tree& tree, int row) {
+    if (tree.from == 0x7fffffff) return ~0ull;
+    return __ldcg(walk.p.tree + walk.q.q0 + token_of(walk.p, walk.row0 + min(row, walk.rows - 1)));
+}
+// Whether a mask hides a key that is no later than its row's own.
+__device__ __forceinline__ bool attn_tree_hides(const Tree& tree, unsigned long long mask, int key) {
+    return key >= tree.from && !((mask >> (min(key - tree.from, kTreeTokens - 1))) & 1u);
+}
+// The 32 keys from `key` on that a mask lets through, as bits (of keys after the
+// row's own any bit).
+__device__ __forceinline__ uint32_t attn_tree_bits(const Tree& tree, unsigned long long mask, int key) {
+    const int at = key - tree.from;  // of the first of them
+    if (at <= -32) return ~0u;
+    if (at < 0) return ((uint32_t)mask << -at) | ((1u << -at) - 1);
+    return at < kTreeTokens ? (uint32_t)(mask >> at) : 0u;
 }
 // Of the keys [key, key + n) (key >= 0): whether the item needs any, and
 // whether there are some that it does not.

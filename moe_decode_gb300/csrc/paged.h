@@ -25,6 +25,16 @@ struct PlanParams {
     int B, n_free, max_blocks, block_size, T;
 };
 
+struct TreeParams {
+    const int32_t* parents;
+    const int32_t* q_start;
+    const int32_t* seq;
+    unsigned long long* masks;
+    int32_t* positions;  // may be null
+    unsigned* ctrl;
+    int B, T;
+};
+
 struct AppendParams {
     const uint16_t* src[2];  // new keys, new values
     uint16_t* dst[2];        // the cache's K and V
@@ -128,7 +138,12 @@ struct AttnParams {
     float scale_log2;  // scale * log2(e)
     unsigned long long timeout_ns;
     int hold_back;  // test hook: 1, a CTA's first keys (scores, in the chunk kernel) never come
+    // Trees of drafted tokens (null: none): of each token row the new tokens of
+    // its request that it sees, where the request has at most kTreeTokens.
+    const unsigned long long* tree;
+    const uint8_t* scales[2];  // of K and V of a cache of 8-bit values
 };
+constexpr int kTreeTokens = 64;
 
 // Whether any request of the call may have many rows.
 inline bool attn_may_chunk(const AttnParams& p) { return (int64_t)p.T * p.group > kAttnFewRows; }
@@ -140,10 +155,15 @@ cudaError_t launch_attn(const AttnParams& p, const void* maps, int head_dim, int
                         int* launches);
 cudaError_t launch_attn_chunk(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
                               cudaStream_t stream);
+// Over a cache of 8-bit values: maps of K and V whose boxes hold all dimensions
+// of `box` keys.
+cudaError_t launch_attn_codes(const AttnParams& p, const void* k_map, const void* v_map, int head_dim, int dtype,
+                              cudaStream_t stream);
 // Floats of one partial result of `rows` rows.
 constexpr int attn_part_floats(int rows, int head_dim) { return rows * (head_dim + 2); }
 
 cudaError_t launch_paged_plan(const PlanParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_tree_plan(const TreeParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_paged_append(const AppendParams& p, int sms, cudaStream_t stream);
 // Chooses p.C and p.slice.
 cudaError_t launch_sample(SampleParams p, int M, int dtype, cudaStream_t stream);

@@ -1,6 +1,7 @@
 // Bookkeeping of a paged KV cache for one step: block tables, slot map and
 // positions from the requests' lengths (moe_paged_plan), and the write of the
-// step's keys and values through the slot map (moe_paged_append).
+// step's keys and values through the slot map (moe_paged_append); masks and
+// positions of trees of drafted tokens (moe_tree_plan).
 #include "layer_params.h"
 #include "paged.h"
 #include "ptx.cuh"
@@ -165,6 +166,70 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanParams p) 
     if (over) report(p.ctrl, -102 /* MOE_EDEVICE_OVERFLOW */);
 }
 
+// A request a block of 64 threads, a thread a token: each keeps the tokens on its
+// path that it knows of and the token above them, and takes both from that one in
+// turn, so that six rounds reach 64 tokens up.
+constexpr int kTreeThreads = kTreeTokens;
+__global__ __launch_bounds__(kTreeThreads) void tree_plan_kernel(TreeParams p) {
+    __shared__ unsigned long long path[kTreeTokens];
+    __shared__ int up[kTreeTokens];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x;
+    bool bad = false;
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const int q0 = p.q_start[b], q1 = p.q_start[b + 1], seq = p.seq[b];
+        if (q0 < 0 || q1 < q0 || q1 > p.T || seq < 0) {
+            bad = true;
+            continue;
+        }
+        const int n = q1 - q0, pos0 = seq - n;
+        if (n > kTreeTokens) {  // not a tree: each token sees all before it
+            for (int i = tid; i < n; i += kTreeThreads) {
+                p.masks[q0 + i] = ~0ull;
+                if (p.positions) p.positions[q0 + i] = pos0 + i;
+            }
+            continue;
+        }
+        unsigned long long mine = 0;
+        int at = -1;
+        if (tid < n) {
+            at = p.parents[q0 + tid];
+            if (at < -1 || at >= tid) {
+                bad = true;
+                at = -1;
+            }
+            mine = 1ull << tid;
+        }
+        path[tid] = mine;
+        up[tid] = at;
+        __syncthreads();
+#pragma unroll
+        for (int round = 0; round < 6; ++round) {
+            unsigned long long more = 0;
+            int next = -1;
+            if (at >= 0) {
+                more = path[at];
+                next = up[at];
+            }
+            __syncthreads();
+            path[tid] = mine |= more;
+            up[tid] = at = next;
+            __syncthreads();
+        }
+        if (tid < n) {
+            p.masks[q0 + tid] = mine;
+            if (p.positions) p.positions[q0 + tid] = pos0 + __popcll(mine) - 1;
+        }
+    }
+    // padding rows
+    for (int64_t t = (int64_t)max(p.q_start[p.B], 0) + blockIdx.x * kTreeThreads + tid; t < p.T; t += (int64_t)gridDim.x * kTreeThreads) {
+        p.masks[t] = 0;
+        if (p.positions) p.positions[t] = -1;
+    }
+    if (bad) report(p.ctrl, -100 /* MOE_EDEVICE_BAD_INDEX */);
+}
+
 // One warp a token: its lanes take the token's 16-byte pieces, keys and
 // values in the same round, four rounds unrolled (16 KB of a token of 8 heads
 // of 128 in flight a warp). Bound by HBM: 8,192 tokens of 8 heads of 128 take
@@ -231,6 +296,10 @@ cudaError_t launch_paged_plan(const PlanParams& p, int sms, cudaStream_t stream)
     const int64_t want = ((int64_t)p.T + kPlanThreads - 1) / kPlanThreads;
     const int grid = (int)(want < 1 ? 1 : want > sms ? sms : want);
     return launch_pdl(paged_plan_kernel, grid, kPlanThreads, p, stream);
+}
+
+cudaError_t launch_tree_plan(const TreeParams& p, int sms, cudaStream_t stream) {
+    return launch_pdl(tree_plan_kernel, p.B < 8 * sms ? p.B : 8 * sms, kTreeThreads, p, stream);
 }
 
 cudaError_t launch_paged_append(const AppendParams& p, int sms, cudaStream_t stream) {

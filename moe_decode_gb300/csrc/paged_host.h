@@ -11,6 +11,8 @@ namespace moe {
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
 inline int check_ws(const void* ws, size_t ws_bytes, size_t need) {
     if (!ws) return MOE_EWORKSPACE;
     if (!aligned16(ws)) return MOE_EALIGN;

@@ -78,3 +78,57 @@ def rotate(x, positions, turns, rotary_dim, interleaved, scale):
     mag[..., first] = mag[..., second] = (a.abs() + b.abs()) * abs(scale)
     real = (positions >= 0)[:, None, None]
     return torch.where(real, y, x), mag
+
+
+def make_step8(api, lens, page, heads, kv_heads, d, dtype, seed, layout="bthd", window=0, pad=0, spread=(1.0, 1.0)):
+    """Inputs of paged_attention over a KvCache8 for requests lens = [(seq, new), ...]: tokens of sizes 2^normal(0, spread) in keys and
+    values; what no row may read is poisoned (codes of NaN, byte 255, table entries -1). k and v hold the values in 64 bits."""
+    rs = np.random.RandomState(seed)
+    pages = [max(0, -(-s // page)) for s, _ in lens]
+    n_blocks = sum(pages) + 3
+    order = rs.permutation(n_blocks)
+    cache = make_cache8(api, n_blocks, page, kv_heads, d, layout)
+    cache.k.fill_(0x7F)
+    cache.v.fill_(0xFF)
+    cache.k_scale.fill_(255)
+    cache.v_scale.fill_(255)
+    table = np.full((len(lens), max(max(pages), 1)), -1, np.int32)
+    held = np.zeros((n_blocks, page), bool)
+    at = 0
+    for b, (s, n) in enumerate(lens):
+        table[b, : pages[b]] = order[at:at + pages[b]]
+        at += pages[b]
+        gone = max(0, s - n - window + 1) // page if window else 0
+        for i in range(gone, pages[b]):
+            held[table[b, i], : min(page, s - i * page)] = True
+        table[b, :gone] = -1
+    values = []
+    for x, scale, by in ((cache.k, cache.k_scale, spread[0]), (cache.v, cache.v_scale, spread[1])):
+        v = rs.randn(n_blocks, page, kv_heads, d) * 2.0 ** (rs.randn(n_blocks, page, kv_heads, 1) * by)
+        codes, byte = quantise(v)
+        on = torch.from_numpy(held).cuda()
+        x[on] = torch.from_numpy(codes).cuda()[on]
+        scale.transpose(1, 2)[on] = torch.from_numpy(byte).cuda()[on]
+        values.append(torch.from_numpy(dequantise(codes, byte)).cuda())
+    starts = np.concatenate([[0], np.cumsum([n for _, n in lens])]).astype(np.int32)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    q = torch.empty((int(starts[-1]) + pad, heads, d), dtype=dtype, device="cuda").normal_(generator=g)
+    return dict(q=q, cache=cache, k=values[0], v=values[1], table=torch.from_numpy(table).cuda(), q_start=torch.from_numpy(starts).cuda(),
+                seq=torch.tensor([s for s, _ in lens], dtype=torch.int32, device="cuda"), lens=lens, window=window)
+
+
+def check_attention8(out, lse, ref, most_keys, what=""):
+    """Each weight is rounded once to fp16 (half a step, 2^-11 of it), the output once to its type; scores, exponentials and sums are in
+    fp32 (2^-14 of the sum of magnitudes, as over a 16-bit cache). Below 2^-14 a weight's step is absolute, 2^-25 where the row's largest
+    (weight times power of two of the values, which `mag` holds at least half of in its largest element) is at least 2^11: 448 * 2^-36 of
+    it for each of the keys."""
+    o, z, mag = ref
+    half = torch.finfo(out.dtype).eps / 2
+    tol = (2.0 ** -11 + 2.0 ** -14) * mag + half * o.abs() + torch.finfo(out.dtype).tiny * half * 2
+    tol = tol + most_keys * 2.0 ** -27 / 224 * mag.amax(-1, keepdim=True)
+    err = (out.double() - o).abs()
+    assert torch.isfinite(out).all(), what
+    assert (err <= tol).all(), (what, float((err / tol.clamp_min(1e-300)).max()))
+    if lse is not None:
+        assert torch.equal(lse.isinf(), z.isinf()), what
+        assert (torch.where(z.isinf(), 0.0, lse.double() - z).abs() <= 2.0 ** -13).all(), what
