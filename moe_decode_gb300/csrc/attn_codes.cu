@@ -11,6 +11,8 @@
 // type. The second one's weights are 2^(x_j + ev_j - w) with a reference w of
 // their own, by the largest x + ev of the row: rounded once to fp16, they keep
 // their 11 bits however the values' exponents differ.
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace moe {
@@ -18,7 +20,8 @@ namespace {
 
 constexpr int kRows = kAttnRows;
 constexpr int kConsumers = 8;
-constexpr int kThreads = 384;  // two warpgroups of consumers, one for the producer
+constexpr int kThreads = 384;  // two warpgroups of consumers, one of producers
+constexpr int kLoaders = 3;    // warps that bring tiles, in turn; a fourth brings queries
 // Sums of 32 rows of 128 dimensions are 128 registers of a thread: the consumers
 // take registers from the third warpgroup. Together exactly what the block is
 // launched with.
@@ -30,6 +33,9 @@ static_assert(kWarpKeys == 16, "one step of the second product");
 // A weight is at most 2^15, the least that is held 2^-24: 2^-35 of the largest
 // when that has just become the reference, and 2^-39 before the next.
 constexpr float kBias = 11.f, kLimit = 15.f;
+// A reference before the first key: below any score, and finite, so that a score
+// of -inf has the weight 0 by it.
+constexpr float kNone = -3e38f;
 
 template <int D>
 struct CodesShape {
@@ -41,12 +47,12 @@ struct CodesShape {
     static constexpr int kMerge = kRows * D * 4;
     static constexpr int kOffScale = kStages * kStage;  // of a stage: the bytes of K, then of V
     static constexpr int kOffQ = kOffScale + kStages * 2 * kAttnTile;
-    static constexpr int kOffMerge = kOffQ + 2 * kQ;        // two sums of warps
-    static constexpr int kOffStat = kOffMerge + 2 * kMerge;  // largest score and sum of each warp's rows
+    static constexpr int kOffMerge = kOffQ + 2 * kQ;
+    static constexpr int kOffStat = kOffMerge + kMerge;  // largest score and sum of each warp's rows
     static constexpr int kOffRow = kOffStat + kConsumers * kRows * 8;  // powers of two of the queries
     static constexpr int kOffBar = kOffRow + kRows * 4;
     static constexpr int kOffMisc = kOffBar + 16 * (kStages + 2);
-    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + (int)sizeof(Start) + 16;
+    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + (int)sizeof(Start) + 16 + 4 * kLoaders;
     static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -60,6 +66,13 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
+}
+// The transpose of an 8 x 8 tile of 16-bit elements: thread l gives row l / 4,
+// elements 2 (l % 4) and 2 (l % 4) + 1, and receives those of the transpose.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
 }
 // One box of a cache's tensor map (dimensions, token of the block, head, block):
 // `box` keys, D bytes a key in the swizzle of that width.
@@ -75,18 +88,75 @@ __device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32
                  : "memory");
 }
 
+// 16 bytes by the thread itself; copies_arrive then counts for the barrier once
+// all its copies are there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // The 16-byte piece c of a key's row in a tile.
 template <int D>
 __device__ __forceinline__ int piece_at(int key, int c) {
     return D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
 }
 
+// Joins the parts of an item, in the order of the keys (the part 1 of the CTA
+// that it begins in, then the part 0 of the CTAs after it), all consumers
+// together: the parts' statistics come at once, then the rows, 4 dimensions a
+// thread, several parts' loads in flight. `stat`: place for kRows values.
+template <int D, int DT>
+__device__ __forceinline__ void join_parts(const AttnParams& p, const Span& span, int rows, int row0, int head, int token0,
+                                           float2* stat, int tid) {
+    constexpr int kFloats = attn_part_floats(kRows, D), kPer = D / 4, kNum = kConsumers * 32;
+    const float* first = p.part + ((int64_t)span.cta * 2 + 1) * kFloats;
+    const float* rest = p.part + (int64_t)span.cta * 2 * kFloats;  // part 0 of the k-th CTA at k * 2 * kFloats
+    auto part_of = [&](int k) { return k == 0 ? first : rest + (int64_t)k * 2 * kFloats; };
+    {
+        // eight threads a row; whole warps at the shuffles, so those past the
+        // last row take it again
+        static_assert(kNum == 8 * kRows, "every row at once");
+        const int row = min(tid / 8, rows - 1);
+        auto stat_of = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part_of(k) + kRows * D) + row); };
+        float mx = kNone, sum = 0.f;
+        for (int k = tid % 8; k < span.parts; k += 8) mx = fmaxf(mx, stat_of(k).x);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        for (int k = tid % 8; k < span.parts; k += 8) sum += stat_of(k).y * exp2_approx(stat_of(k).x - mx);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (tid % 8 == 0 && tid / 8 < rows) stat[row] = make_float2(mx, sum);
+    }
+    warps_sync(1, kNum);
+    for (int i = tid; i < rows * kPer; i += kNum) {
+        const int row = i / kPer;
+        const float2 all = stat[row];
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < span.parts; ++k) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(k)) + i);
+            const float f = exp2_approx(__ldcg(reinterpret_cast<const float2*>(part_of(k) + kRows * D) + row).x - all.x);
+            v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+        }
+        const float inv = all.y != 0.f ? 1.f / all.y : 0.f;
+        const int R = row0 + row, t = token_of(p, R), h = head * p.group + (R - t * p.group);
+        const int64_t at_row = (int64_t)(token0 + t) * p.heads + h;
+        *reinterpret_cast<uint2*>(p.out + at_row * D + (i % kPer) * 4) = make_uint2(pack2<DT>(v.x * inv, v.y * inv), pack2<DT>(v.z * inv, v.w * inv));
+        if (i % kPer == 0 && p.lse) p.lse[at_row] = all.y != 0.f ? (all.x + log2f(all.y)) * kLn2 : -INFINITY;
+    }
+}
+
 // Eight consumer warps share a tile's 128 keys, 16 each, so that a code is
 // turned into fp16 once for all of the item's 32 rows; they are joined at the
-// end of the item. Codes come out of shared memory four at a time: of K the four
-// dimensions 4i..4i+3 of a key, which the queries' order in shared memory
-// answers; of V two dimensions of two keys, whose even and odd dimensions go to
-// tiles of their own. A producer warp keeps the ring of tiles filled.
+// end of the item. Codes are the 16-row operand of both products and the queries
+// the one of 8 columns (S^T = K Q^T, O^T = V^T P^T): an item of 8 rows takes half
+// the matrix instructions that 16 rows of queries would, one of 24 three
+// quarters of those of 32. Codes come out of shared memory four at a time: of K
+// the four dimensions 4i..4i+3 of a key, which the queries' order in shared memory
+// answers; of V two dimensions of two keys, whose even and odd dimensions are the
+// product's rows i and i + 8. A producer warp keeps the ring of tiles filled.
 template <int D, int DT, bool TREE>
 __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_constant__ AttnParams p,
                                                                   const __grid_constant__ CUtensorMap kmap,
@@ -104,10 +174,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
     Start* found = reinterpret_cast<Start*>(scan + kThreads / 32);
     int& abort_flag = *reinterpret_cast<int*>(found + 1);
     volatile int* join_info = &abort_flag + 1;  // first CTA, parts, whether this one is the last
+    volatile int* loaded = join_info + 3;       // the last tile that each loader has issued
     if (tid == 0) {
         abort_flag = 0;
         for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(full + 8 * s, 1);
+            mbar_init(full + 8 * s, 1 + 32);  // boxes, and each lane's powers of two
             mbar_init(empty + 8 * s, kConsumers);
         }
         for (int i = 0; i < 2; ++i) {
@@ -131,55 +202,76 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
 
     if (warp >= kConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-        if (warp > kConsumers) return;
-        // producer: lane i brings the tile's i-th box, if a row sees any of it
-        int stage = 0, issued = 0;
-        uint32_t parity = 1, items = 0;
-        TileFeed<All> feed(p, at, lane);
-        auto cur = feed.box(), next = cur;
-        for (bool more = feed.any; more; cur = next) {
-            more = feed.advance();
-            if (more) next = feed.box();
-            if (cur.rows > 0) {
-                // the item's queries, a row a lane
+        if (warp == kConsumers + kLoaders) {
+            // the items' queries, a row a lane
+            uint32_t items = 0;
+            for (Walk<All> walk(p, at); walk.next(); walk.done(), ++items) {
                 const uint32_t i = items & 1u;
                 if (!__all_sync(0xffffffffu, attn_wait(q_empty + 8 * i, ((items >> 1) & 1u) ^ 1u, p, flag))) break;
-                if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * i, (uint32_t)(cur.rows * D * 2));
+                if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * i, (uint32_t)(walk.rows * D * 2));
                 __syncwarp();
-                if (lane < cur.rows) {
-                    const int R = cur.row0 + lane, t = token_of(p, R), h = cur.head * p.group + (R - t * p.group);
+                if (lane < walk.rows) {
+                    const int R = walk.row0 + lane, t = token_of(p, R), h = walk.head * p.group + (R - t * p.group);
                     copy_bytes(base + S::kOffQ + i * S::kQ + lane * S::kQRow,
-                               p.q + (cur.token0 + t) * p.q_token + h * p.q_head, D * 2, q_full + 8 * i);
+                               p.q + (int64_t)(walk.q.q0 + t) * p.q_token + h * p.q_head, D * 2, q_full + 8 * i);
                 }
-                ++items;
             }
-            if (!__all_sync(0xffffffffu, attn_wait(empty + 8 * stage, parity, p, flag))) break;
-            const bool held = p.hold_back && issued == 0;
+            // the last copies, in flight where a consumer gave up
+            if (lane == 0)
+                for (uint32_t i = items > 2 ? items - 2 : 0; i < items; ++i) attn_drain(q_full + 8 * (i & 1u), (i >> 1) & 1u);
+            return;
+        }
+        // Every kLoaders-th tile of the range: lane i brings the tile's i-th box,
+        // if a row sees any of it. (One warp alone, at 16 keys a box, was behind
+        // the consumers.)
+        TileFeed<All> feed(p, at, lane);
+        bool more = feed.any;
+        int tile = warp - kConsumers, last = -1;
+        for (int i = 0; more && i < tile; ++i) more = feed.advance();
+        auto cur = feed.box(), next = cur;
+        for (; more; cur = next) {
+            for (int i = 0; more && i < kLoaders; ++i) more = feed.advance();
+            if (more) next = feed.box();
+            const int stage = tile % S::kStages;
+            const uint32_t bar = full + 8 * stage;
+            if (!__all_sync(0xffffffffu, attn_wait(empty + 8 * stage, ((tile / S::kStages) & 1) ^ 1, p, flag))) break;
+            const bool held = p.hold_back && tile == 0;
             const bool take = attn_take(p, cur.wanted, cur.block) && !held;
             const int n = __popc(__ballot_sync(0xffffffffu, take));
-            if (lane == 0 && !held) mbar_arrive_expect_tx(full + 8 * stage, (uint32_t)(n * p.box * (2 * D + 2)));
+            if (lane == 0 && !held) mbar_arrive_expect_tx(bar, (uint32_t)(n * p.box * 2 * D));
             __syncwarp();
             if (take) {
                 const uint32_t dst = base + stage * S::kStage + lane * p.box * D;
-                copy_box(dst, &kmap, cur.token, cur.head, cur.block, full + 8 * stage);
-                copy_box(dst + S::kHalf, &vmap, cur.token, cur.head, cur.block, full + 8 * stage);
-                const int64_t byte = ((int64_t)cur.block * p.kv_heads + cur.head) * p.block_size + cur.token;
-                const uint32_t to = base + S::kOffScale + stage * 2 * kAttnTile + lane * p.box;
-                copy_bytes(to, p.scales[0] + byte, p.box, full + 8 * stage);
-                copy_bytes(to + kAttnTile, p.scales[1] + byte, p.box, full + 8 * stage);
+                copy_box(dst, &kmap, cur.token, cur.head, cur.block, bar);
+                copy_box(dst + S::kHalf, &vmap, cur.token, cur.head, cur.block, bar);
             }
-            ++issued;
-            if (++stage == S::kStages) {
-                stage = 0;
-                parity ^= 1u;
+            // The powers of two, 16 keys a lane: of K by the first 8 lanes, of V
+            // by the next. (By bulk copies, four for each box of a page of 16, 32
+            // requests of 6 tokens took 232 us for 188.)
+            const int from = (lane & 7) << 4 >> p.box_shift;  // the lane that brings their box
+            const bool there = __shfl_sync(0xffffffffu, (int)take, from) && lane < 16;
+            const int block = __shfl_sync(0xffffffffu, cur.block, from), token = __shfl_sync(0xffffffffu, cur.token, from);
+            if (there) {
+                const int64_t byte = ((int64_t)block * p.kv_heads + cur.head) * p.block_size + token + (((lane & 7) << 4) & (p.box - 1));
+                copy16(base + S::kOffScale + stage * 2 * kAttnTile + lane * 16, p.scales[lane >> 3] + byte);
             }
+            copies_arrive(bar);
+            last = tile;
+            tile += kLoaders;
         }
-        // the last copies of each stage, in flight where a consumer gave up
-        if (lane == 0) {
-            for (int i = max(p.hold_back, issued - S::kStages); i < issued; ++i)
-                attn_drain(full + 8 * (i % S::kStages), (uint32_t)((i / S::kStages) & 1));
-            for (uint32_t i = items > 2 ? items - 2 : 0; i < items; ++i) attn_drain(q_full + 8 * (i & 1u), (i >> 1) & 1u);
-        }
+        // The last copies of each stage, in flight where a consumer gave up: known
+        // once no loader issues any more (a parity says nothing of a copy that
+        // another has followed in its place).
+        if (lane == 0) loaded[warp - kConsumers] = last;
+        warps_sync(2, kLoaders * 32);
+        if (warp == kConsumers && lane == 0)
+            for (int s = 0; s < S::kStages; ++s) {
+                int newest = -1;
+                for (int i = 0; i < kLoaders; ++i)
+                    for (int t = loaded[i]; t > newest; t -= kLoaders)
+                        if (t % S::kStages == s) newest = t;
+                if (newest > 0 || (newest == 0 && !p.hold_back)) attn_drain(full + 8 * s, (uint32_t)((newest / S::kStages) & 1));
+            }
         return;
     }
 
@@ -197,90 +289,57 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
         return ok;
     };
     float2* stat = reinterpret_cast<float2*>(sm + S::kOffStat);  // [warp][row]
-    float* row_scale = reinterpret_cast<float*>(sm + S::kOffRow);
-    // [two][row][D], groups of 16 columns swizzled by the row
+    const float* row_scale = reinterpret_cast<const float*>(sm + S::kOffRow);
+    // [row][D], groups of 8 columns swizzled by the pair of rows
     float* merge = reinterpret_cast<float*>(sm + S::kOffMerge);
-    for (; walk.next(); walk.done()) {
-        const int q_off = S::kOffQ + (items & 1u) * S::kQ;
-        wait(q_full + 8 * (items & 1u), (items >> 1) & 1u);
-        // The queries in place into fp16 times a power of two that brings the
-        // row's largest into [2^14, 2^15), four rows a warp. Of 16 dimensions
-        // 4i, 4i+1 go to places 2i, 2i+1 and 4i+2, 4i+3 to 8+2i, 9+2i.
+    auto merged = [&](int row, int group) { return merge + row * D + ((group ^ ((row >> 1) & 3)) << 3); };
+
+    // The item at hand, of 8 (NT - 1) + 1 to 8 NT rows: its tiles, and its sums
+    // joined in shared memory.
+    auto item = [&](auto sets) {
+        constexpr int NT = decltype(sets)::value;
+        constexpr bool kHold = NT <= 2;  // the queries stay in registers
+        const uint32_t q_addr = base + S::kOffQ + (items & 1u) * S::kQ + (lane & 7) * S::kQRow + (lane >> 3) * 16;
+        uint32_t q[kHold ? NT : 1][D / 32][4];
+        if (kHold)
 #pragma unroll
-        for (int r = 0; r < kRows / kConsumers; ++r) {
-            const int row = warp * (kRows / kConsumers) + r;
-            if (row >= walk.rows) break;
-            constexpr int kWords = D / 64;  // of two dimensions a lane
-            uint32_t* words = reinterpret_cast<uint32_t*>(sm + q_off + row * S::kQRow);
-            float2 v[kWords];
-            uint32_t top = 0;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-                const uint32_t w = words[lane * kWords + i];
-                v[i] = DT == 0 ? make_float2(bf16lo(w), bf16hi(w)) : f16x2_to_f32(w);
-                top = max(top, max(__float_as_uint(v[i].x) & 0x7fffffffu, __float_as_uint(v[i].y) & 0x7fffffffu));
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            const int s = top ? max(-113, min(126, 14 - ((int)(top >> 23) - 127))) : 0;
-            const float by = exp2i(s);
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-                const int g = lane * kWords + i, in = g & 7;  // pair of dimensions, in its group of 16
-                words[(g & ~7) + (in & 1) * 4 + (in >> 1)] = f32x2_to_f16x2(v[i].x * by, v[i].y * by);
-            }
-            if (lane == 0) row_scale[row] = exp2i(-s) * p.scale_log2;
-        }
-        warps_sync(1, kConsumers * 32);
-        // (rows past the item's last hold anything; a row's results depend on
-        // no other row)
-        const uint32_t q_addr = base + q_off + (lane & 15) * S::kQRow + (lane >> 4) * 16;
+                for (int c = 0; c < D / 32; ++c) ldsm_x4(q_addr + n * 8 * S::kQRow + c * 64, q[n][c]);
         const AllKeys all = attn_all_keys(walk, 0, walk.rows);
         const Tree tree = attn_tree<TREE>(walk);
-        // of this thread's four rows (8 h + quad): the last key that each sees
-        // and the first
-        int last[4], from[4];
-        float factor[4];
-        unsigned long long mask[4];
+        // sums of this thread's rows 8 n + 2 pair + (j & 1), dimensions 16 g +
+        // 2 quad + (j >> 1); references of the scores and of the products'
+        // weights, sums of weights (of this thread's keys)
+        float o[NT][D / 16][4];
+        float m[NT][2], w[NT][2], l[NT][2], factor[NT][2];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const RowKeys k = attn_row_keys(walk, h * 8 + quad);
-            last[h] = k.last;
-            from[h] = k.from;
-            factor[h] = row_scale[h * 8 + quad];
-            mask[h] = TREE ? attn_tree_mask(walk, tree, h * 8 + quad) : ~0ull;
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                m[n][r] = w[n][r] = kNone;
+                l[n][r] = 0.f;
+                factor[n][r] = row_scale[n * 8 + 2 * pair + r];
+            }
+#pragma unroll
+            for (int g = 0; g < D / 16; ++g)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][g][j] = 0.f;
         }
-        float o[2][D / 8][4];
-        float m[4], w[4], l[4];  // references of the scores and of the products' weights
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            m[h] = w[h] = -INFINITY;
-            l[h] = 0.f;
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
-        const bool two = walk.rows > 16;  // sets of 16 rows
         for (int t = walk.t0; t < walk.t1; ++t) {
             if (!wait(full + 8 * stage, parity)) break;
             const int key0 = (walk.tile0 + t) * kAttnTile + warp * kWarpKeys;
             const uint32_t ks = base + stage * S::kStage, vs = ks + S::kHalf;
             if (attn_needs(walk, key0, kWarpKeys)) {
                 const bool ragged = attn_ragged(walk, key0, kWarpKeys);
-                // the exponents of this thread's four keys, 8 i + 2 pair + j
-                float kf[4], ve[4];
+                // powers of two of this thread's keys, quad and quad + 8
+                const uint8_t* bytes = sm + S::kOffScale + stage * 2 * kAttnTile + warp * kWarpKeys + quad;
+                float kf[2], ve[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint8_t* bytes = sm + S::kOffScale + stage * 2 * kAttnTile + warp * kWarpKeys + i * 8 + 2 * pair;
-                    const uint32_t kb = *reinterpret_cast<const uint16_t*>(bytes), vb = *reinterpret_cast<const uint16_t*>(bytes + kAttnTile);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t a = (kb >> (8 * j)) & 255u, b = (vb >> (8 * j)) & 255u;
-                        kf[2 * i + j] = e8m0_to_f32(a);
-                        ve[2 * i + j] = b == 255u ? __uint_as_float(0x7fc00000u) : (float)((int)b - 127);
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t a = bytes[8 * k], b = bytes[kAttnTile + 8 * k];
+                    kf[k] = e8m0_to_f32(a);
+                    ve[k] = b == 255u ? __uint_as_float(0x7fc00000u) : (float)((int)b - 127);
                 }
                 if (ragged) {
                     // values that no row sees may be anything: a weight of 0 times
@@ -292,19 +351,22 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
                         for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int k = key0 + (i >> 1) * 8 + 2 * pair + (i & 1);
-                        if (k < walk.lo || k >= walk.hi) ve[i] = 0.f;
-                    }
+                    for (int k = 0; k < 2; ++k)
+                        if (key0 + 8 * k + quad < walk.lo || key0 + 8 * k + quad >= walk.hi) ve[k] = 0.f;
                     __syncwarp();
                 }
-                float s[2][2][4];
+                // scores of 16 keys (rows of the product) and 8 queries each
+                // (in two sums of every other step where there are few of them:
+                // a product waits for the one before it)
+                constexpr int kSums = NT <= 2 ? 2 : 1;
+                float s[NT][4], s2[kSums > 1 ? NT : 1][4];
 #pragma unroll
-                for (int t2 = 0; t2 < 2; ++t2)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s[t2][i][j] = 0.f;
+                    for (int j = 0; j < 4; ++j) {
+                        s[n][j] = 0.f;
+                        if (kSums > 1) s2[n][j] = 0.f;
+                    }
                 const int k_row = warp * kWarpKeys + (lane & 7) + ((lane >> 4) << 3), k_piece = (lane >> 3) & 1;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -312,89 +374,91 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
                     ldsm_x4(ks + piece_at<D>(k_row, 2 * c + k_piece), codes);
                     // codes of keys 0-7: dimensions 32 c .., 32 c + 16 ..; then
                     // of keys 8-15
+                    uint32_t a[2][4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        uint32_t b[2][2];
-                        e4m3x4_to_f16x2(codes[k], b[0][0], b[0][1]);
-                        e4m3x4_to_f16x2(codes[2 + k], b[1][0], b[1][1]);
-                        uint32_t a[4];
-                        ldsm_x4(q_addr + (2 * c + k) * 32, a);
-                        mma_f16(s[0][0], a, b[0][0], b[0][1]);
-                        mma_f16(s[0][1], a, b[1][0], b[1][1]);
-                        if (two) {
-                            ldsm_x4(q_addr + 16 * S::kQRow + (2 * c + k) * 32, a);
-                            mma_f16(s[1][0], a, b[0][0], b[0][1]);
-                            mma_f16(s[1][1], a, b[1][0], b[1][1]);
-                        }
+                        e4m3x4_to_f16x2(codes[k], a[k][0], a[k][2]);
+                        e4m3x4_to_f16x2(codes[2 + k], a[k][1], a[k][3]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t b[4];
+                        if (!kHold) ldsm_x4(q_addr + n * 8 * S::kQRow + c * 64, b);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mma_f16(kSums > 1 && k == 1 ? s2[kSums > 1 ? n : 0] : s[n], a[k], kHold ? q[kHold ? n : 0][c][2 * k] : b[2 * k],
+                                    kHold ? q[kHold ? n : 0][c][2 * k + 1] : b[2 * k + 1]);
                     }
                 }
-                // scores in units of log2, element (i, j & 1) of row half j >> 1
-                const bool some = all.lacks(key0, kWarpKeys), leaves = TREE && tree.reaches(key0, kWarpKeys);
+                // scores in units of log2: element j is key quad + 8 (j >> 1),
+                // row j & 1
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (kSums > 1) s[n][j] += s2[n][j];
+                        s[n][j] *= factor[n][j & 1] * kf[j >> 1];
+                    }
+                if (all.lacks(key0, kWarpKeys) || (TREE && tree.reaches(key0, kWarpKeys)))
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const RowKeys sees = attn_row_keys(walk, n * 8 + 2 * pair + r);
+                            const unsigned long long mask = TREE ? attn_tree_mask(walk, tree, n * 8 + 2 * pair + r) : ~0ull;
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int key = key0 + 8 * k + quad;
+                                if (key > sees.last || key < sees.from || (TREE && attn_tree_hides(tree, mask, key)))
+                                    s[n][2 * k + r] = -INFINITY;
+                            }
+                        }
                 bool grows = false;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (h >= 2 && !two) break;
-                    float big = -INFINITY, big_v = -INFINITY;
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float& x = s[h >> 1][e >> 1][(h & 1) * 2 + (e & 1)];
-                        x *= factor[h] * kf[e];
-                        if (some || leaves) {
-                            const int key = key0 + (e >> 1) * 8 + 2 * pair + (e & 1);
-                            if (key > last[h] || key < from[h]) x = -INFINITY;
-                            if (TREE && attn_tree_hides(tree, mask[h], key)) x = -INFINITY;
-                        }
-                        big = fmaxf(big, x);
-                        big_v = fmaxf(big_v, x + ve[e]);
-                    }
-                    grows |= big > m[h] + kLimit || big_v > w[h] + kLimit;
-                }
-                // (rare: the largest scores so far move up by more than 2^4 a
-                // few times in a row of any length)
+                    for (int r = 0; r < 2; ++r)
+                        grows |= fmaxf(s[n][r], s[n][2 + r]) > m[n][r] + kLimit ||
+                                 fmaxf(s[n][r] + ve[0], s[n][2 + r] + ve[1]) > w[n][r] + kLimit;
+                // (rare: a row's largest score so far moves up by more than 2^4
+                // a few times, however long the row)
                 if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        if (h >= 2 && !two) break;
-                        float big = -INFINITY, big_v = -INFINITY;
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float x = s[h >> 1][e >> 1][(h & 1) * 2 + (e & 1)];
-                            big = fmaxf(big, x);
-                            big_v = fmaxf(big_v, x + ve[e]);
-                        }
+                        for (int r = 0; r < 2; ++r) {
+                            float big = fmaxf(s[n][r], s[n][2 + r]), big_v = fmaxf(s[n][r] + ve[0], s[n][2 + r] + ve[1]);
 #pragma unroll
-                        for (int d = 1; d < 4; d <<= 1) {
-                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-                            big_v = fmaxf(big_v, __shfl_xor_sync(0xffffffffu, big_v, d));
-                        }
-                        if (big > m[h] + kLimit) {
-                            l[h] *= exp2_approx(m[h] - (big - kBias));
-                            m[h] = big - kBias;
-                        }
-                        const bool up = big_v > w[h] + kLimit;
-                        const float f = up ? exp2_approx(w[h] - (big_v - kBias)) : 1.f;
-                        if (up) w[h] = big_v - kBias;
+                            for (int d = 4; d < 32; d <<= 1) {
+                                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+                                big_v = fmaxf(big_v, __shfl_xor_sync(0xffffffffu, big_v, d));
+                            }
+                            if (big > m[n][r] + kLimit) {
+                                l[n][r] *= exp2_approx(m[n][r] - (big - kBias));
+                                m[n][r] = big - kBias;
+                            }
+                            const bool up = big_v > w[n][r] + kLimit;
+                            const float f = up ? exp2_approx(w[n][r] - (big_v - kBias)) : 1.f;
+                            if (up) w[n][r] = big_v - kBias;
 #pragma unroll
-                        for (int i = 0; i < D / 8; ++i) {
-                            o[h >> 1][i][(h & 1) * 2] *= f;
-                            o[h >> 1][i][(h & 1) * 2 + 1] *= f;
+                            for (int g = 0; g < D / 16; ++g) {
+                                o[n][g][r] *= f;
+                                o[n][g][2 + r] *= f;
+                            }
                         }
-                    }
                 }
-                uint32_t pa[2][4];
+                uint32_t pb[NT][2];  // weights of keys 0-7 and 8-15, keys along the registers
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (h >= 2 && !two) break;
-                    const float ref = m[h] == -INFINITY ? 0.f : m[h], ref_v = w[h] == -INFINITY ? 0.f : w[h];
-                    float sum = 0.f;
+                for (int n = 0; n < NT; ++n) {
+                    float x[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float x = s[h >> 1][i][(h & 1) * 2], y = s[h >> 1][i][(h & 1) * 2 + 1];
-                        sum += exp2_approx(x - ref) + exp2_approx(y - ref);
-                        pa[h >> 1][i * 2 + (h & 1)] =
-                            f32x2_to_f16x2(exp2_approx(x + (ve[2 * i] - ref_v)), exp2_approx(y + (ve[2 * i + 1] - ref_v)));
+                    for (int r = 0; r < 2; ++r) {
+                        l[n][r] += exp2_approx(s[n][r] - m[n][r]) + exp2_approx(s[n][2 + r] - m[n][r]);
+                        x[r] = exp2_approx(s[n][r] + (ve[0] - w[n][r]));
+                        x[2 + r] = exp2_approx(s[n][2 + r] + (ve[1] - w[n][r]));
                     }
-                    l[h] += sum;
+                    pb[n][0] = transpose8(f32x2_to_f16x2(x[0], x[1]));
+                    pb[n][1] = transpose8(f32x2_to_f16x2(x[2], x[3]));
                 }
                 const int v_row = warp * kWarpKeys + (lane & 15), v_piece = lane >> 4;
 #pragma unroll
@@ -405,15 +469,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
                     // dimensions keys 0-7 and 8-15, then of the next 16
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        uint32_t even[2], odd[2];
+                        uint32_t a[4];  // even dimensions, odd ones; then of the later keys
+                        e4m3x4_to_f16x2(__byte_perm(codes[2 * g], 0, 0x3120), a[0], a[1]);
+                        e4m3x4_to_f16x2(__byte_perm(codes[2 * g + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) e4m3x4_to_f16x2(__byte_perm(codes[2 * g + k], 0, 0x3120), even[k], odd[k]);
-                        mma_f16(o[0][4 * c + 2 * g], pa[0], even[0], even[1]);
-                        mma_f16(o[0][4 * c + 2 * g + 1], pa[0], odd[0], odd[1]);
-                        if (two) {
-                            mma_f16(o[1][4 * c + 2 * g], pa[1], even[0], even[1]);
-                            mma_f16(o[1][4 * c + 2 * g + 1], pa[1], odd[0], odd[1]);
-                        }
+                        for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * c + g], a, pb[n][0], pb[n][1]);
                     }
                 }
                 if (ragged) fence_proxy_async_shared();
@@ -425,75 +485,121 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
                 parity ^= 1u;
             }
         }
+        // join the warps: each scales to the largest score of all, then they add
+        // up, in each of eight rounds each warp an eighth of the dimensions (or
+        // rows) that no other is at
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], d);
+                if (quad == 0) stat[warp * kRows + n * 8 + 2 * pair + r] = make_float2(m[n][r], l[n][r]);
+            }
+        warps_sync(1, kConsumers * 32);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = n * 8 + 2 * pair + r;
+                float mx = -INFINITY, tot = 0.f;
+#pragma unroll
+                for (int x = 0; x < kConsumers; ++x) mx = fmaxf(mx, stat[x * kRows + row].x);
+#pragma unroll
+                for (int x = 0; x < kConsumers; ++x) tot += stat[x * kRows + row].y * exp2_approx(stat[x * kRows + row].x - mx);
+                m[n][r] = mx;
+                l[n][r] = tot;
+                // (nothing was seen: 0 times infinity is not 0)
+                const float f = w[n][r] == kNone ? 1.f : exp2_approx(w[n][r] - mx);
+#pragma unroll
+                for (int g = 0; g < D / 16; ++g) {
+                    o[n][g][r] *= f;
+                    o[n][g][2 + r] *= f;
+                }
+            }
+        for (int x = 0; x < kConsumers; ++x) {
+            auto slice = [&](auto which) {
+                constexpr int e = decltype(which)::value;
+                constexpr bool kHalves = D == 64;  // of the rows, by their low bit
+                constexpr int g = kHalves ? e >> 1 : e;
+                if ((warp ^ x) != e) return;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (kHalves && r != (e & 1)) continue;
+                        float2* to = reinterpret_cast<float2*>(merged(n * 8 + 2 * pair + r, 2 * g + (quad >> 2)) + 2 * (quad & 3));
+                        const float2 u = x > 0 ? *to : make_float2(0.f, 0.f);
+                        *to = make_float2(u.x + o[n][g][r], u.y + o[n][g][2 + r]);
+                    }
+            };
+            slice(std::integral_constant<int, 0>{});
+            slice(std::integral_constant<int, 1>{});
+            slice(std::integral_constant<int, 2>{});
+            slice(std::integral_constant<int, 3>{});
+            slice(std::integral_constant<int, 4>{});
+            slice(std::integral_constant<int, 5>{});
+            slice(std::integral_constant<int, 6>{});
+            slice(std::integral_constant<int, 7>{});
+            // (everyone has read the statistics by the first of these)
+            if (x == kConsumers - 1 && warp == 0 && quad == 0)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) stat[n * 8 + 2 * pair + r] = make_float2(m[n][r], l[n][r]);
+            warps_sync(1, kConsumers * 32);
+        }
+    };
+
+    for (; walk.next(); walk.done()) {
+        const int q_off = S::kOffQ + (items & 1u) * S::kQ;
+        wait(q_full + 8 * (items & 1u), (items >> 1) & 1u);
+        // The queries in place into fp16 times a power of two that brings the
+        // row's largest into [2^14, 2^15), four rows a warp. Of 16 dimensions
+        // 4i, 4i+1 go to places 2i, 2i+1 and 4i+2, 4i+3 to 8+2i, 9+2i. (Rows past
+        // the item's last hold anything; a row's results depend on no other.)
+#pragma unroll
+        for (int r = 0; r < kRows / kConsumers; ++r) {
+            const int row = warp * (kRows / kConsumers) + r;
+            if (row >= walk.rows) break;
+            constexpr int kWords = D / 64;  // of two dimensions a lane
+            uint32_t* words = reinterpret_cast<uint32_t*>(sm + q_off + row * S::kQRow);
+            float2 v[kWords];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const uint32_t x = words[lane * kWords + i];
+                v[i] = DT == 0 ? make_float2(bf16lo(x), bf16hi(x)) : f16x2_to_f32(x);
+                top = max(top, max(__float_as_uint(v[i].x) & 0x7fffffffu, __float_as_uint(v[i].y) & 0x7fffffffu));
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int s = top ? max(-113, min(126, 14 - ((int)(top >> 23) - 127))) : 0;
+            const float by = exp2i(s);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const int g = lane * kWords + i, in = g & 7;  // pair of dimensions, in its group of 16
+                words[(g & ~7) + (in & 1) * 4 + (in >> 1)] = f32x2_to_f16x2(v[i].x * by, v[i].y * by);
+            }
+            if (lane == 0) reinterpret_cast<float*>(sm + S::kOffRow)[row] = exp2i(-s) * p.scale_log2;
+        }
+        warps_sync(1, kConsumers * 32);
+        if (walk.rows <= 8) item(std::integral_constant<int, 1>{});
+        else if (walk.rows <= 16) item(std::integral_constant<int, 2>{});
+        else if (walk.rows <= 24) item(std::integral_constant<int, 3>{});
+        else item(std::integral_constant<int, 4>{});
         // (this warp's rows of the queries were written in place: the next copy
         // into them comes after)
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_empty + 8 * (items & 1u));
         ++items;
-        // join the warps: each scales to the largest score of all, then they add
-        // up one after another, four in each of two places
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (pair == 0) stat[warp * kRows + h * 8 + quad] = make_float2(m[h], l[h]);
-        }
-        warps_sync(1, kConsumers * 32);
-        float all_m[4], all_l[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const int row = h * 8 + quad;
-            float mx = -INFINITY, tot = 0.f;
-#pragma unroll
-            for (int x = 0; x < kConsumers; ++x) mx = fmaxf(mx, stat[x * kRows + row].x);
-            const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-            for (int x = 0; x < kConsumers; ++x) tot += stat[x * kRows + row].y * exp2_approx(stat[x * kRows + row].x - ref);
-            all_m[h] = mx;
-            all_l[h] = tot;
-            const float f = exp2_approx(w[h] - ref);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                o[h >> 1][i][(h & 1) * 2] *= f;
-                o[h >> 1][i][(h & 1) * 2 + 1] *= f;
-            }
-        }
-        for (int x = 0; x < kConsumers / 2; ++x) {
-            if (warp / 2 == x) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (h >= 2 && !two) break;
-                    // dimensions 16 g + 4 pair .. + 3
-                    float* row = merge + (warp & 1) * (kRows * D) + (h * 8 + quad) * D + 4 * pair;
-#pragma unroll
-                    for (int g = 0; g < D / 16; ++g) {
-                        float4* to = reinterpret_cast<float4*>(row + (g ^ (quad & 1)) * 16);
-                        float4 u = x > 0 ? *to : make_float4(0.f, 0.f, 0.f, 0.f);
-                        u.x += o[h >> 1][2 * g][(h & 1) * 2];
-                        u.y += o[h >> 1][2 * g + 1][(h & 1) * 2];
-                        u.z += o[h >> 1][2 * g][(h & 1) * 2 + 1];
-                        u.w += o[h >> 1][2 * g + 1][(h & 1) * 2 + 1];
-                        *to = u;
-                    }
-                }
-            }
-            // (everyone has read the statistics by the first of these)
-            if (x == kConsumers / 2 - 1 && warp == 0 && pair == 0)
-#pragma unroll
-                for (int h = 0; h < 4; ++h) stat[h * 8 + quad] = make_float2(all_m[h], all_l[h]);
-            warps_sync(1, kConsumers * 32);
-        }
         // 16 bytes of output a thread
         const bool whole = walk.whole();
         float* part = p.part + ((int64_t)blockIdx.x * 2 + walk.part()) * attn_part_floats(kRows, D);
         for (int i = tid; i < walk.rows * (D / 8); i += kConsumers * 32) {
             const int row = i / (D / 8), c = i % (D / 8);
-            const float* from_row = merge + row * D + ((c >> 1) ^ (row & 1)) * 16 + (c & 1) * 8;
-            float4 x = *reinterpret_cast<const float4*>(from_row), y = *reinterpret_cast<const float4*>(from_row + 4);
-            const float4 x2 = *reinterpret_cast<const float4*>(from_row + kRows * D), y2 = *reinterpret_cast<const float4*>(from_row + kRows * D + 4);
-            x.x += x2.x; x.y += x2.y; x.z += x2.z; x.w += x2.w;
-            y.x += y2.x; y.y += y2.y; y.z += y2.z; y.w += y2.w;
+            const float4* sum = reinterpret_cast<const float4*>(merged(row, c));
+            const float4 x = sum[0], y = sum[1];
             if (whole) {
                 const float2 ml = stat[row];
                 const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
@@ -523,8 +629,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
             }
             warps_sync(1, kConsumers * 32);
             if (join_info[2])
-                attn_join<D, DT, kRows, kConsumers * 32, 2>(p, p.part, Span{join_info[0], join_info[1]}, 0, walk.rows,
-                                                         walk.row0, walk.head, walk.q.q0, tid);
+                join_parts<D, DT>(p, Span{join_info[0], join_info[1]}, walk.rows, walk.row0, walk.head, walk.q.q0, stat, tid);
             warps_sync(1, kConsumers * 32);
         }
     }
