@@ -25,7 +25,7 @@ constexpr int kLoaders = 3;    // warps that bring tiles, in turn; a fourth brin
 // Sums of 32 rows of 128 dimensions are 128 registers of a thread: the consumers
 // take registers from the third warpgroup. Together exactly what the block is
 // launched with.
-constexpr int kLaunchRegs = 168, kConsumerRegs = 224, kProducerRegs = 56;
+constexpr int kLaunchRegs = 168, kConsumerRegs = 232, kProducerRegs = 40;
 static_assert(2 * kConsumerRegs + kProducerRegs == 3 * kLaunchRegs, "registers of the block");
 constexpr int kWarpKeys = kAttnTile / kConsumers;  // 16
 static_assert(kWarpKeys == 16, "one step of the second product");
@@ -49,7 +49,7 @@ struct CodesShape {
     static constexpr int kOffQ = kOffScale + kStages * 2 * kAttnTile;
     static constexpr int kOffMerge = kOffQ + 2 * kQ;
     static constexpr int kOffStat = kOffMerge + kMerge;  // largest score and sum of each warp's rows
-    static constexpr int kOffRow = kOffStat + kConsumers * kRows * 8;  // powers of two of the queries
+    static constexpr int kOffRow = kOffStat + (kConsumers + 1) * kRows * 8;  // powers of two of the queries
     static constexpr int kOffBar = kOffRow + kRows * 4;
     static constexpr int kOffMisc = kOffBar + 16 * (kStages + 2);
     static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + (int)sizeof(Start) + 16 + 4 * kLoaders;
@@ -95,6 +95,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A key's power of two from its byte, times 2^-24 (the queries' factors make up
+// for it, so that neither the sums of a row's products nor their products with
+// this pass fp32's range); a value's exponent. 255 is NaN.
+__device__ __forceinline__ float key_power(uint32_t byte) {
+    return __uint_as_float(byte == 255u ? 0x7fc00000u : (uint32_t)max((int)byte - 24, 0) << 23);
+}
+__device__ __forceinline__ float value_exponent(uint32_t byte) {
+    return byte == 255u ? __uint_as_float(0x7fc00000u) : (float)((int)byte - 127);
 }
 
 // The 16-byte piece c of a key's row in a tile.
@@ -289,6 +299,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
         return ok;
     };
     float2* stat = reinterpret_cast<float2*>(sm + S::kOffStat);  // [warp][row]
+    float2* total = stat + kConsumers * kRows;                   // [row]
     const float* row_scale = reinterpret_cast<const float*>(sm + S::kOffRow);
     // [row][D], groups of 8 columns swizzled by the pair of rows
     float* merge = reinterpret_cast<float*>(sm + S::kOffMerge);
@@ -312,172 +323,198 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
         // 2 quad + (j >> 1); references of the scores and of the products'
         // weights, sums of weights (of this thread's keys)
         float o[NT][D / 16][4];
-        float m[NT][2], w[NT][2], l[NT][2], factor[NT][2];
+        float m[NT][2], w[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 m[n][r] = w[n][r] = kNone;
                 l[n][r] = 0.f;
-                factor[n][r] = row_scale[n * 8 + 2 * pair + r];
             }
 #pragma unroll
             for (int g = 0; g < D / 16; ++g)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[n][g][j] = 0.f;
         }
-        for (int t = walk.t0; t < walk.t1; ++t) {
-            if (!wait(full + 8 * stage, parity)) break;
-            const int key0 = (walk.tile0 + t) * kAttnTile + warp * kWarpKeys;
-            const uint32_t ks = base + stage * S::kStage, vs = ks + S::kHalf;
-            if (attn_needs(walk, key0, kWarpKeys)) {
-                const bool ragged = attn_ragged(walk, key0, kWarpKeys);
-                // powers of two of this thread's keys, quad and quad + 8
-                const uint8_t* bytes = sm + S::kOffScale + stage * 2 * kAttnTile + warp * kWarpKeys + quad;
-                float kf[2], ve[2];
+        // Scores of 16 keys (rows of the product) and 8 queries each, in two sums
+        // of every other step where there are few of them: a product waits for
+        // the one before it.
+        constexpr int kSums = NT <= 2 ? 2 : 1;
+        struct Scores {
+            float s[kSums][NT][4];
+            int key0, stage;
+            bool needed;
+        };
+        auto product = [&](int t, int at_stage) {
+            Scores x;
+            x.key0 = (walk.tile0 + t) * kAttnTile + warp * kWarpKeys;
+            x.stage = at_stage;
+            x.needed = attn_needs(walk, x.key0, kWarpKeys);
+#pragma unroll
+            for (int h = 0; h < kSums; ++h)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x.s[h][n][j] = 0.f;
+            if (!x.needed) return x;
+            const uint32_t ks = base + at_stage * S::kStage;
+            const int k_row = warp * kWarpKeys + (lane & 7) + ((lane >> 4) << 3), k_piece = (lane >> 3) & 1;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t codes[4], b[kHold ? 1 : NT][4];
+                ldsm_x4(ks + piece_at<D>(k_row, 2 * c + k_piece), codes);
+                if (!kHold)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) ldsm_x4(q_addr + n * 8 * S::kQRow + c * 64, b[kHold ? 0 : n]);
+                // codes of keys 0-7: dimensions 32 c .., 32 c + 16 ..; then of
+                // keys 8-15
+                uint32_t a[2][4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t a = bytes[8 * k], b = bytes[kAttnTile + 8 * k];
-                    kf[k] = e8m0_to_f32(a);
-                    ve[k] = b == 255u ? __uint_as_float(0x7fc00000u) : (float)((int)b - 127);
+                    e4m3x4_to_f16x2(codes[k], a[k][0], a[k][2]);
+                    e4m3x4_to_f16x2(codes[2 + k], a[k][1], a[k][3]);
                 }
-                if (ragged) {
-                    // values that no row sees may be anything: a weight of 0 times
-                    // NaN is not 0, so they are cleared, and their exponents
-                    const int key = key0 + (lane & 15);
-                    if (key < walk.lo || key >= walk.hi) {
-                        uint8_t* v = sm + stage * S::kStage + S::kHalf + (warp * kWarpKeys + (lane & 15)) * D + (lane >> 4) * (D / 2);
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (key0 + 8 * k + quad < walk.lo || key0 + 8 * k + quad >= walk.hi) ve[k] = 0.f;
-                    __syncwarp();
-                }
-                // scores of 16 keys (rows of the product) and 8 queries each
-                // (in two sums of every other step where there are few of them:
-                // a product waits for the one before it)
-                constexpr int kSums = NT <= 2 ? 2 : 1;
-                float s[NT][4], s2[kSums > 1 ? NT : 1][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        s[n][j] = 0.f;
-                        if (kSums > 1) s2[n][j] = 0.f;
-                    }
-                const int k_row = warp * kWarpKeys + (lane & 7) + ((lane >> 4) << 3), k_piece = (lane >> 3) & 1;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t codes[4];
-                    ldsm_x4(ks + piece_at<D>(k_row, 2 * c + k_piece), codes);
-                    // codes of keys 0-7: dimensions 32 c .., 32 c + 16 ..; then
-                    // of keys 8-15
-                    uint32_t a[2][4];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        e4m3x4_to_f16x2(codes[k], a[k][0], a[k][2]);
-                        e4m3x4_to_f16x2(codes[2 + k], a[k][1], a[k][3]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        uint32_t b[4];
-                        if (!kHold) ldsm_x4(q_addr + n * 8 * S::kQRow + c * 64, b);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            mma_f16(kSums > 1 && k == 1 ? s2[kSums > 1 ? n : 0] : s[n], a[k], kHold ? q[kHold ? n : 0][c][2 * k] : b[2 * k],
-                                    kHold ? q[kHold ? n : 0][c][2 * k + 1] : b[2 * k + 1]);
-                    }
-                }
-                // scores in units of log2: element j is key quad + 8 (j >> 1),
-                // row j & 1
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (kSums > 1) s[n][j] += s2[n][j];
-                        s[n][j] *= factor[n][j & 1] * kf[j >> 1];
-                    }
-                if (all.lacks(key0, kWarpKeys) || (TREE && tree.reaches(key0, kWarpKeys)))
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
+                        mma_f16(x.s[k % kSums][n], a[k], kHold ? q[kHold ? n : 0][c][2 * k] : b[kHold ? 0 : n][2 * k],
+                                kHold ? q[kHold ? n : 0][c][2 * k + 1] : b[kHold ? 0 : n][2 * k + 1]);
+            }
+            return x;
+        };
+        // What a tile's scores are for: weights, sums, the second product.
+        auto finish = [&](Scores& x) {
+            auto& s = x.s[0];
+            const int key0 = x.key0;
+            const bool ragged = attn_ragged(walk, key0, kWarpKeys);
+            // powers of two of this thread's keys, quad and quad + 8
+            const uint8_t* bytes = sm + S::kOffScale + x.stage * 2 * kAttnTile + warp * kWarpKeys + quad;
+            float kf[2], ve[2];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const RowKeys sees = attn_row_keys(walk, n * 8 + 2 * pair + r);
-                            const unsigned long long mask = TREE ? attn_tree_mask(walk, tree, n * 8 + 2 * pair + r) : ~0ull;
+            for (int k = 0; k < 2; ++k) {
+                kf[k] = key_power(bytes[8 * k]);
+                ve[k] = value_exponent(bytes[kAttnTile + 8 * k]);
+            }
+            if (ragged) {
+                // values that no row sees may be anything: a weight of 0 times NaN
+                // is not 0, so they are cleared, and their exponents
+                const int key = key0 + (lane & 15);
+                if (key < walk.lo || key >= walk.hi) {
+                    uint8_t* v = sm + x.stage * S::kStage + S::kHalf + (warp * kWarpKeys + (lane & 15)) * D + (lane >> 4) * (D / 2);
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int key = key0 + 8 * k + quad;
-                                if (key > sees.last || key < sees.from || (TREE && attn_tree_hides(tree, mask, key)))
-                                    s[n][2 * k + r] = -INFINITY;
-                            }
-                        }
-                bool grows = false;
+                    for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (key0 + 8 * k + quad < walk.lo || key0 + 8 * k + quad >= walk.hi) ve[k] = 0.f;
+                __syncwarp();
+            }
+            // element j is key quad + 8 (j >> 1), row j & 1; its score, in units of
+            // log2, is it times the row's factor
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[n][j] = (kSums > 1 ? s[n][j] + x.s[kSums - 1][n][j] : s[n][j]) * kf[j >> 1];
+            if (all.lacks(key0, kWarpKeys) || (TREE && tree.reaches(key0, kWarpKeys)))
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        grows |= fmaxf(s[n][r], s[n][2 + r]) > m[n][r] + kLimit ||
-                                 fmaxf(s[n][r] + ve[0], s[n][2 + r] + ve[1]) > w[n][r] + kLimit;
-                // (rare: a row's largest score so far moves up by more than 2^4
-                // a few times, however long the row)
-                if (__any_sync(0xffffffffu, grows)) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float big = fmaxf(s[n][r], s[n][2 + r]), big_v = fmaxf(s[n][r] + ve[0], s[n][2 + r] + ve[1]);
-#pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) {
-                                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-                                big_v = fmaxf(big_v, __shfl_xor_sync(0xffffffffu, big_v, d));
-                            }
-                            if (big > m[n][r] + kLimit) {
-                                l[n][r] *= exp2_approx(m[n][r] - (big - kBias));
-                                m[n][r] = big - kBias;
-                            }
-                            const bool up = big_v > w[n][r] + kLimit;
-                            const float f = up ? exp2_approx(w[n][r] - (big_v - kBias)) : 1.f;
-                            if (up) w[n][r] = big_v - kBias;
-#pragma unroll
-                            for (int g = 0; g < D / 16; ++g) {
-                                o[n][g][r] *= f;
-                                o[n][g][2 + r] *= f;
-                            }
-                        }
-                }
-                uint32_t pb[NT][2];  // weights of keys 0-7 and 8-15, keys along the registers
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float x[4];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        l[n][r] += exp2_approx(s[n][r] - m[n][r]) + exp2_approx(s[n][2 + r] - m[n][r]);
-                        x[r] = exp2_approx(s[n][r] + (ve[0] - w[n][r]));
-                        x[2 + r] = exp2_approx(s[n][2 + r] + (ve[1] - w[n][r]));
+                        const RowKeys sees = attn_row_keys(walk, n * 8 + 2 * pair + r);
+                        const unsigned long long mask = TREE ? attn_tree_mask(walk, tree, n * 8 + 2 * pair + r) : ~0ull;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int key = key0 + 8 * k + quad;
+                            if (key > sees.last || key < sees.from || (TREE && attn_tree_hides(tree, mask, key)))
+                                s[n][2 * k + r] = -INFINITY;
+                        }
                     }
-                    pb[n][0] = transpose8(f32x2_to_f16x2(x[0], x[1]));
-                    pb[n][1] = transpose8(f32x2_to_f16x2(x[2], x[3]));
-                }
-                const int v_row = warp * kWarpKeys + (lane & 15), v_piece = lane >> 4;
+            // exponents of the weights, by the references as they are
+            float xm[NT][4], xv[NT][4], factor[NT][2];
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t codes[4];
-                    ldsm_x4_trans(vs + piece_at<D>(v_row, 2 * c + v_piece), codes);
-                    // two keys' codes of dimensions 2i and 2i + 1: of 16
-                    // dimensions keys 0-7 and 8-15, then of the next 16
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t a[4];  // even dimensions, odd ones; then of the later keys
-                        e4m3x4_to_f16x2(__byte_perm(codes[2 * g], 0, 0x3120), a[0], a[1]);
-                        e4m3x4_to_f16x2(__byte_perm(codes[2 * g + 1], 0, 0x3120), a[2], a[3]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * c + g], a, pb[n][0], pb[n][1]);
-                    }
-                }
-                if (ragged) fence_proxy_async_shared();
+            for (int n = 0; n < NT; ++n) {
+                const float2 f = *reinterpret_cast<const float2*>(row_scale + n * 8 + 2 * pair);
+                factor[n][0] = f.x;
+                factor[n][1] = f.y;
             }
+            bool grows = false;
+            auto exponents = [&] {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        xm[n][j] = fmaf(s[n][j], factor[n][j & 1], -m[n][j & 1]);
+                        xv[n][j] = fmaf(s[n][j], factor[n][j & 1], ve[j >> 1] - w[n][j & 1]);
+                    }
+            };
+            exponents();
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) grows |= fmaxf(xm[n][j], xv[n][j]) > kLimit;
+            // (rare: a row's largest score so far moves up by more than 2^4 a few
+            // times, however long the row)
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float x0 = s[n][r] * factor[n][r], x1 = s[n][2 + r] * factor[n][r];
+                        float big = fmaxf(x0, x1), big_v = fmaxf(x0 + ve[0], x1 + ve[1]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+                            big_v = fmaxf(big_v, __shfl_xor_sync(0xffffffffu, big_v, d));
+                        }
+                        if (big > m[n][r] + kLimit) {
+                            l[n][r] *= exp2_approx(m[n][r] - (big - kBias));
+                            m[n][r] = big - kBias;
+                        }
+                        const bool up = big_v > w[n][r] + kLimit;
+                        const float f = up ? exp2_approx(w[n][r] - (big_v - kBias)) : 1.f;
+                        if (up) w[n][r] = big_v - kBias;
+#pragma unroll
+                        for (int g = 0; g < D / 16; ++g) {
+                            o[n][g][r] *= f;
+                            o[n][g][2 + r] *= f;
+                        }
+                    }
+                exponents();
+            }
+            uint32_t pb[NT][2];  // weights of keys 0-7 and 8-15, keys along the registers
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) l[n][r] += exp2_approx(xm[n][r]) + exp2_approx(xm[n][2 + r]);
+                pb[n][0] = transpose8(f32x2_to_f16x2(exp2_approx(xv[n][0]), exp2_approx(xv[n][1])));
+                pb[n][1] = transpose8(f32x2_to_f16x2(exp2_approx(xv[n][2]), exp2_approx(xv[n][3])));
+            }
+            const uint32_t vs = base + x.stage * S::kStage + S::kHalf;
+            const int v_row = warp * kWarpKeys + (lane & 15), v_piece = lane >> 4;
+            uint32_t codes[D / 32][4];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) ldsm_x4_trans(vs + piece_at<D>(v_row, 2 * c + v_piece), codes[c]);
+            // two keys' codes of dimensions 2i and 2i + 1: of 16 dimensions keys
+            // 0-7 and 8-15, then of the next 16
+#pragma unroll
+            for (int g = 0; g < D / 16; ++g) {
+                uint32_t a[4];  // even dimensions, odd ones; then of the later keys
+                e4m3x4_to_f16x2(__byte_perm(codes[g / 2][2 * (g & 1)], 0, 0x3120), a[0], a[1]);
+                e4m3x4_to_f16x2(__byte_perm(codes[g / 2][2 * (g & 1) + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(o[n][g], a, pb[n][0], pb[n][1]);
+            }
+            if (ragged) fence_proxy_async_shared();
+        };
+        // (Scores of the next tile computed ahead, two tiles at a time, and the two
+        // warps of a scheduler taking turns at the products all took more time, at
+        // any number of rows: what bounds the loop beside HBM is the rate at which
+        // two warps a scheduler fetch and issue its instructions.)
+        for (int t = walk.t0; t < walk.t1; ++t) {
+            if (!wait(full + 8 * stage, parity)) break;
+            Scores x = product(t, stage);
+            if (x.needed) finish(x);
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * stage);
             if (++stage == S::kStages) {
@@ -497,38 +534,47 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
                 if (quad == 0) stat[warp * kRows + n * 8 + 2 * pair + r] = make_float2(m[n][r], l[n][r]);
             }
         warps_sync(1, kConsumers * 32);
+        {
+            // (eight threads a row; rows past the item's last give anything. Code
+            // that runs once an item comes from beyond the instruction cache: it
+            // is kept short.)
+            const float2 own = stat[(tid & 7) * kRows + (tid >> 3)];
+            float mx = own.x;
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            float sum = own.y * exp2_approx(own.x - mx);
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if ((tid & 7) == 0) total[tid >> 3] = make_float2(mx, sum);
+        }
+        warps_sync(1, kConsumers * 32);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = n * 8 + 2 * pair + r;
-                float mx = -INFINITY, tot = 0.f;
-#pragma unroll
-                for (int x = 0; x < kConsumers; ++x) mx = fmaxf(mx, stat[x * kRows + row].x);
-#pragma unroll
-                for (int x = 0; x < kConsumers; ++x) tot += stat[x * kRows + row].y * exp2_approx(stat[x * kRows + row].x - mx);
-                m[n][r] = mx;
-                l[n][r] = tot;
                 // (nothing was seen: 0 times infinity is not 0)
-                const float f = w[n][r] == kNone ? 1.f : exp2_approx(w[n][r] - mx);
+                const float f = w[n][r] == kNone ? 1.f : exp2_approx(w[n][r] - total[n * 8 + 2 * pair + r].x);
 #pragma unroll
                 for (int g = 0; g < D / 16; ++g) {
                     o[n][g][r] *= f;
                     o[n][g][2 + r] *= f;
                 }
             }
+#pragma unroll 1
         for (int x = 0; x < kConsumers; ++x) {
             auto slice = [&](auto which) {
                 constexpr int e = decltype(which)::value;
                 constexpr bool kHalves = D == 64;  // of the rows, by their low bit
                 constexpr int g = kHalves ? e >> 1 : e;
                 if ((warp ^ x) != e) return;
+                // row 2 pair, and from it the others at fixed distances
+                float* at = merge + 2 * pair * D + (((2 * g + (quad >> 2)) ^ pair) << 3) + 2 * (quad & 3);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         if (kHalves && r != (e & 1)) continue;
-                        float2* to = reinterpret_cast<float2*>(merged(n * 8 + 2 * pair + r, 2 * g + (quad >> 2)) + 2 * (quad & 3));
+                        float2* to = reinterpret_cast<float2*>(at + (n * 8 + r) * D);
                         const float2 u = x > 0 ? *to : make_float2(0.f, 0.f);
                         *to = make_float2(u.x + o[n][g][r], u.y + o[n][g][2 + r]);
                     }
@@ -541,12 +587,6 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
             slice(std::integral_constant<int, 5>{});
             slice(std::integral_constant<int, 6>{});
             slice(std::integral_constant<int, 7>{});
-            // (everyone has read the statistics by the first of these)
-            if (x == kConsumers - 1 && warp == 0 && quad == 0)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) stat[n * 8 + 2 * pair + r] = make_float2(m[n][r], l[n][r]);
             warps_sync(1, kConsumers * 32);
         }
     };
@@ -580,7 +620,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
                 const int g = lane * kWords + i, in = g & 7;  // pair of dimensions, in its group of 16
                 words[(g & ~7) + (in & 1) * 4 + (in >> 1)] = f32x2_to_f16x2(v[i].x * by, v[i].y * by);
             }
-            if (lane == 0) reinterpret_cast<float*>(sm + S::kOffRow)[row] = exp2i(-s) * p.scale_log2;
+            if (lane == 0) reinterpret_cast<float*>(sm + S::kOffRow)[row] = fminf(fmaxf(exp2i(-s) * p.scale_log2 * 0x1p24f, 1.2e-38f), 3e38f);
         }
         warps_sync(1, kConsumers * 32);
         if (walk.rows <= 8) item(std::integral_constant<int, 1>{});
@@ -596,12 +636,13 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
         // 16 bytes of output a thread
         const bool whole = walk.whole();
         float* part = p.part + ((int64_t)blockIdx.x * 2 + walk.part()) * attn_part_floats(kRows, D);
+#pragma unroll 1
         for (int i = tid; i < walk.rows * (D / 8); i += kConsumers * 32) {
             const int row = i / (D / 8), c = i % (D / 8);
             const float4* sum = reinterpret_cast<const float4*>(merged(row, c));
             const float4 x = sum[0], y = sum[1];
             if (whole) {
-                const float2 ml = stat[row];
+                const float2 ml = total[row];
                 const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
                 const int R = walk.row0 + row, t = token_of(p, R), h = walk.head * p.group + (R - t * p.group);
                 const int64_t at_row = (int64_t)(walk.q.q0 + t) * p.heads + h;
@@ -615,7 +656,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
             } else {
                 *reinterpret_cast<float4*>(part + row * D + c * 8) = x;
                 *reinterpret_cast<float4*>(part + row * D + c * 8 + 4) = y;
-                if (c == 0) reinterpret_cast<float2*>(part + kRows * D)[row] = stat[row];
+                if (c == 0) reinterpret_cast<float2*>(part + kRows * D)[row] = total[row];
             }
         }
         // the next item writes the rows and the statistics after this barrier
@@ -629,7 +670,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
             }
             warps_sync(1, kConsumers * 32);
             if (join_info[2])
-                join_parts<D, DT>(p, Span{join_info[0], join_info[1]}, walk.rows, walk.row0, walk.head, walk.q.q0, stat, tid);
+                join_parts<D, DT>(p, Span{join_info[0], join_info[1]}, walk.rows, walk.row0, walk.head, walk.q.q0, total, tid);
             warps_sync(1, kConsumers * 32);
         }
     }

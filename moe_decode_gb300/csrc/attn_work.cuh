@@ -127,7 +127,7 @@ struct Few {
 };
 // (over a cache of 8-bit values one kernel takes every request)
 struct All {
-    static constexpr int kRows = kAttnRows, kItem = 2;
+    static constexpr int kRows = kAttnRows, kItem = 5;
     static __device__ __forceinline__ bool mine(const AttnParams& p, const Request& q) { return q.n > 0; }
 };
 struct Many {
