@@ -20,6 +20,8 @@
 // 900 of hand-overs and of waiting for shared memory, which brings the 128
 // bytes a clock that Q K^T with both operands from it wants (without any
 // softmax the call takes 2.17 ms).
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace moe {
@@ -116,6 +118,7 @@ template <int D, int DT, bool TREE>
 __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_constant__ AttnParams p,
                                                                   const __grid_constant__ CUtensorMap kmap,
                                                                   const __grid_constant__ CUtensorMap vmap) {
+    using Class = std::conditional_t<TREE, ManyTree, Many>;
     using S = ChunkShape<D>;
     extern __shared__ uint8_t dyn[];
     __shared__ int64_t scan[kThreads / 32];
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
     // so the two overlap (all reads go to the L2, where what came before is).
     // The wait at the end keeps the order for what follows.
     pdl_launch_dependents();
-    const Place at = attn_place<Many, kThreads>(p, blockIdx.x, scan, &found);
+    const Place at = attn_place<Class, kThreads>(p, blockIdx.x, scan, &found);
     if (at.begin >= at.end) {
         pdl_wait();
         return;
@@ -175,7 +178,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             int stage = 0, issued = 0;
             uint32_t parity = 1;
             bool ok = true;
-            TileFeed<Many> feed(p, at, lane);
+            TileFeed<Class> feed(p, at, lane);
             auto cur = feed.box(), next = cur;
             for (bool more = feed.any; ok && more; cur = next) {
                 more = feed.advance();
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
             __syncwarp();
         } else if (warp == kMmaWarp) {
             if (lane == 0) {
-                Walk<Many> walk(p, at);
+                Walk<Class> walk(p, at);
                 uint32_t pos = 0;  // stages consumed
                 uint32_t q_par = 0, p_par = 0;  // parity bits by slot
                 bool ok = true;
@@ -267,7 +270,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_chunk_kernel(const __grid_co
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        Walk<Many> walk(p, at);
+        Walk<Class> walk(p, at);
         const int slot = warp >> 2, t = tid & (kSlotRows - 1);
         const int row = t;  // of the slot: that of the warp's lanes of tensor memory
         auto piece_at = [&](int slot, int row, int c) {  // 16 bytes of a slot's row

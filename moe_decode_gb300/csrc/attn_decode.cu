@@ -1,5 +1,7 @@
 // Attention of few query rows over the paged cache: decoding streams, verify
 // chains and short chunks.
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace moe {
@@ -74,6 +76,7 @@ template <int D, int DT, bool TREE>
 __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_constant__ AttnParams p,
                                                                    const __grid_constant__ CUtensorMap kmap,
                                                                    const __grid_constant__ CUtensorMap vmap) {
+    using Class = std::conditional_t<TREE, FewTree, Few>;
     using S = DecodeShape<D>;
     // (no static shared memory: this begins on a 1024-byte boundary, which the
     // swizzle counts from)
@@ -101,7 +104,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
     }
     pdl_wait();
     pdl_launch_dependents();
-    const Place at = attn_place<Few, kThreads>(p, blockIdx.x, scan, found);
+    const Place at = attn_place<Class, kThreads>(p, blockIdx.x, scan, found);
     // padding rows
     for (int64_t i = (int64_t)min(max(p.q_start[p.B], 0), p.T) * p.heads + blockIdx.x + (int64_t)p.G * warp;
          i < (int64_t)p.T * p.heads; i += (int64_t)p.G * (kThreads / 32)) {
@@ -116,7 +119,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
         // producer: lane i brings the tile's i-th box, if a row sees any of it
         int stage = 0, issued = 0;
         uint32_t parity = 1, items = 0;
-        TileFeed<Few> feed(p, at, lane);
+        TileFeed<Class> feed(p, at, lane);
         auto cur = feed.box(), next = cur;
         for (bool more = feed.any; more; cur = next) {
             more = feed.advance();
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_decode_kernel(const __grid_c
         return;
     }
 
-    Walk<Few> walk(p, at);
+    Walk<Class> walk(p, at);
     const int quad = lane >> 2, pair = lane & 3;
     const int set = warp / kKeyWarps, kw = warp % kKeyWarps;  // rows [16 set, 16 set + 16), a quarter of the keys
     // a key's row in a stage: boxes of `box` keys, in each the panels of 64

@@ -137,6 +137,17 @@ struct Many {
     }
 };
 
+// The same in a call with trees, where an item counts for what it costs: some six
+// tiles of 256 rows (24 trees of 33 to 64 tokens over 200 to 12,000 keys take
+// 213 us with two), five of 32. (The calls without keep their division, and with
+// it the order in which parts are added up.)
+struct FewTree : Few {
+    static constexpr int kItem = 5;
+};
+struct ManyTree : Many {
+    static constexpr int kItem = 6;
+};
+
 // A place in the order of units, and the CTA's range.
 struct Start {
     int request, head, row0;

@@ -10,6 +10,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxPairs = 256;  // of a head of 512 dimensions
+// Rounds whose loads are on their way together, and CTAs of an SM: 8,192 tokens of
+// 32 and 8 heads of 128 take 34.8 us with (4, 2), 32.2 with (2, 3), 28.2 with (2, 4).
+constexpr int kRounds = 2, kCtas = 4;
 
 __device__ __forceinline__ void report_slot(unsigned* ctrl) {
     atomicCAS(reinterpret_cast<int*>(ctrl + kCtlStatus), 0, -100 /* MOE_EDEVICE_BAD_INDEX */);
@@ -63,7 +66,7 @@ __device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
 // rounds. With a cache of codes the head's lanes find its largest magnitude by
 // shuffles.
 template <int DT, int TO>
-__global__ __launch_bounds__(kThreads) void rotate_kernel(const __grid_constant__ RotateParams p) {
+__global__ __launch_bounds__(kThreads, kCtas) void rotate_kernel(const __grid_constant__ RotateParams p) {
     __shared__ float2 table[kWarps][kMaxPairs];
     pdl_wait();
     pdl_launch_dependents();
@@ -82,34 +85,20 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(const __grid_constant_
     for (int64_t w = (int64_t)blockIdx.x * kWarps + warp; w < all; w += step) {
         const int t = (int)(w / p.split), part = (int)(w - (int64_t)t * p.split);
         const int pos = p.positions ? p.positions[t] : 0;
+        int slot = TO != kRotateRows ? p.slots[t] : -1;
         if (pos < 0) continue;
-        int slot = -1;
-        if (TO != kRotateRows) {
-            slot = p.slots[t];
-            if (slot < -1 || slot >= p.n_slots) {
-                if (lane == 0 && part == 0) report_slot(p.ctrl);
-                slot = -1;
-            }
+        if (TO != kRotateRows && (slot < -1 || slot >= p.n_slots)) {
+            if (lane == 0 && part == 0) report_slot(p.ctrl);
+            slot = -1;
         }
         const int block = slot < 0 ? 0 : slot / p.block_size, token = slot < 0 ? 0 : slot - block * p.block_size;
-        float2 cs[8];
-        if (p.positions) {
-            __syncwarp();
-            for (int j = lane; j < p.rotary_dim / 2; j += 32) {
-                const float2 c = turn((uint32_t)(((unsigned long long)(unsigned)pos * __ldg(p.turns + j)) >> 32));
-                table[warp][j] = make_float2(c.x * p.scale, c.y * p.scale);
-            }
-            __syncwarp();
-            if (turns)
+        // `kRounds` rounds from r0 on: which head this lane has of each (kind 0
+        // queries, 1 keys, 2 values, -1 nothing), and its pieces on their way
+        uint4 a[kRounds], b[kRounds];
+        int kind[kRounds], head[kRounds];
+        auto load = [&](int r0) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) cs[j] = table[warp][8 * i + j];
-        }
-        constexpr int U = 4;  // rounds whose loads are in flight together
-        for (int r0 = part; r0 < rounds; r0 += U * p.split) {
-            uint4 a[U], b[U];
-            int kind[U], head[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < kRounds; ++u) {
                 const int r = r0 + u * p.split;
                 int h = r * p.per + sub;
                 kind[u] = -1;
@@ -136,8 +125,24 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(const __grid_constant_
                     b[u] = *reinterpret_cast<const uint4*>(s + at1);
                 }
             }
+        };
+        load(part);
+        float2 cs[8];
+        if (p.positions) {
+            __syncwarp();
+            for (int j = lane; j < p.rotary_dim / 2; j += 32) {
+                const float2 c = turn((uint32_t)(((unsigned long long)(unsigned)pos * __ldg(p.turns + j)) >> 32));
+                table[warp][j] = make_float2(c.x * p.scale, c.y * p.scale);
+            }
+            __syncwarp();
+            if (turns)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+                for (int j = 0; j < 8; ++j) cs[j] = table[warp][8 * i + j];
+        }
+        for (int r0 = part; r0 < rounds; r0 += kRounds * p.split) {
+            if (r0 != part) load(r0);
+#pragma unroll
+            for (int u = 0; u < kRounds; ++u) {
                 const int k = kind[u];
                 uint32_t* x = reinterpret_cast<uint32_t*>(&a[u]);
                 uint32_t* y = reinterpret_cast<uint32_t*>(&b[u]);
@@ -173,7 +178,7 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(const __grid_constant_
                     *reinterpret_cast<uint4*>(row + 2 * at0) = a[u];
                     *reinterpret_cast<uint4*>(row + 2 * at1) = b[u];
                 }
-                if (TO == kRotateCache8) {
+                if (TO == kRotateCache8 && __any_sync(0xffffffffu, k > 0)) {
                     // the largest magnitude of the head, of bits without their
                     // signs, in which NaN comes above infinity above all others
                     float2 f[8];
@@ -285,14 +290,15 @@ cudaError_t launch_pdl(void (*kern)(P), int grid, const P& p, cudaStream_t strea
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Few tokens are shared by as many warps as have a round each; many have a warp
-// each.
-int split_of(int T, int rounds, int sms) {
-    const int64_t want = ((int64_t)sms * 16 + T - 1) / T;
+// Few tokens are shared by as many warps as have a round each, many by two or
+// three: `warps` of an SM are wanted. (8,192 tokens into e4m3 codes: 43.6 us with
+// 16, 41.2 with 160, 60.8 with 400, where each computes the angles.)
+int split_of(int T, int rounds, int sms, int warps) {
+    const int64_t want = ((int64_t)sms * warps + T - 1) / T;
     return (int)(want > rounds ? rounds : want);
 }
-int grid_of(int64_t warps, int sms) {
-    const int64_t want = (warps + kWarps - 1) / kWarps, most = (int64_t)sms * 8;
+int grid_of(int64_t warps, int64_t most) {
+    const int64_t want = (warps + kWarps - 1) / kWarps;
     return (int)(want > most ? most : want);
 }
 
@@ -302,8 +308,8 @@ cudaError_t launch_rotate(RotateParams p, int to, int dtype, int sms, cudaStream
     p.lanes = p.head_dim / 16;
     p.per = 32 / p.lanes;
     const int heads = p.heads[0] + p.heads[1] + p.heads[2], rounds = (heads + p.per - 1) / p.per;
-    p.split = split_of(p.T, rounds, sms);
-    const int grid = grid_of((int64_t)p.T * p.split, sms);
+    p.split = split_of(p.T, rounds, sms, 160);
+    const int grid = grid_of((int64_t)p.T * p.split, (int64_t)sms * 8);
     if (dtype == 0) {
         if (to == kRotateRows) return launch_pdl(rotate_kernel<0, kRotateRows>, grid, p, stream);
         if (to == kRotateCache16) return launch_pdl(rotate_kernel<0, kRotateCache16>, grid, p, stream);
@@ -316,8 +322,9 @@ cudaError_t launch_rotate(RotateParams p, int to, int dtype, int sms, cudaStream
 
 cudaError_t launch_read(ReadParams p, int from, int dtype, int sms, cudaStream_t stream) {
     const int rounds = ((2 * p.heads << p.lane_shift) + 31) / 32;
-    p.split = split_of(p.T, rounds, sms);
-    const int grid = grid_of((int64_t)p.T * p.split, sms);
+    p.split = split_of(p.T, rounds, sms, 64);
+    // (CTAs without a second token: 65,521 tokens 63.5 us, 69.3 by 8 an SM in turn)
+    const int grid = grid_of((int64_t)p.T * p.split, (int64_t)sms * 64);
     if (from == 0) return launch_pdl(read_kernel<0, 0>, grid, p, stream);
     return dtype == 0 ? launch_pdl(read_kernel<1, 0>, grid, p, stream) : launch_pdl(read_kernel<1, 1>, grid, p, stream);
 }

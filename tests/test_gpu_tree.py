@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from paged_util import attention as plain_attention
 from paged_util import check_attention, make_step
 from tree_util import attention, plan, random_parents
 
@@ -132,15 +133,19 @@ def test_attention_under_any_masks(api, ctas):
 
 
 @pytest.mark.parametrize("lens,page,heads,kv,d,dtype,layout", CASES)
-def test_chains_are_what_they_were(api, lens, page, heads, kv, d, dtype, layout):
-    """A tree without branches gives the plain call's results bit for bit."""
+def test_chains_are_the_plain_call(api, lens, page, heads, kv, d, dtype, layout):
+    """A tree without branches, and the plain call on the same inputs, against
+    the same reference (their work is divided differently, so sums over keys are
+    joined in other places)."""
     s = make_step(lens, page, heads, kv, d, dtype, 5, layout)
     masks = plan([list(range(-1, n - 1)) for _, n in lens], lens)[0]
     out, lse = run(api, s, i64(masks))
     cache = api.KvCache(s["k"], s["v"])
     ws, out2, lse2 = api.paged_workspace(heads, cache), torch.empty_like(out), torch.empty_like(lse)
     api.paged_attention(s["q"], cache, s["table"], s["q_start"], s["seq"], out2, ws, lse=lse2)
-    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    ref = plain_attention(s)
+    check_attention(out, lse, ref)
+    check_attention(out2, lse2, ref)
 
 
 def test_captured_and_replayed_at_other_trees(api):
