@@ -445,21 +445,33 @@ def tree_plan(parents, q_start, seq_lens, masks, positions, ws, stream=None):
         raise MoeError(rc, "moe_tree_plan")
 
 
-def _strides(t: torch.Tensor, least: int = 0):
-    """Token and head strides of [T, heads, d]; a dimension of one element has
-    no stride of its own."""
-    T, heads, d = t.shape
-    a, b, _ = t.stride()
-    own = (d + 7) // 8 * 8
-    return (a if T > 1 else max(least, own) * heads if least else 0), (b if heads > 1 else own if least else 0)
+def _rows(what: str, dev: int, dtype: torch.dtype, shape, t: torch.Tensor, out: bool = False):
+    """(address, token stride, head stride) of [T, heads, d] on the current
+    device. A dimension of one element has no stride of its own: 0, or of an
+    output one that its rows would have."""
+    strides = t.stride()
+    if t.shape != shape:
+        raise MoeError(ESHAPE, f"{what}: {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != dev or strides[2] != 1:
+        raise MoeError(EINVAL, f"{what}: {dtype}, the last dimension contiguous, on the current device; got {t.dtype} on {t.device}")
+    token, head = strides[0], strides[1]
+    if shape[1] == 1:
+        head = (shape[2] + 7) // 8 * 8 if out else 0
+    if shape[0] == 1:
+        token = (shape[2] + 7) // 8 * 8 * shape[1] if out else 0
+    return t.data_ptr(), token, head
 
 
-def _rows(what: str, dev: int, dtype: torch.dtype, shape, *tensors):
-    for t in tensors:
-        if t.shape != shape:
-            raise MoeError(ESHAPE, f"{what}: {tuple(shape)}, got {tuple(t.shape)}")
-        if t.dtype != dtype or t.get_device() != dev or t.stride(2) != 1:
-            raise MoeError(EINVAL, f"{what}: {dtype}, the last dimension contiguous, on the current device; got {t.dtype} on {t.device}")
+def _pair(what: str, dev: int, dtype: torch.dtype, shape, t: torch.Tensor, out: Optional[torch.Tensor]):
+    """_rows of an input and of its output, which is the input's place without one."""
+    o = _rows(what, dev, dtype, shape, t if out is None else out, True)
+    if out is None or out is t:
+        return (*o, *o)
+    i = _rows(what, dev, dtype, shape, t)
+    return (*(o if i[0] == o[0] and (shape[0] == 1 or i[1] == o[1]) and (shape[1] == 1 or i[2] == o[2]) else i), *o)
+
+
+_NO_PAIR = (None, 0, 0, None, 0, 0)
 
 
 def paged_append(k_new, v_new, slot_map, cache, ws, stream=None):
@@ -538,29 +550,18 @@ def rope(q, k, positions, angles: Rope, q_out=None, k_out=None, stream=None):
     position stay as they are."""
     T, heads, d = q.shape
     dev = _device("rope", q)
-    _want(q.dtype in DTYPES, "rope: q bf16 or fp16")
-    q_out = q if q_out is None else q_out
-    _rows("rope: q, q_out", dev, q.dtype, q.shape, q, q_out)
-    qt, qh = _strides(q)
-    ot, oh = _strides(q_out, d)
-    if q_out.data_ptr() == q.data_ptr():
-        qt, qh = (ot if T == 1 else qt), (oh if heads == 1 else qh)
-    kv, kp, ko, kt, kh, pt, ph = 0, None, None, 0, 0, 0, 0
+    dtype = q.dtype
+    _want(dtype in DTYPES, "rope: q bf16 or fp16")
+    qs = _pair("rope: q, q_out", dev, dtype, q.shape, q, q_out)
+    kv, ks = 0, _NO_PAIR
     if k is not None:
         kv = k.shape[1]
-        k_out = k if k_out is None else k_out
-        _rows("rope: k, k_out", dev, q.dtype, (T, kv, d), k, k_out)
-        kt, kh = _strides(k)
-        pt, ph = _strides(k_out, d)
-        if k_out.data_ptr() == k.data_ptr():
-            kt, kh = (pt if T == 1 else kt), (ph if kv == 1 else kh)
-        kp, ko = k.data_ptr(), k_out.data_ptr()
+        ks = _pair("rope: k, k_out", dev, dtype, (T, kv, d), k, k_out)
     else:
         _want(k_out is None, "rope: k_out without k")
     _vectors("rope: positions", dev, torch.int32, (positions, T))
     _want(angles.device_index == dev, "rope: angles on the current device")
-    rc = lib.moe_rope(q.data_ptr(), qt, qh, q_out.data_ptr(), ot, oh, heads, kp, kt, kh, ko, pt, ph, kv, T, d,
-                      DTYPES[q.dtype], positions.data_ptr(), angles._ref, _raw_stream(stream, dev))
+    rc = lib.moe_rope(*qs, heads, *ks, kv, T, d, DTYPES[dtype], positions.data_ptr(), angles._ref, _raw_stream(stream, dev))
     if rc:
         raise MoeError(rc, "moe_rope")
 
@@ -577,24 +578,17 @@ def paged_rope_append(q, k_new, v_new, positions, slot_map, angles: Rope, cache,
     dtype = k_new.dtype if codes else cache.dtype
     _want(dtype in DTYPES and cache.device_index == dev and angles.device_index == dev,
           "paged_rope_append: bf16 or fp16, cache and angles on the current device")
-    _rows("paged_rope_append: k_new, v_new", dev, dtype, (T, cache.kv_heads, d), k_new, v_new)
-    kt, kh = _strides(k_new)
-    vt, vh = _strides(v_new)
-    heads, qp, op, qt, qh, ot, oh = 0, None, None, 0, 0, 0, 0
+    ks = _rows("paged_rope_append: k_new, v_new", dev, dtype, (T, cache.kv_heads, d), k_new)
+    vs = _rows("paged_rope_append: k_new, v_new", dev, dtype, (T, cache.kv_heads, d), v_new)
+    heads, qs = 0, _NO_PAIR
     if q is not None:
-        q_out = q if q_out is None else q_out
         heads = q.shape[1]
-        _rows("paged_rope_append: q, q_out", dev, dtype, (T, heads, d), q, q_out)
-        qt, qh = _strides(q)
-        ot, oh = _strides(q_out, d)
-        if q_out.data_ptr() == q.data_ptr():
-            qt, qh = (ot if T == 1 else qt), (oh if heads == 1 else qh)
-        qp, op = q.data_ptr(), q_out.data_ptr()
+        qs = _pair("paged_rope_append: q, q_out", dev, dtype, (T, heads, d), q, q_out)
     else:
         _want(q_out is None, "paged_rope_append: q_out without q")
     _vectors("paged_rope_append: positions, slot_map", dev, torch.int32, (positions, T), (slot_map, T))
     _workspace("paged_rope_append", dev, ws)
-    args = (qp, qt, qh, op, ot, oh, heads, k_new.data_ptr(), kt, kh, v_new.data_ptr(), vt, vh, T)
+    args = (*qs, heads, *ks, *vs, T)
     rest = (positions.data_ptr(), slot_map.data_ptr(), angles._ref, cache._ref, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     rc = lib.moe_paged_rope_append8(*args, DTYPES[dtype], *rest) if codes else lib.moe_paged_rope_append(*args, *rest)
     if rc:
@@ -610,12 +604,11 @@ def paged_read(cache, slot_map, k_out, v_out, ws, stream=None):
     codes = isinstance(cache, KvCache8)
     dtype = k_out.dtype if codes else cache.dtype
     _want(dtype in DTYPES and cache.device_index == dev, "paged_read: bf16 or fp16, cache on the current device")
-    _rows("paged_read: k_out, v_out", dev, dtype, (T, cache.kv_heads, cache.head_dim), k_out, v_out)
+    shape = (T, cache.kv_heads, cache.head_dim)
+    ks, vs = (_rows("paged_read: k_out, v_out", dev, dtype, shape, t, True) for t in (k_out, v_out))
     _vectors("paged_read: slot_map", dev, torch.int32, (slot_map, T))
     _workspace("paged_read", dev, ws)
-    kt, kh = _strides(k_out, cache.head_dim)
-    vt, vh = _strides(v_out, cache.head_dim)
-    out = (k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    out = (*ks, *vs, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if codes:
         rc = lib.moe_paged_read8(cache._ref, slot_map.data_ptr(), T, DTYPES[dtype], *out)
     else:

@@ -126,12 +126,13 @@ int append(const Rows& q, const Rows& q_out, int q_heads, const Rows& k, const R
            const int32_t* positions, const int32_t* slot_map, const moe_rope_angles* angles, bool rotate,
            const Cache* cache, int to, void* ws, size_t ws_bytes, void* stream) {
     if (T < 0 || (dtype != 0 && dtype != 1)) return MOE_ESHAPE;
-    if (q_heads < 0 || q_heads > 1024 || ((q.p != nullptr) != (q_heads > 0))) return MOE_ESHAPE;
+    if (q_heads < 0 || q_heads > 1024) return MOE_ESHAPE;
     if (rotate) {
         const int rc = check_angles(angles, cache->head_dim);
         if (rc) return rc;
     }
     if (T == 0) return MOE_OK;
+    if ((q.p != nullptr) != (q_heads > 0)) return MOE_ESHAPE;
     if (!slot_map || (rotate && !positions)) return MOE_EINVAL;
     int rc = check_rows(k);
     if (rc == MOE_OK) rc = check_rows(v);
@@ -257,9 +258,9 @@ int moe_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, void*
     if (head_dim < 16 || head_dim % 16 != 0 || head_dim > 512 || (dtype != 0 && dtype != 1)) return MOE_ESHAPE;
     int rc = check_angles(angles, head_dim);
     if (rc) return rc;
-    if (T < 0 || q_heads < 1 || q_heads > 1024 || kv_heads < 0 || kv_heads > 1024 || ((k != nullptr) != (kv_heads > 0)))
-        return MOE_ESHAPE;
+    if (T < 0 || q_heads < 1 || q_heads > 1024 || kv_heads < 0 || kv_heads > 1024) return MOE_ESHAPE;
     if (T == 0) return MOE_OK;
+    if ((k != nullptr) != (kv_heads > 0)) return MOE_ESHAPE;
     const Rows qs{q, q_token_stride, q_head_stride}, qo{q_out, q_out_token_stride, q_out_head_stride};
     const Rows ks{k, k_token_stride, k_head_stride}, ko{k_out, k_out_token_stride, k_out_head_stride};
     rc = check_pair(qs, qo, head_dim);
