@@ -222,8 +222,9 @@ __global__ __launch_bounds__(kTreeThreads) void tree_plan_kernel(TreeParams p) {
             if (p.positions) p.positions[q0 + tid] = pos0 + __popcll(mine) - 1;
         }
     }
-    // padding rows
-    for (int64_t t = (int64_t)max(p.q_start[p.B], 0) + blockIdx.x * kTreeThreads + tid; t < p.T; t += (int64_t)gridDim.x * kTreeThreads) {
+    // padding rows (none are known where the last request is placed wrongly)
+    const int end = p.q_start[p.B];
+    for (int64_t t = (int64_t)(end < max(p.q_start[p.B - 1], 0) ? p.T : end) + blockIdx.x * kTreeThreads + tid; t < p.T; t += (int64_t)gridDim.x * kTreeThreads) {
         p.masks[t] = 0;
         if (p.positions) p.positions[t] = -1;
     }

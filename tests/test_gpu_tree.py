@@ -70,12 +70,14 @@ def test_plan_of_wrong_parents(api, bad):
     assert masks.tolist() == [1, 3, 7, 8, 24] and positions.tolist() == [5, 6, 7, 5, 6]
 
 
-@pytest.mark.parametrize("q_start,seq", [([0, 9, 3], [5, 5]), ([-1, 2, 3], [5, 5]), ([0, 2, 900], [5, 5]), ([0, 2, 3], [-4, 5])])
+@pytest.mark.parametrize("q_start,seq", [([0, 2, -1], [5, 5]), ([0, 3, 2], [5, 5]), ([0, 9, 3], [5, 5]), ([-1, 2, 3], [5, 5]), ([0, 2, 900], [5, 5]), ([0, 2, 3], [-4, 5])])
 def test_plan_of_wrong_requests(api, q_start, seq):
     """Rows of the request that is placed wrongly stay as they are."""
     masks, positions, ws = i64([9] * 4), i32([9] * 4), api.paged_workspace()
     api.tree_plan(i32([-1, 0, -1, 0]), i32(q_start), i32(seq), masks, positions, ws)
     assert api.read_status(ws) == api.EDEVICE_BAD_INDEX
+    if q_start in ([0, 2, -1], [0, 3, 2]):  # and what is padding is not known
+        assert masks.tolist() == [1, 3] + ([9, 9] if q_start[1] == 2 else [4, 9])
     if q_start == [0, 2, 3]:
         assert masks.tolist() == [9, 9, 1, 0] and positions.tolist() == [9, 9, 4, -1]
 
