@@ -9,7 +9,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxPairs = 256;  // of a head of 512 dimensions
+constexpr int kPitch = 33;  // an eighth of the pairs of a head of 512 dimensions, and one
 // Rounds whose loads are on their way together, and CTAs of an SM: 8,192 tokens of
 // 32 and 8 heads of 128 take 34.8 us with (4, 2), 32.2 with (2, 3), 28.2 with (2, 4).
 constexpr int kRounds = 2, kCtas = 4;
@@ -67,7 +67,8 @@ __device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
 // shuffles.
 template <int DT, int TO>
 __global__ __launch_bounds__(kThreads, kCtas) void rotate_kernel(const __grid_constant__ RotateParams p) {
-    __shared__ float2 table[kWarps][kMaxPairs];
+    // pair 8 i + j at j * kPitch + i: lanes of a head read neighbours
+    __shared__ float2 table[kWarps][8 * kPitch];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -92,10 +93,15 @@ __global__ __launch_bounds__(kThreads, kCtas) void rotate_kernel(const __grid_co
             slot = -1;
         }
         const int block = slot < 0 ? 0 : slot / p.block_size, token = slot < 0 ? 0 : slot - block * p.block_size;
+        uint8_t* to[2] = {};
+        if (TO != kRotateRows)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) to[n] = p.cache[n] + block * p.cache_block[n] + token * p.cache_token[n];
         // `kRounds` rounds from r0 on: which head this lane has of each (kind 0
         // queries, 1 keys, 2 values, -1 nothing), and its pieces on their way
         uint4 a[kRounds], b[kRounds];
         int kind[kRounds], head[kRounds];
+        const uint16_t* const from[3] = {p.src[0] + t * p.src_token[0], p.src[1] + t * p.src_token[1], p.src[2] + t * p.src_token[2]};
         auto load = [&](int r0) {
 #pragma unroll
             for (int u = 0; u < kRounds; ++u) {
@@ -118,8 +124,7 @@ __global__ __launch_bounds__(kThreads, kCtas) void rotate_kernel(const __grid_co
                 a[u] = b[u] = make_uint4(0, 0, 0, 0);
                 if (kind[u] >= 0) {
                     const int k = kind[u];
-                    const uint16_t* s = (k == 0 ? p.src[0] : k == 1 ? p.src[1] : p.src[2]) +
-                                        t * (k == 0 ? p.src_token[0] : k == 1 ? p.src_token[1] : p.src_token[2]) +
+                    const uint16_t* s = (k == 0 ? from[0] : k == 1 ? from[1] : from[2]) +
                                         h * (k == 0 ? p.src_head[0] : k == 1 ? p.src_head[1] : p.src_head[2]);
                     a[u] = *reinterpret_cast<const uint4*>(s + at0);
                     b[u] = *reinterpret_cast<const uint4*>(s + at1);
@@ -132,12 +137,12 @@ __global__ __launch_bounds__(kThreads, kCtas) void rotate_kernel(const __grid_co
             __syncwarp();
             for (int j = lane; j < p.rotary_dim / 2; j += 32) {
                 const float2 c = turn((uint32_t)(((unsigned long long)(unsigned)pos * __ldg(p.turns + j)) >> 32));
-                table[warp][j] = make_float2(c.x * p.scale, c.y * p.scale);
+                table[warp][(j & 7) * kPitch + (j >> 3)] = make_float2(c.x * p.scale, c.y * p.scale);
             }
             __syncwarp();
             if (turns)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) cs[j] = table[warp][8 * i + j];
+                for (int j = 0; j < 8; ++j) cs[j] = table[warp][j * kPitch + i];
         }
         for (int r0 = part; r0 < rounds; r0 += kRounds * p.split) {
             if (r0 != part) load(r0);
@@ -171,27 +176,20 @@ __global__ __launch_bounds__(kThreads, kCtas) void rotate_kernel(const __grid_co
                     if (TO != kRotateCache8) continue;
                 }
                 const int n = k == 2 ? 1 : 0;  // keys, values
-                uint8_t* row = nullptr;
-                if (TO != kRotateRows)
-                    row = p.cache[n] + block * p.cache_block[n] + token * p.cache_token[n] + head[u] * p.cache_head[n];
                 if (TO == kRotateCache16 && k > 0) {
+                    uint8_t* row = to[n] + head[u] * p.cache_head[n];
                     *reinterpret_cast<uint4*>(row + 2 * at0) = a[u];
                     *reinterpret_cast<uint4*>(row + 2 * at1) = b[u];
                 }
                 if (TO == kRotateCache8 && __any_sync(0xffffffffu, k > 0)) {
                     // the largest magnitude of the head, of bits without their
                     // signs, in which NaN comes above infinity above all others
-                    float2 f[8];
-                    uint32_t top = 0;
+                    uint32_t most = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        f[j] = widen<DT>(x[j]);
-                        f[4 + j] = widen<DT>(y[j]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        top = max(top, max(__float_as_uint(f[j].x) & 0x7fffffffu, __float_as_uint(f[j].y) & 0x7fffffffu));
-                    for (int o = 1; o < p.lanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    for (int j = 0; j < 4; ++j) most = __vmaxu2(most, __vmaxu2(x[j] & 0x7fff7fffu, y[j] & 0x7fff7fffu));
+                    most = max(most & 0xffffu, most >> 16);
+                    for (int o = 1; o < p.lanes; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    const uint32_t top = __float_as_uint(widen<DT>(most).x);
                     if (k > 0) {
                         // 448 is 1.75 * 2^8
                         int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
@@ -201,9 +199,11 @@ __global__ __launch_bounds__(kThreads, kCtas) void rotate_kernel(const __grid_co
                         uint32_t c[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            c[j] = finite ? codes4(make_float2(f[2 * j].x * by, f[2 * j].y * by),
-                                                   make_float2(f[2 * j + 1].x * by, f[2 * j + 1].y * by))
-                                          : 0u;
+                        {
+                            const float2 f = widen<DT>(j < 2 ? x[2 * j & 3] : y[2 * j & 3]), g = widen<DT>(j < 2 ? x[(2 * j + 1) & 3] : y[(2 * j + 1) & 3]);
+                            c[j] = finite ? codes4(make_float2(f.x * by, f.y * by), make_float2(g.x * by, g.y * by)) : 0u;
+                        }
+                        uint8_t* row = to[n] + head[u] * p.cache_head[n];
                         *reinterpret_cast<uint2*>(row + at0) = make_uint2(c[0], c[1]);
                         *reinterpret_cast<uint2*>(row + at1) = make_uint2(c[2], c[3]);
                         if (i == 0)
@@ -291,8 +291,8 @@ cudaError_t launch_pdl(void (*kern)(P), int grid, const P& p, cudaStream_t strea
 }
 
 // Few tokens are shared by as many warps as have a round each, many by two or
-// three: `warps` of an SM are wanted. (8,192 tokens into e4m3 codes: 43.6 us with
-// 16, 41.2 with 160, 60.8 with 400, where each computes the angles.)
+// three: `warps` of an SM are wanted. (8,192 tokens into e4m3 codes: 40.3 us with
+// 16, 38.0 with 160; with 400, where each computes the angles, half as much again.)
 int split_of(int T, int rounds, int sms, int warps) {
     const int64_t want = ((int64_t)sms * warps + T - 1) / T;
     return (int)(want > rounds ? rounds : want);
