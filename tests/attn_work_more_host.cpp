@@ -5,6 +5,32 @@
 #include "attn_work_host.cpp"
 #undef main
 
+// The CTAs that have tiles of an item are as many as its count says, one after
+// another from its first.
+template <class Class>
+static void parts(const AttnParams& p) {
+    Place at = {};
+    for (int r = 0; r < p.B; ++r) {
+        const Request q = attn_request(p, r);
+        if (Class::mine(p, q)) at.total += attn_request_units<Class>(p, q) * p.kv_heads;
+    }
+    std::map<std::tuple<int, int, int>, std::pair<int, int>> at_item;  // CTAs so far, their count
+    for (int cta = 0; cta < p.G; ++cta) {
+        attn_range(p, cta, at);
+        if (at.begin >= at.end) continue;
+        at.start = attn_seek<Class>(p, 0, p.B, at.begin);
+        for (Walk<Class> w(p, at); w.next(); w.done()) {
+            const Span s = attn_span(w, at);
+            auto& have = at_item[{w.r, w.head, w.row0}];
+            if (cta != s.cta + have.first) fail("a CTA between without a tile");
+            ++have.first;
+            have.second = s.parts;
+        }
+    }
+    for (const auto& i : at_item)
+        if (i.second.first != i.second.second) fail("a count of parts that is not that of the CTAs");
+}
+
 int main(int argc, char** argv) {
     if (host_main(argc, argv)) return 1;
     AttnParams p = {};
@@ -33,8 +59,11 @@ int main(int argc, char** argv) {
     unsigned status[64] = {};
     p.ctrl = status;
     readable = {{start.data(), start.size()}, {seq.data(), seq.size()}, {p.tables, entries}};
-    check<All>(p, lens);
     check<FewTree>(p, lens);
     check<ManyTree>(p, lens);
+    check<All>(p, lens);
+    parts<All>(p);
+    parts<FewTree>(p);
+    parts<ManyTree>(p);
     return 0;
 }
