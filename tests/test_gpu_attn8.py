@@ -228,3 +228,28 @@ def test_captured_and_replayed_at_other_lengths(api):
             check_attention8(out, None, paged_util.attention(s), 300)
     torch.cuda.current_stream().wait_stream(stream)
     assert api.read_status(ws) == 0
+
+
+def test_far_into_a_large_cache(api):
+    """Slots beyond 2^31 bytes of codes: written, rotated, read back and attended
+    over as at the beginning."""
+    heads, page, d, n_blocks = 8, 16, 128, 140000  # 2.3 GB of K, and of V
+    k, v = (torch.empty((n_blocks, page, heads, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty((n_blocks, heads, page), dtype=torch.uint8, device="cuda") for _ in range(2))
+    cache = api.KvCache8(k, v, ks, vs)
+    x = torch.randn((2, 40, heads, d), device="cuda").bfloat16()
+    positions, r = torch.arange(40, device="cuda").int(), api.Rope(d)
+    q = torch.randn((2, 32, d), device="cuda").bfloat16()
+    ws, got = api.paged_workspace(32, cache), []
+    for blocks in ([0, 2, 5], [n_blocks - 1, n_blocks - 2, n_blocks - 7]):
+        table = torch.tensor([blocks], dtype=torch.int32, device="cuda")
+        slots = (table[0].long()[positions.long() // page] * page + positions % page).int()
+        back, out = torch.empty_like(x), torch.empty_like(q)
+        api.paged_rope_append(None, x[0], x[1], positions, slots, r, cache, ws)
+        api.paged_read(cache, slots, back[0], back[1], ws)
+        starts, seq = torch.tensor([0, 2], dtype=torch.int32, device="cuda"), torch.tensor([40], dtype=torch.int32, device="cuda")
+        api.paged_attention(q, cache, table, starts, seq, out, ws)
+        got.append((back, out))
+    assert api.read_status(ws) == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert ((got[0][0][1].double() - x[1].double()).abs() <= 2.0 ** -4 * x[1].double().abs() + 2.0 ** -10 * x[1].double().abs().amax(-1, keepdim=True) / 224).all()
