@@ -492,9 +492,11 @@ int moe_paged_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_
  * written by the append calls: for the head_dim values x of a token's head the
  * byte is that of the least exponent e >= -127 with max |x| <= 448 * 2^e, and a
  * code is the e4m3 number nearest to x * 2^-e (ties to even; no value is cut
- * off, and a power of two adds no rounding of its own). A head in which some
- * value is not finite gets the byte 255: all its values are NaN. Writing again
- * what was read back gives the same values.
+ * off, and a power of two adds no rounding of its own), but values of which the
+ * nearest is the first one beyond their type (above 61,440 in fp16, above 240 *
+ * 2^120 in bf16) are held as 240 * 2^e. A head in which some value is not finite
+ * gets the byte 255: all its values are NaN. Writing again what was read back, in
+ * the type that it was written in, gives the same values.
  * Codes by strides as in moe_kv_cache, in bytes, multiples of 16. Scales
  * [n_blocks, kv_heads, block_size], contiguous, 16-byte aligned. block_size a
  * multiple of 16, at most 1024; the other limits as in moe_kv_cache. */

@@ -190,6 +190,16 @@ __global__ __launch_bounds__(kThreads, kCtas) void rotate_kernel(const __grid_co
                     most = max(most & 0xffffu, most >> 16);
                     for (int o = 1; o < p.lanes; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
                     const uint32_t top = __float_as_uint(widen<DT>(most).x);
+                    // 240 of the largest power of two: what lies above it is rounded
+                    // down to it, as 256 of them is the first value beyond the type
+                    constexpr uint32_t kLast = DT == 0 ? 0x7f70u : 0x7b80u;
+                    if (most > kLast) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            x[j] = (x[j] & 0x80008000u) | __vminu2(x[j] & 0x7fff7fffu, kLast * 0x10001u);
+                            y[j] = (y[j] & 0x80008000u) | __vminu2(y[j] & 0x7fff7fffu, kLast * 0x10001u);
+                        }
+                    }
                     if (k > 0) {
                         // 448 is 1.75 * 2^8
                         int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);

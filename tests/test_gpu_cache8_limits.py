@@ -1,0 +1,73 @@
+"""The cache of 8-bit values at the ends of its range."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from cache8_util import by_slot, dequantise, make_cache8
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module")
+def api():
+    from moe_decode_gb300 import build
+    build.build()
+    from moe_decode_gb300 import api as a
+    a.set_option(a.OPT_GRID_CTAS, 0)
+    return a
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def next_to_the_largest(dtype, d):
+    """[8, 1, d]: the type's largest value, the tie of codes below it (248 times a
+    power of two), what lies around them, and rows without any of that."""
+    t = torch.finfo(dtype)
+    by = t.max * (1 + t.eps / 2) / 256  # the largest value is just below 256 of these
+    by = 2.0 ** round(math.log2(by))
+    x = torch.randn((8, 1, d), dtype=torch.float64, generator=torch.Generator().manual_seed(3)) * by * 50
+    x[0, 0, 0] = t.max
+    x[1, 0, 1] = -t.max
+    x[2, 0, 2] = 248 * by
+    x[3, 0, 3], x[3, 0, 4] = 248 * by * (1 - t.eps), -240 * by  # one step below the tie
+    x[4, 0, :] = t.max
+    x[5, 0, 5], x[5, 0, 6] = 250 * by, -t.max
+    x[6, 0, 0] = 240 * by
+    return x.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rotated", [False, True])
+def test_values_next_to_the_largest_stay_finite(api, dtype, d, rotated):
+    """Written, read back and written again, as an accepted path is: the same
+    values, each within half a step of its code (2^-4 of it, or of the head's
+    smallest normal code) of what was written."""
+    x = next_to_the_largest(dtype, d)
+    cache, again, ws = make_cache8(api, 1, 16, 1, d), make_cache8(api, 1, 16, 1, d), api.paged_workspace()
+    slots = i32([3, 0, 15, 7, 8, 1, 4, 9])
+    out = torch.zeros((2, 2, *x.shape), dtype=dtype, device="cuda")
+
+    def write(k, v, c):
+        if rotated:  # by no turn at all
+            api.paged_rope_append(None, k, v, i32([0] * 8), slots, api.Rope(d), c, ws)
+        else:
+            api.paged_append(k, v, slots, c, ws)
+
+    write(x, x.flip(2).contiguous(), cache)
+    api.paged_read(cache, slots, out[0, 0], out[0, 1], ws)
+    write(out[0, 0], out[0, 1], again)
+    api.paged_read(again, slots, out[1, 0], out[1, 1], ws)
+    assert api.read_status(ws) == 0
+    assert torch.isfinite(out).all() and torch.equal(out[0], out[1])
+    for a, b in zip(by_slot(cache), by_slot(again)):
+        at = slots.cpu().numpy()
+        assert np.array_equal(dequantise(a[0][at], a[1][at]), dequantise(b[0][at], b[1][at]))
+    for o, want in ((out[0, 0], x), (out[0, 1], x.flip(2))):
+        o, want = o.double(), want.double()
+        assert ((o - want).abs() <= 2.0 ** -4 * want.abs() + 2.0 ** -10 * want.abs().amax(-1, keepdim=True) / 224).all()
