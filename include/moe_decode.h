@@ -532,9 +532,10 @@ int moe_paged_rope_append8(const void* q, int64_t q_token_stride, int64_t q_head
  * moe_paged_tree_attention, or NULL (with masks window is 0). What it says of
  * scale, window, out, lse, padding, pages and bad tables holds here. Codes and
  * powers of two are exact, queries are held in fp16 times a power of two of
- * their row's own (exact down to 2^-28 of the row's largest), keys whose power
- * of two is below 2^-102 (none of them above 2^-93) count as 0, products are
- * summed in fp32, and the softmax weights times the values' powers of two are
+ * their row's own (exact down to 2^-28 of the row's largest; any finite size, by
+ * scales up to 4,096), keys whose power of two is below 2^-102 (none of them above
+ * 2^-93) may count as 0, and next to queries of 2^117 / scale and more those of
+ * 2^97 and more as infinite, products are summed in fp32, and the softmax weights times the values' powers of two are
  * rounded once to fp16, relative to the row's largest such weight. A key whose
  * byte is 255 gives the rows that see it NaN, and may give NaN to the request's
  * rows that do not see it yet. A request of any length is taken 32 rows (tokens

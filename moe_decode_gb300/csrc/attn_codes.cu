@@ -52,7 +52,7 @@ struct CodesShape {
     static constexpr int kOffRow = kOffStat + (kConsumers + 1) * kRows * 8;  // powers of two of the queries
     static constexpr int kOffBar = kOffRow + kRows * 4;
     static constexpr int kOffMisc = kOffBar + 16 * (kStages + 2);
-    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + (int)sizeof(Start) + 16 + 4 * kLoaders;
+    static constexpr int kBytes = kOffMisc + 8 * (kThreads / 32) + (int)sizeof(Start) + 16 + 4 * kLoaders + 4;
     static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -97,11 +97,16 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// A key's power of two from its byte, times 2^-24 (the queries' factors make up
+// A key's power of two from its byte, times 2^-less (the queries' factors make up
 // for it, so that neither the sums of a row's products nor their products with
 // this pass fp32's range); a value's exponent. 255 is NaN.
-__device__ __forceinline__ float key_power(uint32_t byte) {
-    return __uint_as_float(byte == 255u ? 0x7fc00000u : (uint32_t)max((int)byte - 24, 0) << 23);
+constexpr int kLess = 24;
+__device__ __forceinline__ float key_power(uint32_t byte, int less) {
+    return __uint_as_float(byte == 255u ? 0x7fc00000u : (uint32_t)max((int)byte - less, 0) << 23);
+}
+// A row's factor of its scores from its queries' power of two.
+__device__ __forceinline__ float row_factor(const AttnParams& p, int s, int less) {
+    return exp2i(-s) * (p.scale_log2 * exp2i(less));
 }
 __device__ __forceinline__ float value_exponent(uint32_t byte) {
     return byte == 255u ? __uint_as_float(0x7fc00000u) : (float)((int)byte - 127);
@@ -193,6 +198,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
     int& abort_flag = *reinterpret_cast<int*>(found + 1);
     volatile int* join_info = &abort_flag + 1;  // first CTA, parts, whether this one is the last
     volatile int* loaded = join_info + 3;       // the last tile that each loader has issued
+    volatile int* less = loaded + kLoaders;     // key_power's, for the item at hand
     if (tid == 0) {
         abort_flag = 0;
         for (int s = 0; s < S::kStages; ++s) {
@@ -398,10 +404,11 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
             const bool ragged = attn_ragged(walk, key0, kWarpKeys);
             // powers of two of this thread's keys, quad and quad + 8
             const uint8_t* bytes = sm + S::kOffScale + x.stage * 2 * kAttnTile + warp * kWarpKeys + quad;
+            const int item_less = *less;
             float kf[2], ve[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                kf[k] = key_power(bytes[8 * k]);
+                kf[k] = key_power(bytes[8 * k], item_less);
                 ve[k] = value_exponent(bytes[kAttnTile + 8 * k]);
             }
             if (ragged) {
@@ -606,9 +613,17 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
         // row's largest into [2^14, 2^15), four rows a warp. Of 16 dimensions
         // 4i, 4i+1 go to places 2i, 2i+1 and 4i+2, 4i+3 to 8+2i, 9+2i. (Rows past
         // the item's last hold anything; a row's results depend on no other.)
+        // Where a row's queries are so large that its factor passes fp32's range,
+        // the item takes the keys' powers of two as they are: then no factor of
+        // bf16 or fp16 queries does, by scales up to 2^12. (In a register of its
+        // own for the length of the item that choice costs items of 32 rows 4%.)
+        constexpr int kOwn = kRows / kConsumers;
+        float* factors = reinterpret_cast<float*>(sm + S::kOffRow) + warp * kOwn;
+        int shift[kOwn];
+        bool far = false;
 #pragma unroll
-        for (int r = 0; r < kRows / kConsumers; ++r) {
-            const int row = warp * (kRows / kConsumers) + r;
+        for (int r = 0; r < kOwn; ++r) {
+            const int row = warp * kOwn + r;
             if (row >= walk.rows) break;
             constexpr int kWords = D / 64;  // of two dimensions a lane
             uint32_t* words = reinterpret_cast<uint32_t*>(sm + q_off + row * S::kQRow);
@@ -628,7 +643,18 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
                 const int g = lane * kWords + i, in = g & 7;  // pair of dimensions, in its group of 16
                 words[(g & ~7) + (in & 1) * 4 + (in >> 1)] = f32x2_to_f16x2(v[i].x * by, v[i].y * by);
             }
-            if (lane == 0) reinterpret_cast<float*>(sm + S::kOffRow)[row] = fminf(fmaxf(exp2i(-s) * p.scale_log2 * 0x1p24f, 1.2e-38f), 3e38f);
+            shift[r] = s;
+            const float factor = row_factor(p, s, kLess);
+            far |= factor > 3e38f;
+            if (lane == 0) factors[r] = fmaxf(factor, 1e-45f);  // (0 times a score of -inf is not that)
+        }
+        far = warps_any(1, kConsumers * 32, far);
+        if (tid == 0) *less = far ? 0 : kLess;
+        if (far) {
+            if (lane == 0)
+#pragma unroll
+                for (int r = 0; r < kOwn; ++r)
+                    if (warp * kOwn + r < walk.rows) factors[r] = fminf(fmaxf(row_factor(p, shift[r], 0), 1e-45f), 3e38f);
         }
         warps_sync(1, kConsumers * 32);
         if (walk.rows <= 8) item(std::integral_constant<int, 1>{});

@@ -56,6 +56,17 @@ __device__ __forceinline__ void warps_sync(uint32_t id, uint32_t threads) {
     named_bar_sync(id, threads);
 }
 
+// The same, and whether any of their threads says so.
+__device__ __forceinline__ bool warps_any(uint32_t id, uint32_t threads, bool x) {
+    uint32_t any;
+    __syncwarp();
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(id), "r"(threads), "r"((uint32_t)x)
+                 : "memory");
+    return any != 0;
+}
+
 // One thread of a CTA whose part is in place (its threads' stores are behind a
 // barrier): whether all the others are. The last one to come leaves the count
 // at zero for the next call.

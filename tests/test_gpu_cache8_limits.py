@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from cache8_util import by_slot, dequantise, make_cache8
+import paged_util
+from cache8_util import by_slot, check_attention8, dequantise, make_cache8, make_step8
 
 pytestmark = pytest.mark.gpu
 TYPES = [torch.bfloat16, torch.float16]
@@ -71,3 +72,34 @@ def test_values_next_to_the_largest_stay_finite(api, dtype, d, rotated):
     for o, want in ((out[0, 0], x), (out[0, 1], x.flip(2))):
         o, want = o.double(), want.double()
         assert ((o - want).abs() <= 2.0 ** -4 * want.abs() + 2.0 ** -10 * want.abs().amax(-1, keepdim=True) / 224).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_up_to_the_largest(api, d):
+    """One large element of a query against a small one of a key: the scores are
+    some 2^8, the row's factor alone passes fp32's range. Every third row of an
+    item is of usual size."""
+    e = torch.tensor([100, 120, 124, 125, 126, 126, 127, 127], device="cuda")  # by head
+    s = make_step8(api, [(300, 20), (33, 2)], 16, 8, 8, d, torch.bfloat16, 7, spread=(0.5, 0.5))
+    cache, g = s["cache"], torch.Generator(device="cuda").manual_seed(1)
+    y = torch.empty(cache.k.shape, device="cuda").normal_(generator=g) * (64 / d) ** 0.5
+    y[..., 0] = 2.0 ** -9
+    y = y.to(torch.float8_e4m3fn)
+    real = cache.k_scale != 255
+    cache.k.copy_(y.view(torch.uint8))
+    byte = (25 + 127 - e).to(torch.uint8)[None, :, None].expand_as(cache.k_scale)
+    cache.k_scale.copy_(torch.where(real, byte, cache.k_scale))
+    s["k"] = y.double() * torch.exp2((25 - e).double())[None, None, :, None]
+    q = torch.empty(s["q"].shape, dtype=torch.float64, device="cuda").normal_(generator=g) * 2.0 ** -20
+    q[..., 0] = 1.0
+    q *= torch.exp2(e.double())[None, :, None]
+    q[1::3] *= 2.0 ** -60
+    s["q"] = q.bfloat16()
+    ws = api.paged_workspace(8, cache)
+    out, lse = torch.empty_like(s["q"]), torch.empty(s["q"].shape[:2], device="cuda")
+    api.paged_attention(s["q"], cache, s["table"], s["q_start"], s["seq"], out, ws, lse=lse, scale=2.0 ** -8)
+    assert api.read_status(ws) == 0
+    ref = paged_util.attention(s, 2.0 ** -8)
+    check_attention8(out, None, ref, 300)
+    # a score of 2^8 is off by its rounding and its factor's, 2^-24 of it each, and by its products'
+    assert ((lse.double() - ref[1]).abs() <= 2.0 ** -13 + 2.0 ** -20 * ref[1].abs()).all()
