@@ -382,8 +382,10 @@ int moe_paged_append(const void* k_new, int64_t k_token_stride, int64_t k_head_s
  * [0, T] in ascending order (moe_paged_plan with more new tokens than T), is
  * reported alike and its rows are not written.
  * scale <= 0 takes 1 / sqrt(head_dim). block_tables int32 [B, max_blocks].
- * ws: moe_paged_attention_workspace_bytes(q_heads, cache). The result is
- * deterministic. */
+ * ws: moe_paged_attention_workspace_bytes(q_heads, cache). One workspace serves
+ * any of the paged step's calls, one after another (moe_paged_attention8 and
+ * other caches and heads too), if it has the largest of the sizes that they ask
+ * for. The result is deterministic. */
 size_t moe_paged_attention_workspace_bytes(int q_heads, const moe_kv_cache* cache);
 int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int T, int q_heads,
                         const moe_kv_cache* cache, const int32_t* block_tables, int max_blocks,

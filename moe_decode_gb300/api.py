@@ -400,7 +400,8 @@ class KvCache8:
 
 def paged_workspace(q_heads: int = 0, cache: "Optional[KvCache | KvCache8]" = None, device="cuda", stream=None) -> torch.Tensor:
     """A zeroed workspace for the paged-step calls: for paged_attention with
-    q_heads over `cache`, or, without them, for the other calls."""
+    q_heads over `cache`, or, without them, for the other calls. One for the
+    largest serves them all, one call after another."""
     need = lib.moe_paged_attention8_workspace_bytes if isinstance(cache, KvCache8) else lib.moe_paged_attention_workspace_bytes
     n = PAGED_WORKSPACE_BYTES if cache is None else int(need(q_heads, cache._ref))
     _want(n > 0, "moe_paged_attention_workspace_bytes", ESHAPE)

@@ -346,7 +346,7 @@ int moe_paged_read8(const moe_kv_cache8* cache, const int32_t* slot_map, int T, 
 size_t moe_paged_attention8_workspace_bytes(int q_heads, const moe_kv_cache8* cache) {
     if (check_cache8(cache) != MOE_OK) return 0;
     if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads / cache->kv_heads > 32) return 0;
-    return MOE_PAGED_WORKSPACE_BYTES + MOE_MAX_GRID * sizeof(unsigned) +
+    return MOE_PAGED_WORKSPACE_BYTES + 3 * MOE_MAX_GRID * sizeof(unsigned) +
            (size_t)MOE_MAX_GRID * 2 * moe::attn_part_floats(moe::kAttnRows, cache->head_dim) * sizeof(float);
 }
 
@@ -387,7 +387,9 @@ int moe_paged_attention8(const void* q, int64_t q_token_stride, int64_t q_head_s
     p.seq = seq_lens;
     p.ctrl = static_cast<unsigned*>(ws);
     p.arrived = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + MOE_PAGED_WORKSPACE_BYTES);
-    p.part = reinterpret_cast<float*>(p.arrived + MOE_MAX_GRID);
+    // (behind all the counters of the attention over 16 bits, which a workspace that
+    // serves both keeps zero between calls)
+    p.part = reinterpret_cast<float*>(p.arrived + 3 * MOE_MAX_GRID);
     p.q_token = q_token_stride;
     p.q_head = q_head_stride;
     p.T = T;

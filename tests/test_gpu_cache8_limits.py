@@ -1,4 +1,5 @@
-"""The cache of 8-bit values at the ends of its range."""
+"""The cache of 8-bit values at the ends of its range, and one workspace for the
+attentions over both kinds of cache."""
 import math
 
 import numpy as np
@@ -103,3 +104,35 @@ def test_queries_up_to_the_largest(api, d):
     check_attention8(out, None, ref, 300)
     # a score of 2^8 is off by its rounding and its factor's, 2^-24 of it each, and by its products'
     assert ((lse.double() - ref[1]).abs() <= 2.0 ** -13 + 2.0 ** -20 * ref[1].abs()).all()
+
+
+def test_one_workspace_for_both_attentions(api):
+    """Calls over both kinds of cache in turn, of few and of many rows, on a buffer
+    of the larger size, zeroed once: each as on a workspace of its own."""
+    lens = [(3000, 300), (700, 6), (90, 90), (5000, 1), (64, 20)]
+    a = paged_util.make_step(lens, 16, 32, 8, 128, torch.bfloat16, 31)
+    b = make_step8(api, lens, 16, 32, 8, 128, torch.bfloat16, 32)
+    small = make_step8(api, [(1500, 2), (40, 1)], 16, 8, 2, 64, torch.float16, 33)
+    cache = api.KvCache(a["k"], a["v"])
+    runs = [(a, cache), (b, b["cache"]), (small, small["cache"])]
+
+    def call(s, c, ws):
+        out = torch.full_like(s["q"], 3.0)
+        api.paged_attention(s["q"], c, s["table"], s["q_start"], s["seq"], out, ws)
+        assert api.read_status(ws) == 0
+        return out
+
+    want = [call(s, c, api.paged_workspace(s["q"].shape[1], c)) for s, c in runs]
+    sizes = [api.paged_workspace(s["q"].shape[1], c).numel() for s, c in runs]
+    assert max(sizes) == sizes[0]
+    ws = api.paged_workspace(32, cache)
+    for ctas in (0, 7, 152, 0):
+        api.set_option(api.OPT_GRID_CTAS, ctas)
+        try:
+            got = [call(s, c, ws) for _ in range(2) for s, c in runs]
+        finally:
+            api.set_option(api.OPT_GRID_CTAS, 0)
+        if ctas in (0, 152):
+            for g, w in zip(got, want * 2):
+                assert torch.equal(g, w)
+        assert int(ws[api.PAGED_WORKSPACE_BYTES:api.PAGED_WORKSPACE_BYTES + 3 * 4 * 256].count_nonzero()) == 0
