@@ -380,7 +380,9 @@ int moe_paged_append(const void* k_new, int64_t k_token_stride, int64_t k_head_s
  * (MOE_EDEVICE_BAD_INDEX) and that request's outputs are unspecified. A
  * request with a negative length, or whose rows q_start does not place within
  * [0, T] in ascending order (moe_paged_plan with more new tokens than T), is
- * reported alike and its rows are not written.
+ * reported alike and its rows are not written, nor are padding rows where it is
+ * the last one. Rows that q_start gives to two requests, or to one and to the
+ * padding, are unspecified.
  * scale <= 0 takes 1 / sqrt(head_dim). block_tables int32 [B, max_blocks].
  * ws: moe_paged_attention_workspace_bytes(q_heads, cache). One workspace serves
  * any of the paged step's calls, one after another (moe_paged_attention8 and
@@ -406,7 +408,8 @@ int moe_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * bits and consecutive positions, padding rows (from q_start[B] on) 0 and -1.
  * q_start and seq_lens as moe_paged_plan gives them. A parent outside
  * [-1, i) counts as -1 and is reported (MOE_EDEVICE_BAD_INDEX); so is a
- * request that q_start or seq_lens place wrongly, whose rows are not written. */
+ * request that q_start or seq_lens place wrongly, whose rows are not written (nor
+ * padding rows, where q_start places the last one so). */
 #define MOE_TREE_MAX_TOKENS 64
 int moe_tree_plan(const int32_t* parents, const int32_t* q_start, const int32_t* seq_lens, int B, int T, uint64_t* masks,
                   int32_t* positions, void* ws, size_t ws_bytes, void* stream);

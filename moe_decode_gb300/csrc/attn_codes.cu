@@ -215,7 +215,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
     pdl_launch_dependents();
     const Place at = attn_place<All, kThreads>(p, blockIdx.x, scan, found);
     // padding rows
-    for (int64_t i = (int64_t)min(max(p.q_start[p.B], 0), p.T) * p.heads + blockIdx.x + (int64_t)p.G * warp;
+    for (int64_t i = (int64_t)attn_padding(p) * p.heads + blockIdx.x + (int64_t)p.G * warp;
          i < (int64_t)p.T * p.heads; i += (int64_t)p.G * (kThreads / 32)) {
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) reinterpret_cast<uint32_t*>(p.out + i * D)[32 * x + lane] = 0u;

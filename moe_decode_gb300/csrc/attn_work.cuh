@@ -50,6 +50,13 @@ __device__ __forceinline__ Request attn_request(const AttnParams& p, int r) {
     return q;
 }
 
+// The first padding row (p.T: none). None are known where the last request is
+// placed wrongly: its end may lie within another's rows.
+__device__ __forceinline__ int attn_padding(const AttnParams& p) {
+    const int last = p.q_start[p.B - 1], end = p.q_start[p.B];
+    return end < max(last, 0) ? p.T : min(end, p.T);
+}
+
 // The first key that a row at position pos sees. (Without a step past 32 bits,
 // however wide the window and however far below zero the position: an overflow
 // is undefined, and the counts of units of the CTAs' roles then need not agree.)
