@@ -34,6 +34,18 @@ def i32(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
+@pytest.mark.parametrize("q_start,seq,masks,positions", [
+    ([0, 2, -1], [5, 5], [1, 3, 9, 9], [3, 4, 9, 9]), ([0, 3, 2], [5, 5], [1, 3, 4, 9], [2, 3, 2, 9]),
+    ([0, 9, 3], [5, 5], [9, 9, 9, 9], [9, 9, 9, 9]), ([-1, 2, 3], [5, 5], [9, 9, 1, 0], [9, 9, 4, -1]),
+    ([0, 2, 900], [5, 5], [1, 3, 9, 9], [3, 4, 9, 9]), ([0, 2, 3], [-4, 5], [9, 9, 1, 0], [9, 9, 4, -1]),
+    ([0, 1, 3], [5, -1], [1, 9, 9, 0], [4, 9, 9, -1])])
+def test_tree_plan(api, q_start, seq, masks, positions):
+    got, at, ws = torch.full((4,), 9, dtype=torch.int64, device="cuda"), i32([9] * 4), api.paged_workspace()
+    api.tree_plan(i32([-1, 0, -1, 0]), i32(q_start), i32(seq), got, at, ws)
+    assert api.read_status(ws) == api.EDEVICE_BAD_INDEX
+    assert got.tolist() == masks and at.tolist() == positions
+
+
 @pytest.mark.parametrize("q_start,seq,rows,padding", WRONG)
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("codes", [False, True])
