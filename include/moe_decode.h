@@ -434,8 +434,10 @@ int moe_paged_tree_attention(const void* q, int64_t q_token_stride, int64_t q_he
  *   y_second = scale (x_first sin a + x_second cos a)
  * in fp32, rounded once. The other dimensions are copied. Frequencies are held
  * as turns: f_i / (2 pi), its whole part dropped, in units of 2^-64 turns. p
- * times that is exact modulo one turn in 64-bit integers, so the angle is as
- * good at position 2^31 - 1 as at 1. */
+ * times that is exact modulo one turn in 64-bit integers, of which the upper 32
+ * bits are taken. moe_rope_table's turns are off by less than one unit, so the
+ * angle is as good at position 2^31 - 1 as at 1, to 2^-32 turns; moe_rope_turns
+ * is as good as its numbers of 64 bits, 2^-52 of a frequency, times p. */
 typedef struct moe_rope_angles {
     const uint64_t* turns; /* device, [rotary_dim / 2] */
     int32_t rotary_dim;    /* a multiple of 16, at most the head's dimensions */
@@ -457,7 +459,7 @@ typedef struct moe_rope_angles {
 #define MOE_ROPE_YARN 3
 #define MOE_ROPE_BANDS 4
 /* Fills turns (host, [rotary_dim / 2]) and *scale (host) for these settings;
- * computed on the host in 64 bits, once when a model is loaded. base > 1,
+ * computed on the host, once when a model is loaded. base > 1,
  * factor > 0; context >= 1 for YARN and BANDS, with low < high (low <= 0: 1,
  * high <= 0: 32 for YARN, 4 for BANDS). */
 int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int context, double low, double high,

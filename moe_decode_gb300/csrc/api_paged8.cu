@@ -30,14 +30,58 @@ using moe::g_opt;
 using moe::launched;
 using moe::stride_ok;
 
-constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr double kTwoPi = 6.283185307179586476925286766559, kTwoPiLo = 2.4492935982947064e-16;  // and what it lacks
 
-// The part of a turn that a position adds, in 2^-64 of one.
+// The part of a turn that a position adds, in 2^-64 of one. (By a division of 64
+// bits, so that pi in 64 bits is half a turn.)
 uint64_t turns_of(double radians) {
     double t = radians / kTwoPi;
     t -= std::floor(t);
     const double units = std::nearbyint(std::ldexp(t, 64));
     return units >= 18446744073709551616.0 ? 0u : static_cast<uint64_t>(units);
+}
+
+// A number as the sum of two of 64 bits, some 106 bits of it: a table's turns are
+// good to their last unit, 2^-64, and a position multiplies what they are off by.
+// (Sums and products without error by two-sum and by a fused multiply-add.)
+struct Wide {
+    double hi, lo;
+    Wide(double h, double l = 0) : hi(h), lo(l) {}
+};
+Wide sum_of(double a, double b) {
+    const double s = a + b, c = s - a;
+    return Wide(s, (a - (s - c)) + (b - c));
+}
+Wide operator+(Wide a, Wide b) {
+    const Wide s = sum_of(a.hi, b.hi), t = sum_of(a.lo, b.lo), u = sum_of(s.hi, s.lo + t.hi);
+    return sum_of(u.hi, u.lo + t.lo);
+}
+Wide operator-(Wide a) { return Wide(-a.hi, -a.lo); }
+Wide operator*(Wide a, Wide b) {
+    const double p = a.hi * b.hi;
+    return sum_of(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Wide operator/(Wide a, Wide b) {
+    const double q = a.hi / b.hi;
+    return sum_of(q, (a + -(b * q)).hi / b.hi);
+}
+// x with x^n = a (a > 0): one of Newton's steps from 64 bits.
+Wide root_of(Wide a, int n) {
+    const double x = std::pow(a.hi, 1.0 / n);
+    Wide power = 1, square = x;
+    for (int i = n; i > 0; i >>= 1) {
+        if (i & 1) power = power * square;
+        square = square * square;
+    }
+    return sum_of(x, x * ((a + -power) / (power * n)).hi);
+}
+// A frequency over 2 pi, its whole part dropped, in 2^-64.
+uint64_t turns_of(Wide radians) {
+    const Wide t = radians / Wide(kTwoPi, kTwoPiLo);
+    const Wide f = sum_of(t.hi - std::floor(t.hi), t.lo - std::nearbyint(t.lo));  // (between -1 and 2)
+    const double half = std::ldexp(f.hi, 32), whole = std::floor(half);
+    return (static_cast<uint64_t>(static_cast<int64_t>(whole)) << 32) +
+           static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(std::ldexp(half - whole, 32) + std::ldexp(f.lo, 64))));
 }
 
 int check_angles(const moe_rope_angles* a, int head_dim) {
@@ -230,7 +274,8 @@ int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int 
     if (high <= 0) high = scaling == MOE_ROPE_YARN ? 32 : 4;
     if (borders && (context < 1 || !(low < high))) return MOE_EINVAL;
     const int pairs = rotary_dim / 2;
-    if (scaling == MOE_ROPE_NTK) base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+    // (factor^(pairs / (pairs - 1)) is the factor times a root of it)
+    const Wide first_base = scaling == MOE_ROPE_NTK ? Wide(base) * factor * root_of(factor, pairs - 1) : Wide(base);
     // the pair's number at which a frequency makes n turns in the context
     auto pair_of = [&](double n) { return rotary_dim * std::log(context / (n * kTwoPi)) / (2 * std::log(base)); };
     double first = 0, last = 0;
@@ -239,13 +284,16 @@ int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int 
         last = std::fmin(std::ceil(pair_of(low)), rotary_dim - 1);
     }
     *scale = scaling == MOE_ROPE_YARN && factor > 1 ? (float)(0.1 * std::log(factor) + 1) : 1.f;
-    for (int i = 0; i < pairs; ++i) {
-        const double f = std::pow(base, -2.0 * i / rotary_dim);
-        double kept = 1;  // share of the frequency that stays
+    const Wide ratio = Wide(1) / root_of(first_base, pairs);
+    Wide f = 1;
+    for (int i = 0; i < pairs; ++i, f = f * ratio) {
+        Wide kept = 1;  // share of the frequency that stays
         if (scaling == MOE_ROPE_LINEAR) kept = 0;
-        if (scaling == MOE_ROPE_YARN) kept = 1 - std::fmin(std::fmax((i - first) / std::fmax(last - first, 0.001), 0), 1);
-        if (scaling == MOE_ROPE_BANDS) kept = std::fmin(std::fmax((context * f / kTwoPi - low) / (high - low), 0), 1);
-        turns[i] = turns_of(kept == 1 ? f : f / factor * (1 - kept) + f * kept);
+        if (scaling == MOE_ROPE_YARN) kept = Wide(1) + -(Wide(i - first) / std::fmax(last - first, 0.001));
+        if (scaling == MOE_ROPE_BANDS) kept = (f * context / Wide(kTwoPi, kTwoPiLo) + -Wide(low)) / (Wide(high) + -Wide(low));
+        if (kept.hi <= 0) kept = 0;
+        if (kept.hi > 1 || (kept.hi == 1 && kept.lo >= 0)) kept = 1;
+        turns[i] = turns_of(kept.hi == 1 && kept.lo == 0 ? f : f / factor * (Wide(1) + -kept) + f * kept);
     }
     return MOE_OK;
 }
