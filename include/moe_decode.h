@@ -461,7 +461,8 @@ typedef struct moe_rope_angles {
 /* Fills turns (host, [rotary_dim / 2]) and *scale (host) for these settings;
  * computed on the host, once when a model is loaded. base > 1,
  * factor > 0; context >= 1 for YARN and BANDS, with low < high (low <= 0: 1,
- * high <= 0: 32 for YARN, 4 for BANDS). */
+ * high <= 0: 32 for YARN, 4 for BANDS). Settings whose base or frequencies are no
+ * finite numbers of 64 bits are refused (MOE_EINVAL), with nothing written. */
 int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int context, double low, double high,
                    uint64_t* turns, float* scale);
 /* turns [n] (host) of any frequencies [n] in radians a position (host). */

@@ -73,7 +73,8 @@ Wide root_of(Wide a, int n) {
         if (i & 1) power = power * square;
         square = square * square;
     }
-    return sum_of(x, x * ((a + -power) / (power * n)).hi);
+    if (!std::isfinite(power.hi)) return x;  // (next to the largest number of 64 bits)
+    return sum_of(x, x * (((a + -power) / power).hi / n));
 }
 // A frequency over 2 pi, its whole part dropped, in 2^-64.
 uint64_t turns_of(Wide radians) {
@@ -276,6 +277,7 @@ int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int 
     const int pairs = rotary_dim / 2;
     // (factor^(pairs / (pairs - 1)) is the factor times a root of it)
     const Wide first_base = scaling == MOE_ROPE_NTK ? Wide(base) * factor * root_of(factor, pairs - 1) : Wide(base);
+    if (!std::isfinite(first_base.hi) || !(first_base.hi > 0)) return MOE_EINVAL;
     // the pair's number at which a frequency makes n turns in the context
     auto pair_of = [&](double n) { return rotary_dim * std::log(context / (n * kTwoPi)) / (2 * std::log(base)); };
     double first = 0, last = 0;
@@ -283,8 +285,8 @@ int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int 
         first = std::fmax(std::floor(pair_of(high)), 0);
         last = std::fmin(std::ceil(pair_of(low)), rotary_dim - 1);
     }
-    *scale = scaling == MOE_ROPE_YARN && factor > 1 ? (float)(0.1 * std::log(factor) + 1) : 1.f;
     const Wide ratio = Wide(1) / root_of(first_base, pairs);
+    uint64_t own[256];
     Wide f = 1;
     for (int i = 0; i < pairs; ++i, f = f * ratio) {
         Wide kept = 1;  // share of the frequency that stays
@@ -293,8 +295,12 @@ int moe_rope_table(int rotary_dim, double base, int scaling, double factor, int 
         if (scaling == MOE_ROPE_BANDS) kept = (f * context / Wide(kTwoPi, kTwoPiLo) + -Wide(low)) / (Wide(high) + -Wide(low));
         if (kept.hi <= 0) kept = 0;
         if (kept.hi > 1 || (kept.hi == 1 && kept.lo >= 0)) kept = 1;
-        turns[i] = turns_of(kept.hi == 1 && kept.lo == 0 ? f : f / factor * (Wide(1) + -kept) + f * kept);
+        const Wide scaled = kept.hi == 1 && kept.lo == 0 ? f : f / factor * (Wide(1) + -kept) + f * kept;
+        if (!std::isfinite(scaled.hi + scaled.lo)) return MOE_EINVAL;
+        own[i] = turns_of(scaled);
     }
+    std::copy(own, own + pairs, turns);
+    *scale = scaling == MOE_ROPE_YARN && factor > 1 ? (float)(0.1 * std::log(factor) + 1) : 1.f;
     return MOE_OK;
 }
 

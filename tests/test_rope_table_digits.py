@@ -87,3 +87,24 @@ def test_turns_of_frequencies_in_64_bits(api):
         off = (Decimal(t) / 2 ** 64 - want) % 1
         assert min(off, 1 - off) <= abs(want) * Decimal(2) ** -52 + Decimal(2) ** -64
     assert turns[5] == 1 << 63
+
+
+@pytest.mark.parametrize("scaling,base,factor,context", [
+    ("linear", 10000.0, 1e-310, 0), ("yarn", 10000.0, 1e-310, 4096), ("bands", 10000.0, 5e-324, 4096), ("ntk", 10000.0, 5e-324, 0),
+    ("ntk", 1e300, 1e300, 0), ("ntk", 1e-3 + 1, 5e-324, 0)])
+def test_frequencies_that_overflow_are_refused(api, scaling, base, factor, context):
+    turns, scale = (ctypes.c_uint64 * 32)(*([7] * 32)), ctypes.c_float(3.0)
+    assert api.lib.moe_rope_table(64, base, api.ROPE_SCALINGS[scaling], factor, context, 0.0, 0.0, turns, ctypes.byref(scale)) == api.EINVAL
+    assert list(turns) == [7] * 32 and scale.value == 3.0
+
+
+@pytest.mark.parametrize("scaling,base,factor", [("none", 1.7e308, 0.0), ("linear", 1e4, 1e-200), ("ntk", 1e4, 1e-20), ("ntk", 10.0, 1e290),
+                                                 ("ntk", 1e4, 1e-310)])  # (1e-310^(32/31) is above 0, and 1e316^(31/32) finite)
+def test_far_settings_are_taken(api, scaling, base, factor):
+    """The pairs whose frequency is small enough for 64 bits to hold its turns."""
+    turns, scale = (ctypes.c_uint64 * 32)(), ctypes.c_float()
+    assert api.lib.moe_rope_table(64, base, api.ROPE_SCALINGS[scaling], factor, 0, 0.0, 0.0, turns, ctypes.byref(scale)) == api.OK
+    for t, f in zip(turns, frequencies(64, base, scaling, factor, 0, 0, 0)):
+        if f < 2 ** 20:
+            off = (Decimal(t) / 2 ** 64 - f / TWO_PI) % 1
+            assert min(off, 1 - off) <= f * Decimal(2) ** -45 + Decimal(2) ** -63
