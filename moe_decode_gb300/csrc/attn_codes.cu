@@ -118,6 +118,15 @@ __device__ __forceinline__ int piece_at(int key, int c) {
     return D == 128 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
 }
 
+// A row's statistics by the reference at which its sum of weights lies in [1/2, 1):
+// what is scaled to that, sums of weights times values, then lies near the output,
+// and passes fp32's range only where that does. (The reference is rounded, and the
+// sum goes by the reference as it is.)
+__device__ __forceinline__ float2 row_total(float m, float sum) {
+    const float ref = m + (float)((int)(__float_as_uint(sum) >> 23) - 126);
+    return make_float2(ref, sum * exp2_approx(m - ref));
+}
+
 // Joins the parts of an item, in the order of the keys (the part 1 of the CTA
 // that it begins in, then the part 0 of the CTAs after it), all consumers
 // together: the parts' statistics come at once, then the rows, 4 dimensions a
@@ -142,7 +151,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Span& span
         for (int k = tid % 8; k < span.parts; k += 8) sum += stat_of(k).y * exp2_approx(stat_of(k).x - mx);
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (tid % 8 == 0 && tid / 8 < rows) stat[row] = make_float2(mx, sum);
+        if (tid % 8 == 0 && tid / 8 < rows) stat[row] = row_total(mx, sum);
     }
     warps_sync(1, kNum);
     for (int i = tid; i < rows * kPer; i += kNum) {
@@ -560,19 +569,21 @@ __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_co
             float sum = own.y * exp2_approx(own.x - mx);
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if ((tid & 7) == 0) total[tid >> 3] = make_float2(mx, sum);
+            if ((tid & 7) == 0) total[tid >> 3] = row_total(mx, sum);
         }
         warps_sync(1, kConsumers * 32);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                // (nothing was seen: 0 times infinity is not 0)
-                const float f = w[n][r] == kNone ? 1.f : exp2_approx(w[n][r] - total[n * 8 + 2 * pair + r].x);
+                // (half the way at a time: with the smallest and the largest values
+                // the whole is beyond fp32. Nothing was seen: 0 times infinity is
+                // not 0)
+                const float f = w[n][r] == kNone ? 1.f : exp2_approx(0.5f * (w[n][r] - total[n * 8 + 2 * pair + r].x));
 #pragma unroll
                 for (int g = 0; g < D / 16; ++g) {
-                    o[n][g][r] *= f;
-                    o[n][g][2 + r] *= f;
+                    o[n][g][r] = o[n][g][r] * f * f;
+                    o[n][g][2 + r] = o[n][g][2 + r] * f * f;
                 }
             }
 #pragma unroll 1

@@ -75,6 +75,24 @@ def test_values_next_to_the_largest_stay_finite(api, dtype, d, rotated):
         assert ((o - want).abs() <= 2.0 ** -4 * want.abs() + 2.0 ** -10 * want.abs().amax(-1, keepdim=True) / 224).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_over_the_largest_values_is_finite(api, dtype):
+    """A row that sees one token has that token's values."""
+    x = next_to_the_largest(dtype, 64)
+    cache, ws = make_cache8(api, 8, 16, 1, 64), api.paged_workspace(1, make_cache8(api, 8, 16, 1, 64))
+    slots = i32([16 * i for i in range(8)])
+    api.paged_append(torch.zeros_like(x), x, slots, cache, ws)
+    back, out = torch.empty((2, *x.shape), dtype=dtype, device="cuda"), torch.empty_like(x)
+    api.paged_read(cache, slots, back[0], back[1], ws)
+    q = torch.randn((8, 1, 64), device="cuda").to(dtype)
+    api.paged_attention(q, cache, i32([[i] for i in range(8)]), i32(list(range(9))), i32([1] * 8), out, ws)
+    assert api.read_status(ws) == 0 and torch.isfinite(out).all()
+    want = back[1].double()
+    # the weight is 2^11, by its reference's rounding (2^-20 for scores below 16) and that of four powers (2^-22 each) off from the sum's; then
+    # the output's own
+    assert ((out.double() - want).abs() <= (torch.finfo(dtype).eps / 2 + 2.0 ** -18) * want.abs()).all()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_queries_up_to_the_largest(api, d):
     """One large element of a query against a small one of a key: the scores are
@@ -104,6 +122,24 @@ def test_queries_up_to_the_largest(api, d):
     check_attention8(out, None, ref, 300)
     # a score of 2^8 is off by its rounding and its factor's, 2^-24 of it each, and by its products'
     assert ((lse.double() - ref[1]).abs() <= 2.0 ** -13 + 2.0 ** -20 * ref[1].abs()).all()
+
+
+@pytest.mark.parametrize("dtype,by", [(torch.bfloat16, (119, 110, 60, -60, -112, -117)), (torch.float16, (13, 12, 0, -4, -9, -14))])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_up_to_the_largest(api, dtype, by, d):
+    """Heads of values from the type's largest to its smallest, over many keys:
+    sums of weights times values pass fp32's range where the outputs do not."""
+    lens = [(3000, 20), (20000, 1), (5, 5)]
+    s = make_step8(api, lens, 16, 12, 6, d, dtype, 6, spread=(0.3, 0.0))
+    e = torch.tensor(by, device="cuda")
+    real = s["cache"].v_scale != 255
+    s["cache"].v_scale.copy_(torch.where(real, (s["cache"].v_scale.int() + e.int()[None, :, None]).to(torch.uint8), s["cache"].v_scale))
+    s["v"] = s["v"] * torch.exp2(e.double())[None, None, :, None]
+    ws = api.paged_workspace(12, s["cache"])
+    out, lse = torch.empty_like(s["q"]), torch.empty(s["q"].shape[:2], device="cuda")
+    api.paged_attention(s["q"], s["cache"], s["table"], s["q_start"], s["seq"], out, ws, lse=lse)
+    assert api.read_status(ws) == 0
+    check_attention8(out, lse, paged_util.attention(s), 20000)
 
 
 def test_one_workspace_for_both_attentions(api):
