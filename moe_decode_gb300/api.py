@@ -298,6 +298,15 @@ def _want(ok: bool, what: str, code: int = EINVAL):
         raise MoeError(code, what)
 
 
+_INT32 = 1 << 31
+
+
+def _int32(what: str, n: int):
+    """A whole number that the library takes in 32 bits (ctypes drops what is above)."""
+    if not -_INT32 <= n < _INT32:
+        raise MoeError(ESHAPE, f"{what} beyond 32 bits")
+
+
 def _raw(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -418,6 +427,7 @@ def paged_plan(ctx_lens, new_lens, free_list, block_tables, block_size: int, q_s
     positions [T], taken [1]; free_head [1] is where the free list begins."""
     B, T = ctx_lens.numel(), slot_map.numel()
     _want(block_tables.dim() == 2 and block_tables.shape[0] == B, "paged_plan: block_tables int32 [B, W]")
+    _int32("paged_plan: block_size", block_size)
     dev = _device("paged_plan", ctx_lens)
     _vectors("paged_plan", dev, torch.int32, (ctx_lens, B), (new_lens, B), (free_list, None), (free_head, 1),
              (block_tables, None), (q_start, B + 1), (seq_lens, B), (slot_map, T), (positions, T), (taken, 1))
@@ -518,6 +528,8 @@ class Rope:
                  factor: float = 1.0, context: int = 0, low: float = 0.0, high: float = 0.0, scale: Optional[float] = None,
                  device="cuda"):
         _want(scaling in ROPE_SCALINGS, f"Rope: scaling one of {', '.join(ROPE_SCALINGS)}")
+        _want(0 < rotary_dim <= 512, "Rope: rotary_dim", ESHAPE)
+        _int32("Rope: context", context)
         turns = (ctypes.c_uint64 * max(1, rotary_dim // 2))()
         own = ctypes.c_float(1.0)
         _check(lib.moe_rope_table(rotary_dim, base, ROPE_SCALINGS[scaling], factor, context, low, high, turns,
@@ -643,6 +655,7 @@ def paged_attention(q, cache, block_tables, q_start, seq_lens, out, ws, lse=None
     _vectors("paged_attention: lse", dev, torch.float32, (lse, T * heads))
     _vectors("paged_attention: tree_masks", dev, torch.int64, (tree_masks, T))
     _want(tree_masks is None or window == 0, "paged_attention: tree_masks and a window", ESHAPE)
+    _int32("paged_attention: window", window)
     _workspace("paged_attention", dev, ws)
     qt, qh, _ = q.stride()
     if T == 1:
