@@ -1,6 +1,8 @@
 // Rotary positions (moe_rope), alone or in one pass with the write of keys and
 // values into a paged cache of 16-bit values or of e4m3 codes, and the reading
 // back of slots (moe_paged_rope_append and its kin, moe_paged_read).
+#include <algorithm>
+
 #include "layer_params.h"
 #include "paged.h"
 #include "ptx.cuh"
@@ -300,9 +302,8 @@ cudaError_t launch_pdl(void (*kern)(P), int grid, const P& p, cudaStream_t strea
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Few tokens are shared by as many warps as have a round each, many by two or
-// three: `warps` of an SM are wanted. (8,192 tokens into e4m3 codes: 40.3 us with
-// 16, 38.0 with 160; with 400, where each computes the angles, half as much again.)
+// The warps that share a token: `warps` of an SM are wanted, each with a round at
+// the least.
 int split_of(int T, int rounds, int sms, int warps) {
     const int64_t want = ((int64_t)sms * warps + T - 1) / T;
     return (int)(want > rounds ? rounds : want);
@@ -318,7 +319,13 @@ cudaError_t launch_rotate(RotateParams p, int to, int dtype, int sms, cudaStream
     p.lanes = p.head_dim / 16;
     p.per = 32 / p.lanes;
     const int heads = p.heads[0] + p.heads[1] + p.heads[2], rounds = (heads + p.per - 1) / p.per;
-    p.split = split_of(p.T, rounds, sms, 160);
+    // Each warp of a token computes the token's angles. Enough of them to have 16 an
+    // SM, and while there are tokens for fewer than 160, as many as leave each four
+    // rounds. (us by 16, by 160, by this: 32/8 heads of 128 into codes, 1,024 tokens
+    // 8.9, 11.6, 8.9, 2,048 14.5, 20.3, 16.5, 4,096 24.3, 24.7, 23.8, 8,192 42.2, 39.7,
+    // 39.7, 20,000 91.7, 85.0, 84.9; 8/2 heads, 8,192 tokens 16.0, 20.6, 16.1; 64/8
+    // heads, 1,024 tokens 14.4, 17.5, 14.7, 8,192 65.8, 61.8, 61.8.)
+    p.split = std::max(split_of(p.T, rounds, sms, 16), std::min(split_of(p.T, rounds, sms, 160), (rounds + 3) / 4));
     const int grid = grid_of((int64_t)p.T * p.split, (int64_t)sms * 8);
     if (dtype == 0) {
         if (to == kRotateRows) return launch_pdl(rotate_kernel<0, kRotateRows>, grid, p, stream);
