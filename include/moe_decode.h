@@ -549,7 +549,7 @@ int moe_paged_rope_append8(const void* q, int64_t q_token_stride, int64_t q_head
  * rows that do not see it yet. A request of any length is taken 32 rows (tokens
  * times the heads that share a kv head) at a time: beyond some 256 rows it is
  * faster to read its context back (moe_paged_read8) into a 16-bit cache for
- * moe_paged_attention. ws: moe_paged_attention8_workspace_bytes. */
+ * moe_paged_attention. An output beyond its type's largest value is infinite. ws: moe_paged_attention8_workspace_bytes. */
 size_t moe_paged_attention8_workspace_bytes(int q_heads, const moe_kv_cache8* cache);
 int moe_paged_attention8(const void* q, int64_t q_token_stride, int64_t q_head_stride, int T, int q_heads, int dtype,
                          const moe_kv_cache8* cache, const int32_t* block_tables, int max_blocks, const int32_t* q_start,

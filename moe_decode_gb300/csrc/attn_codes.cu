@@ -184,11 +184,12 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Span& span
 // (160 KB on their way), a fourth brings the next item's queries.
 //
 // 4 streams of 120,000 to 131,000 keys (64/8 heads of 128, 8 rows an item) take
-// 174 to 194 us replayed from a graph, 5.3 to 5.9 TB/s; the 16-bit cache takes
-// 301. 32 streams of 6 new tokens over 300 to 16,000 keys (24 rows, pages of 16)
-// take 142 us (170), bound by fetching and issuing the instructions of two warps
-// a scheduler: 2,150 cycles a tile, where HBM would take 1,470 and the matrix
-// unit is busy for 770. One token over 1,001 keys takes 12.3 us: latency.
+// 174 to 198 us replayed from a graph, 5.2 to 5.9 TB/s; the 16-bit cache takes
+// 310. 32 streams of 6 new tokens over 300 to 16,000 keys (24 rows, pages of 16)
+// take 142 us (174), of 8 tokens (32 rows) 182 (176), bound by fetching and
+// issuing the instructions of two warps a scheduler: 2,150 cycles a tile of 24
+// rows, where HBM would take 1,470 and the matrix unit is busy for 770. One token
+// over 1,001 keys takes 12.3 us (11.6): latency.
 template <int D, int DT, bool TREE>
 __global__ __launch_bounds__(kThreads, 1) void attn_codes_kernel(const __grid_constant__ AttnParams p,
                                                                   const __grid_constant__ CUtensorMap kmap,
